@@ -3,7 +3,7 @@
 Between two layers the layer's output joins the residual stream, which is
 normalised into the next layer's tokens (moe_add_rmsnorm); after the last one
 an 8-bit block-scaled product gives the logits, or another dense projection
-(moe_linear_f8); from the logits a token is drawn per row, for a decode batch
+(moe_scaled_linear); from the logits a token is drawn per row, for a decode batch
 (moe_sample) or for a verify pass (moe_verify_sample).
 
 ``own`` False: the operators in elementary torch operations; True: the
@@ -160,7 +160,7 @@ def prepare(case, seed):
         s["ws"] = None
         if own:
             import routed_expert_ffn_gemv_amd as moe
-            n = moe.moe_linear_f8_workspace_size(T, N, K)
+            n = moe.moe_scaled_linear_workspace_size(T, N, K)
             s["ws"] = torch.empty(max(n, 256), dtype=torch.uint8, device=dev)
     else:
         V = case["V"]
@@ -208,7 +208,7 @@ def _own_norm(moe, s):
 
 def _own_linear(moe, s):
     c = s["case"]
-    moe.moe_linear_f8(s["x8"], s["x8_scale"], c["T"], s["w8"], s["w8_scale"], c["N"], c["K"], s["out"], s["ws"])
+    moe.moe_scaled_linear(s["x8"], s["x8_scale"], c["T"], s["w8"], s["w8_scale"], c["N"], c["K"], s["out"], s["ws"])
     return s["out"]
 
 
