@@ -370,6 +370,33 @@ moe_status moe_verify_accept(const float* logits, int32_t T, int32_t V, const in
                              int32_t* out_tokens, int32_t* n_out, void* ws, size_t ws_bytes,
                              void* stream);
 
+/* Residual addition and RMS norm between two layers ([MD] "問題": the 48
+ * layers run one after the other; the pages give no formula for what joins
+ * them, this is the usual pre-norm residual stream).  For each of T rows of H
+ * columns:
+ *   v = resid + y in fp32, rounded to resid's format (y NULL: v = resid)
+ *   n = v * (1 / sqrt(mean(v^2) + eps)) * weight   in fp32; the mean square
+ *       is summed in 64 bits
+ *   resid_out = v         (may be NULL; may be resid itself: in place)
+ *   x = bf16(n)           (may be NULL): the x of the next moe_layer
+ *   x8, x8_scale          (may be NULL, both or neither): n in 8 bits for
+ *       moe_scaled_linear.  Per row and block b of 128 columns (the last one
+ *       may be shorter): x8_scale = max(amax |n|, 448 * 2^-126) / 448 and
+ *       x8 = e4m3(n / x8_scale), rounded to the nearest, ties to even.
+ * At least one of x, x8 and resid_out is not NULL.  y, resid (and resid_out,
+ * which has resid's format) and weight are MOE_W_F32 or MOE_W_BF16; y is what
+ * moe_layer or moe_prefill_layer wrote, for example.  Strides are in elements
+ * from row to row, at least H; x8 [T][H] and x8_scale [T][ceil(H / 128)] are contiguous.  No
+ * output overlaps an input, except resid_out equal to resid with the same
+ * stride.  Pointers need their element's alignment only (x8 none); rows whose
+ * pointers, strides and H allow 16-byte accesses are read that way.  Limits:
+ * H <= 32768, T <= 2^22.  Results do not depend on T or on the run. */
+moe_status moe_add_rmsnorm(int32_t T, int32_t H, const void* y, int32_t y_fmt, int64_t y_stride,
+                           const void* resid, int32_t resid_fmt, int64_t resid_stride,
+                           const void* weight, int32_t weight_fmt, float eps, void* resid_out,
+                           int64_t resid_out_stride, uint16_t* x, int64_t x_stride, uint8_t* x8,
+                           float* x8_scale, void* stream);
+
 /* Host tier: the listed misses computed on the CPU ([MD] "1 トークン、三者の
  *分担": experts that are not on the card are computed by the CPU next to the
  * RAM that holds them, and the results are summed with the card's).

@@ -28,7 +28,7 @@ EXPORTS = ("moe_status_string", "moe_version", "moe_workspace_size", "moe_route"
            "moe_host_isa", "moe_verify_workspace_size", "moe_verify_accept",
            "moe_prefill_workspace_size", "moe_prefill_layer", "moe_layer_check",
            "moe_set_wait_budget", "moe_set_trace", "moe_layer_noalloc",
-           "moe_expert_ffn_accum", "moe_set_deterministic")
+           "moe_expert_ffn_accum", "moe_set_deterministic", "moe_add_rmsnorm")
 MOE_REFRESH_MAX_SWAPS = 1024
 
 
@@ -117,6 +117,10 @@ def _load():
     lib.moe_verify_workspace_size.argtypes = [I32, I32, ctypes.POINTER(SZ)]
     lib.moe_verify_accept.restype = I32
     lib.moe_verify_accept.argtypes = [P, I32, I32, P, P, P, P, SZ, P]
+    F32, I64 = ctypes.c_float, ctypes.c_int64
+    lib.moe_add_rmsnorm.restype = I32
+    lib.moe_add_rmsnorm.argtypes = [I32, I32, P, I32, I64, P, I32, I64, P, I32, F32, P, I64, P, I64,
+                                    P, P, P]
     lib.moe_host_isa.restype = I32
     lib.moe_host_isa.argtypes = []
     lib.moe_host_miss_ffn.restype = I32
@@ -346,6 +350,92 @@ def moe_verify_accept(logits, T, V, draft, out_tokens, n_out, ws, stream=None):
     _check(lib.moe_verify_accept(_ptr(logits), int(T), int(V), _ptr(draft), _ptr(out_tokens),
                                  _ptr(n_out), _ptr(ws), ws.numel() if ws is not None else 0,
                                  _stream(stream)), "moe_verify_accept")
+
+
+# ---- The calls around the layer.  They take their formats and strides from
+# the tensors and check these on the host (ValueError) before the library
+# checks the rest (MoEError).
+
+def _formats():
+    import torch
+    bf16 = dict.fromkeys((torch.bfloat16, torch.int16, torch.uint16), MOE_W_BF16)
+    return {torch.float32: MOE_W_F32, **bf16}, (torch.uint8, torch.float8_e4m3fn), (torch.float32,)
+
+
+_FMT_OF, _CODES, _F32 = _formats()
+_BF16 = tuple(t for t, f in _FMT_OF.items() if f == MOE_W_BF16)
+
+
+def _fmt_of(t, what):
+    f = _FMT_OF.get(t.dtype)
+    if f is None:
+        raise ValueError(f"{what}: fp32 or bf16 (or bf16 bits as 16-bit integers) wanted, got {t.dtype}")
+    return f
+
+
+def _rows(t, T, n, what):
+    """Stride of a [>= T][>= n] tensor whose rows are contiguous."""
+    shape = t.shape
+    if len(shape) != 2 or shape[0] < T or shape[1] < n:
+        raise ValueError(f"{what}: [{T}][{n}] wanted, got {list(shape)}")
+    row, col = t.stride()
+    if col != 1 and n > 1:
+        raise ValueError(f"{what}: the elements of a row must be consecutive")
+    return row if T > 1 else max(row, n)
+
+
+def _flat(t, n, what, dtypes):
+    if t.dtype not in dtypes:
+        raise ValueError(f"{what}: {' or '.join(map(str, dtypes))} wanted, got {t.dtype}")
+    if t.numel() < n or not t.is_contiguous():
+        raise ValueError(f"{what}: {n} contiguous elements wanted, got {list(t.shape)}")
+
+
+def _on_device(call, what, stream, *tensors):
+    """call(stream handle) on the device that holds every one of the tensors
+    (None: left out); stream None: that device's current stream."""
+    import torch
+    dev = -1
+    for t in tensors:
+        if t is not None:
+            d = t.get_device()
+            if d < 0 or (dev >= 0 and d != dev):
+                raise ValueError(f"{what}: every tensor must be on one GPU")
+            dev = d
+    if dev == torch.cuda.current_device():
+        return _check(call(_stream(stream)), what)
+    with torch.cuda.device(dev):
+        return _check(call(_stream(stream)), what)
+
+
+def moe_add_rmsnorm(T, H, y, resid, weight, eps, resid_out=None, x=None, x8=None, x8_scale=None,
+                    stream=None):
+    """v = resid + y (y None: resid), into resid_out (may be resid); its RMS
+    norm times weight into x (bf16 [T][H]) and/or x8 (e4m3 codes [T][H],
+    uint8 or float8_e4m3fn) with x8_scale (fp32 [T][ceil(H/128)]).  y, resid
+    and weight: fp32 or bf16, rows may be strided."""
+    T, H = int(T), int(H)
+    y_fmt = y_row = out_row = x_row = 0
+    r_fmt, r_row = _fmt_of(resid, "resid"), _rows(resid, T, H, "resid")
+    if y is not None:
+        y_fmt, y_row = _fmt_of(y, "y"), _rows(y, T, H, "y")
+    if resid_out is not None:
+        if _fmt_of(resid_out, "resid_out") != r_fmt:
+            raise ValueError("resid_out: resid's format wanted")
+        out_row = _rows(resid_out, T, H, "resid_out")
+    if x is not None:
+        if x.dtype not in _BF16:
+            raise ValueError(f"x: bf16 wanted, got {x.dtype}")
+        x_row = _rows(x, T, H, "x")
+    if x8 is not None:
+        _flat(x8, T * H, "x8", _CODES)
+    if x8_scale is not None:
+        _flat(x8_scale, T * ((H + 127) // 128), "x8_scale", _F32)
+    _flat(weight, H, "weight", _FMT_OF)
+    _on_device(lambda st: lib.moe_add_rmsnorm(
+        T, H, _ptr(y), y_fmt, y_row, resid.data_ptr(), r_fmt, r_row, weight.data_ptr(),
+        _FMT_OF[weight.dtype], eps, _ptr(resid_out), out_row, _ptr(x), x_row, _ptr(x8),
+        _ptr(x8_scale), st), "moe_add_rmsnorm", stream, resid, y, weight, resid_out, x, x8, x8_scale)
 
 
 def _hptr(a, dtype):

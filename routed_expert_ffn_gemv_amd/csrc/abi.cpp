@@ -22,6 +22,7 @@ constexpr int kMaxSlots = 16384;
 constexpr int kMaxVerifyT = 64;        // rows of one verify pass
 constexpr int kMaxVocab = 1 << 26;
 constexpr int64_t kMaxT = int64_t(1) << 22;
+constexpr int kMaxNormH = 32768;
 constexpr size_t kAlign = 256;
 constexpr int kRouterGemmMinT = 256;       // tokens from which the router runs on MFMA
 constexpr int64_t kFfnGemmMinPairs = 2048; // pairs from which the FFN runs as grouped GEMMs
@@ -290,6 +291,10 @@ PrefillEvents* prefill_events() {
   return &e;
 }
 
+// Floating formats of the calls around the layer (activations, logits).
+bool act_fmt(int32_t fmt) { return fmt == MOE_W_F32 || fmt == MOE_W_BF16; }
+bool act_aligned(const void* p, int32_t fmt) { return aligned(p, fmt == MOE_W_F32 ? 4 : 2); }
+
 // Whether moe_layer takes the fused launch for this layer and T.
 bool fused_shape(const moe_layer_desc* d, int T) {
   const int fmt = d->gate.fmt;
@@ -357,7 +362,7 @@ const char* moe_status_string(int32_t s) {
   }
 }
 
-int32_t moe_version(void) { return 101; }
+int32_t moe_version(void) { return 102; }
 
 moe_status moe_workspace_size(const moe_layer_desc* desc, int32_t T, size_t* bytes) {
   const moe_status s = check_desc(desc);
@@ -665,6 +670,47 @@ moe_status moe_verify_accept(const float* logits, int32_t T, int32_t V, const in
   if (ws_bytes < need) return MOE_ERR_WORKSPACE;
   return device_status(launch_verify_accept(logits, T, V, T > 1 ? draft : out_tokens, out_tokens,
                                             n_out, ws, static_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_add_rmsnorm(int32_t T, int32_t H, const void* y, int32_t y_fmt, int64_t y_stride,
+                           const void* resid, int32_t resid_fmt, int64_t resid_stride,
+                           const void* weight, int32_t weight_fmt, float eps, void* resid_out,
+                           int64_t resid_out_stride, uint16_t* x, int64_t x_stride, uint8_t* x8,
+                           float* x8_scale, void* stream) {
+  if (T < 0 || H < 1) return MOE_ERR_INVALID;
+  if (T > kMaxT || H > kMaxNormH) return MOE_ERR_UNSUPPORTED;
+  if (!act_fmt(resid_fmt) || !act_fmt(weight_fmt) || (y && !act_fmt(y_fmt)))
+    return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (!resid || !weight || (!x && !x8 && !resid_out) || !x8 != !x8_scale) return MOE_ERR_INVALID;
+  if (!act_aligned(resid, resid_fmt) || !act_aligned(weight, weight_fmt) ||
+      (y && !act_aligned(y, y_fmt)) || !act_aligned(resid_out, resid_fmt) || !aligned(x, 2) ||
+      !aligned(x8_scale, 4))
+    return MOE_ERR_INVALID;
+  if (resid_stride < H || (y && y_stride < H) || (resid_out && resid_out_stride < H) ||
+      (x && x_stride < H) || (resid_out == resid && resid_out_stride != resid_stride))
+    return MOE_ERR_INVALID;
+  if (!(eps >= 0.0f)) return MOE_ERR_INVALID;
+  NormArgs a;
+  memset(&a, 0, sizeof(a));
+  a.T = T;
+  a.H = H;
+  a.y = y;
+  a.y_fmt = y_fmt;
+  a.y_stride = y ? y_stride : 0;
+  a.resid = resid;
+  a.resid_fmt = resid_fmt;
+  a.resid_stride = resid_stride;
+  a.weight = weight;
+  a.weight_fmt = weight_fmt;
+  a.eps = eps;
+  a.resid_out = resid_out;
+  a.resid_out_stride = resid_out ? resid_out_stride : 0;
+  a.x = x;
+  a.x_stride = x ? x_stride : 0;
+  a.x8 = x8;
+  a.x8_scale = x8_scale;
+  return device_status(launch_add_rmsnorm(a, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

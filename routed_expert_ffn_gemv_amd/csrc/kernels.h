@@ -99,4 +99,25 @@ hipError_t launch_combine(int T, int k, int H, const int32_t* slot_idx, const fl
                           const float* pair_out, const float* shared_out, float* y,
                           hipStream_t st);
 
+// residual addition and RMS norm between two layers
+struct NormArgs {
+  int T, H;
+  const void* y;          // [T] rows, or null
+  int y_fmt;
+  int64_t y_stride;       // elements from row to row, as all strides here
+  const void* resid;
+  int resid_fmt;
+  int64_t resid_stride;
+  const void* weight;     // [H]
+  int weight_fmt;
+  float eps;
+  void* resid_out;        // in resid's format (may be null or resid)
+  int64_t resid_out_stride;
+  uint16_t* x;            // bf16 (may be null)
+  int64_t x_stride;
+  uint8_t* x8;            // e4m3 [T][H] (may be null)
+  float* x8_scale;        // [T][ceil(H / 128)]
+};
+hipError_t launch_add_rmsnorm(const NormArgs& a, hipStream_t st);
+
 }  // namespace moe
