@@ -397,6 +397,54 @@ moe_status moe_add_rmsnorm(int32_t T, int32_t H, const void* y, int32_t y_fmt, i
                            int64_t resid_out_stride, uint16_t* x, int64_t x_stride, uint8_t* x8,
                            float* x8_scale, void* stream);
 
+/* Sampling: one token per row of logits ([MD] "予測してから検証する" describes
+ * greedy drafts and acceptance; the pages name no sampler: the rule below is
+ * this library's).  logits: T rows of V entries, MOE_W_F32 or MOE_W_BF16,
+ * stride elements from row to row (>= V).  Per row:
+ *  - -infinity (and NaN) marks a token that cannot be drawn; a row without any
+ *    other gives token -1 and probability 0.
+ *  - Order: logit descending, the lower index first on equal logits (-0.0
+ *    equals +0.0).  w = exp((logit - largest) / temperature).
+ *  - min_p: the tokens with w >= min_p stay.  Of these top_k: the first
+ *    top_k.  Of these top_p: the shortest run from the front whose sum
+ *    reaches top_p times the sum of all.  The first token always stays.
+ *  - u in [0, 1): the token is the first at which the running sum of the
+ *    kept w exceeds u times their sum (u >= 1: the last kept one, u < 0 or
+ *    NaN: the first).  prob [T] fp32 (may be NULL): its w over that sum.
+ *  - temperature <= 0 or NaN: the first token, with probability 1 (what
+ *    moe_verify_accept takes).
+ * temperature, top_k, top_p, min_p: device arrays [T], each may be NULL: 1, 0,
+ * 1, 0.  top_k <= 0, top_p >= 1 (or NaN) and min_p <= 0 (or NaN) filter
+ * nothing; infinite temperatures make every token that is left equal; equal
+ * +infinity logits share the draw.  w is computed in 64 bits and held to
+ * 2^-s, s = min(52, 61 - ceil(log2 V)); weights that round to zero are not
+ * drawn.  Sums are exact: results do not depend on T, on the other rows or on
+ * the run.  tokens [T] int32.  Limits: 1 <= V <= 2^26, T <= 16384.  ws:
+ * moe_sample_workspace_size bytes, 256-byte aligned, in use by one call at a
+ * time. */
+typedef struct {
+  const float* temperature;
+  const int32_t* top_k;
+  const float* top_p;
+  const float* min_p;
+} moe_sample_params;
+
+moe_status moe_sample_workspace_size(int32_t T, int32_t V, size_t* bytes);
+moe_status moe_sample(const void* logits, int32_t fmt, int32_t T, int32_t V, int64_t stride,
+                      const moe_sample_params* params, const float* u, int32_t* tokens,
+                      float* prob, void* ws, size_t ws_bytes, void* stream);
+
+/* Acceptance of a verify pass whose tokens are sampled: moe_sample on the T
+ * rows, then the rule of moe_verify_accept with row i's sampled token in
+ * g_i's place.  The drafts are fixed before the pass, so keeping a draft
+ * exactly when the row draws it leaves the distribution of the output that
+ * of sampling token after token.  out_tokens [T]: every row's token; *n_out =
+ * kept drafts + 1.  1 <= T <= 64; draft [T-1] may be NULL when T = 1. */
+moe_status moe_verify_sample(const void* logits, int32_t fmt, int32_t T, int32_t V, int64_t stride,
+                             const moe_sample_params* params, const float* u,
+                             const int32_t* draft, int32_t* out_tokens, float* prob,
+                             int32_t* n_out, void* ws, size_t ws_bytes, void* stream);
+
 /* Host tier: the listed misses computed on the CPU ([MD] "1 トークン、三者の
  *分担": experts that are not on the card are computed by the CPU next to the
  * RAM that holds them, and the results are summed with the card's).

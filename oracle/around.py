@@ -64,13 +64,14 @@ def sample_row(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
         w = np.where(x == top, 1.0, np.exp(np.where(x == -np.inf, -np.inf, (x - top) / temperature)))
     w = np.where(x == -np.inf, 0.0, w)
     w = w[order]
-    keep = (x[order] > -np.inf) & (w >= min_p)
+    keep = (x[order] > -np.inf) & ~(w < min_p)
     keep[0] = True
     w = w[keep]
     order = order[keep]
     if top_k > 0:
         w, order = w[:top_k], order[:top_k]
     slack = 1.0
+    u = 0.0 if not u > 0 else min(u, 1.0)
     if top_p < 1:
         cum = np.cumsum(w)
         n = int((cum < top_p * cum[-1]).sum()) + 1

@@ -28,7 +28,8 @@ EXPORTS = ("moe_status_string", "moe_version", "moe_workspace_size", "moe_route"
            "moe_host_isa", "moe_verify_workspace_size", "moe_verify_accept",
            "moe_prefill_workspace_size", "moe_prefill_layer", "moe_layer_check",
            "moe_set_wait_budget", "moe_set_trace", "moe_layer_noalloc",
-           "moe_expert_ffn_accum", "moe_set_deterministic", "moe_add_rmsnorm")
+           "moe_expert_ffn_accum", "moe_set_deterministic", "moe_add_rmsnorm",
+           "moe_sample_workspace_size", "moe_sample", "moe_verify_sample")
 MOE_REFRESH_MAX_SWAPS = 1024
 
 
@@ -64,6 +65,11 @@ class moe_slot_pool(ctypes.Structure):
 
 class moe_miss(ctypes.Structure):
     _fields_ = [("expert", ctypes.c_int32), ("token", ctypes.c_int32), ("gate", ctypes.c_float)]
+
+
+class moe_sample_params(ctypes.Structure):
+    _fields_ = [("temperature", ctypes.c_void_p), ("top_k", ctypes.c_void_p),
+                ("top_p", ctypes.c_void_p), ("min_p", ctypes.c_void_p)]
 
 
 def _load():
@@ -121,6 +127,13 @@ def _load():
     lib.moe_add_rmsnorm.restype = I32
     lib.moe_add_rmsnorm.argtypes = [I32, I32, P, I32, I64, P, I32, I64, P, I32, F32, P, I64, P, I64,
                                     P, P, P]
+    SA = ctypes.POINTER(moe_sample_params)
+    lib.moe_sample_workspace_size.restype = I32
+    lib.moe_sample_workspace_size.argtypes = [I32, I32, ctypes.POINTER(SZ)]
+    lib.moe_sample.restype = I32
+    lib.moe_sample.argtypes = [P, I32, I32, I32, I64, SA, P, P, P, P, SZ, P]
+    lib.moe_verify_sample.restype = I32
+    lib.moe_verify_sample.argtypes = [P, I32, I32, I32, I64, SA, P, P, P, P, P, P, SZ, P]
     lib.moe_host_isa.restype = I32
     lib.moe_host_isa.argtypes = []
     lib.moe_host_miss_ffn.restype = I32
@@ -359,10 +372,11 @@ def moe_verify_accept(logits, T, V, draft, out_tokens, n_out, ws, stream=None):
 def _formats():
     import torch
     bf16 = dict.fromkeys((torch.bfloat16, torch.int16, torch.uint16), MOE_W_BF16)
-    return {torch.float32: MOE_W_F32, **bf16}, (torch.uint8, torch.float8_e4m3fn), (torch.float32,)
+    return {torch.float32: MOE_W_F32, **bf16}, (torch.uint8, torch.float8_e4m3fn), (torch.float32,), (
+        torch.int32,), (torch.uint8,)
 
 
-_FMT_OF, _CODES, _F32 = _formats()
+_FMT_OF, _CODES, _F32, _I32, _U8 = _formats()
 _BF16 = tuple(t for t, f in _FMT_OF.items() if f == MOE_W_BF16)
 
 
@@ -436,6 +450,56 @@ def moe_add_rmsnorm(T, H, y, resid, weight, eps, resid_out=None, x=None, x8=None
         T, H, _ptr(y), y_fmt, y_row, resid.data_ptr(), r_fmt, r_row, weight.data_ptr(),
         _FMT_OF[weight.dtype], eps, _ptr(resid_out), out_row, _ptr(x), x_row, _ptr(x8),
         _ptr(x8_scale), st), "moe_add_rmsnorm", stream, resid, y, weight, resid_out, x, x8, x8_scale)
+
+
+def moe_sample_workspace_size(T, V):
+    n = ctypes.c_size_t(0)
+    _check(lib.moe_sample_workspace_size(int(T), int(V), ctypes.byref(n)),
+           "moe_sample_workspace_size")
+    return n.value
+
+
+def _sample_args(logits, T, V, u, tokens, ws, temperature, top_k, top_p, min_p, prob):
+    fmt, row = _fmt_of(logits, "logits"), _rows(logits, T, V, "logits")
+    _flat(u, T, "u", _F32)
+    _flat(tokens, T, "tokens", _I32)
+    _flat(ws, 0, "ws", _U8)
+    for t, what, dtypes in ((temperature, "temperature", _F32), (top_k, "top_k", _I32),
+                            (top_p, "top_p", _F32), (min_p, "min_p", _F32), (prob, "prob", _F32)):
+        if t is not None:
+            _flat(t, T, what, dtypes)
+    return fmt, row, moe_sample_params(_ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p))
+
+
+def moe_sample(logits, T, V, u, tokens, ws, temperature=None, top_k=None, top_p=None, min_p=None,
+               prob=None, stream=None):
+    """tokens [T] int32: one draw per row of logits (fp32 or bf16 [T][V], rows
+    may be strided) from the uniform numbers u [T]; prob [T]: the drawn
+    tokens' probabilities after the filters.  The filters' parameters are
+    device tensors [T] (top_k int32, the others fp32) or None: off.  ws: uint8
+    device tensor of at least moe_sample_workspace_size(T, V) bytes."""
+    T, V = int(T), int(V)
+    fmt, row, par = _sample_args(logits, T, V, u, tokens, ws, temperature, top_k, top_p, min_p, prob)
+    _on_device(lambda st: lib.moe_sample(
+        logits.data_ptr(), fmt, T, V, row, par, u.data_ptr(), tokens.data_ptr(), _ptr(prob),
+        ws.data_ptr(), ws.numel(), st), "moe_sample", stream, logits, u, tokens, ws, temperature,
+        top_k, top_p, min_p, prob)
+
+
+def moe_verify_sample(logits, T, V, draft, u, out_tokens, n_out, ws, temperature=None, top_k=None,
+                      top_p=None, min_p=None, prob=None, stream=None):
+    """moe_sample on the rows of a verify pass, and n_out [1] int32: 1 + the
+    drafts [T-1] int32 (None when T = 1) that the rows' tokens agree with
+    from the front."""
+    T, V = int(T), int(V)
+    fmt, row, par = _sample_args(logits, T, V, u, out_tokens, ws, temperature, top_k, top_p, min_p, prob)
+    if draft is not None:
+        _flat(draft, max(T - 1, 0), "draft", _I32)
+    _flat(n_out, 1, "n_out", _I32)
+    _on_device(lambda st: lib.moe_verify_sample(
+        logits.data_ptr(), fmt, T, V, row, par, u.data_ptr(), _ptr(draft), out_tokens.data_ptr(),
+        _ptr(prob), n_out.data_ptr(), ws.data_ptr(), ws.numel(), st), "moe_verify_sample", stream,
+        logits, draft, u, out_tokens, n_out, ws, temperature, top_k, top_p, min_p, prob)
 
 
 def _hptr(a, dtype):

@@ -23,6 +23,7 @@ constexpr int kMaxVerifyT = 64;        // rows of one verify pass
 constexpr int kMaxVocab = 1 << 26;
 constexpr int64_t kMaxT = int64_t(1) << 22;
 constexpr int kMaxNormH = 32768;
+constexpr int kMaxSampleT = 16384;
 constexpr size_t kAlign = 256;
 constexpr int kRouterGemmMinT = 256;       // tokens from which the router runs on MFMA
 constexpr int64_t kFfnGemmMinPairs = 2048; // pairs from which the FFN runs as grouped GEMMs
@@ -294,6 +295,47 @@ PrefillEvents* prefill_events() {
 // Floating formats of the calls around the layer (activations, logits).
 bool act_fmt(int32_t fmt) { return fmt == MOE_W_F32 || fmt == MOE_W_BF16; }
 bool act_aligned(const void* p, int32_t fmt) { return aligned(p, fmt == MOE_W_F32 ? 4 : 2); }
+
+// moe_sample and moe_verify_sample (n_out set).
+moe_status run_sample(const void* logits, int32_t fmt, int32_t T, int32_t V, int64_t stride,
+                      const moe_sample_params* params, const float* u, const int32_t* draft,
+                      int32_t* tokens, float* prob, int32_t* n_out, void* ws, size_t ws_bytes,
+                      void* stream) {
+  size_t need = 0;
+  const moe_status s = moe_sample_workspace_size(T, V, &need);
+  if (s != MOE_OK) return s;
+  if (!act_fmt(fmt)) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (!logits || !act_aligned(logits, fmt) || stride < V || !u || !tokens) return MOE_ERR_INVALID;
+  if (!aligned(u, 4) || !aligned(tokens, 4) || !aligned(prob, 4) || !aligned(draft, 4) ||
+      !aligned(n_out, 4))
+    return MOE_ERR_INVALID;
+  SampleArgs a;
+  memset(&a, 0, sizeof(a));
+  if (params) {
+    a.temperature = params->temperature;
+    a.top_k = params->top_k;
+    a.top_p = params->top_p;
+    a.min_p = params->min_p;
+    if (!aligned(a.temperature, 4) || !aligned(a.top_k, 4) || !aligned(a.top_p, 4) ||
+        !aligned(a.min_p, 4))
+      return MOE_ERR_INVALID;
+  }
+  if (!ws || !aligned(ws, kAlign)) return MOE_ERR_INVALID;
+  if (ws_bytes < need) return MOE_ERR_WORKSPACE;
+  a.logits = logits;
+  a.fmt = fmt;
+  a.T = T;
+  a.V = V;
+  a.stride = stride;
+  a.u = u;
+  a.tokens = tokens;
+  a.prob = prob;
+  a.draft = draft;
+  a.n_out = n_out;
+  a.ws = ws;
+  return device_status(launch_sample(a, static_cast<hipStream_t>(stream)));
+}
 
 // Whether moe_layer takes the fused launch for this layer and T.
 bool fused_shape(const moe_layer_desc* d, int T) {
@@ -711,6 +753,30 @@ moe_status moe_add_rmsnorm(int32_t T, int32_t H, const void* y, int32_t y_fmt, i
   a.x8 = x8;
   a.x8_scale = x8_scale;
   return device_status(launch_add_rmsnorm(a, static_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_sample_workspace_size(int32_t T, int32_t V, size_t* bytes) {
+  if (!bytes || T < 0 || V < 1) return MOE_ERR_INVALID;
+  if (T > kMaxSampleT || V > kMaxVocab) return MOE_ERR_UNSUPPORTED;
+  *bytes = up(sample_ws(T));
+  return MOE_OK;
+}
+
+moe_status moe_sample(const void* logits, int32_t fmt, int32_t T, int32_t V, int64_t stride,
+                      const moe_sample_params* params, const float* u, int32_t* tokens,
+                      float* prob, void* ws, size_t ws_bytes, void* stream) {
+  return run_sample(logits, fmt, T, V, stride, params, u, nullptr, tokens, prob, nullptr, ws,
+                    ws_bytes, stream);
+}
+
+moe_status moe_verify_sample(const void* logits, int32_t fmt, int32_t T, int32_t V, int64_t stride,
+                             const moe_sample_params* params, const float* u,
+                             const int32_t* draft, int32_t* out_tokens, float* prob,
+                             int32_t* n_out, void* ws, size_t ws_bytes, void* stream) {
+  if (T < 1 || !n_out || (T > 1 && !draft)) return MOE_ERR_INVALID;
+  if (T > kMaxVerifyT) return MOE_ERR_UNSUPPORTED;
+  return run_sample(logits, fmt, T, V, stride, params, u, draft, out_tokens, prob, n_out, ws,
+                    ws_bytes, stream);
 }
 
 }  // extern "C"

@@ -120,4 +120,25 @@ struct NormArgs {
 };
 hipError_t launch_add_rmsnorm(const NormArgs& a, hipStream_t st);
 
+// sampling: one token per row of logits
+struct SampleArgs {
+  const void* logits;
+  int fmt;                     // MOE_W_F32 or MOE_W_BF16
+  int T, V;
+  int64_t stride;              // elements from row to row
+  const float* temperature;    // [T] each; null: 1, 0 (all), 1 (all), 0
+  const int32_t* top_k;
+  const float* top_p;
+  const float* min_p;
+  const float* u;              // [T]
+  int32_t* tokens;             // [T]
+  float* prob;                 // [T] (may be null)
+  const int32_t* draft;        // [T - 1], with n_out
+  int32_t* n_out;              // null: no acceptance
+  void* ws;
+  int parts, shift;            // set by launch_sample
+};
+size_t sample_ws(int T);
+hipError_t launch_sample(SampleArgs a, hipStream_t st);
+
 }  // namespace moe

@@ -63,3 +63,84 @@ def test_norm_binding_refusals():
 def test_e4m3_values_are_torchs():
     t = torch.arange(256, dtype=torch.uint8).view(torch.float8_e4m3fn).double().numpy()
     np.testing.assert_array_equal(around.E4M3, t)
+
+
+def _sample(verify=False, **kw):
+    a = dict(x=FAKE, fmt=F32, T=4, V=1000, stride=1000, par=None, u=FAKE)
+    if verify:
+        a["draft"] = FAKE
+    a.update(tok=FAKE, prob=FAKE)
+    if verify:
+        a["n"] = FAKE
+    a.update(ws=FAKE, size=1 << 30)
+    a.update(kw)
+    f = moe.lib.moe_verify_sample if verify else moe.lib.moe_sample
+    return f(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(T=0), OK), (dict(T=-1), INVALID), (dict(V=0, stride=0), INVALID),
+    (dict(T=16385), UNSUPPORTED), (dict(V=(1 << 26) + 1, stride=1 << 27), UNSUPPORTED),
+    (dict(fmt=moe.MOE_W_Q4B32), UNSUPPORTED), (dict(x=None), INVALID), (dict(x=FAKE + 2), INVALID),
+    (dict(fmt=BF16, x=FAKE + 1), INVALID), (dict(stride=999), INVALID), (dict(u=None), INVALID),
+    (dict(u=FAKE + 2), INVALID), (dict(tok=None), INVALID), (dict(tok=FAKE + 1), INVALID),
+    (dict(prob=FAKE + 2), INVALID), (dict(ws=None), INVALID), (dict(ws=FAKE + 64), INVALID),
+    (dict(size=1000), WORKSPACE),
+])
+def test_sample_refusals(kw, status):
+    assert _sample(**kw) == status
+    if kw != dict(T=0) and kw != dict(T=16385):
+        assert _sample(verify=True, **kw) == status
+
+
+def test_verify_sample_refusals():
+    import ctypes
+    assert _sample(verify=True, T=0) == INVALID
+    assert _sample(verify=True, T=65) == UNSUPPORTED
+    assert _sample(verify=True, draft=None) == INVALID
+    assert _sample(verify=True, n=None) == INVALID
+    assert _sample(verify=True, n=FAKE + 2) == INVALID
+    assert _sample(verify=True, draft=FAKE + 2) == INVALID
+    n = ctypes.c_size_t(0)
+    size = moe.lib.moe_sample_workspace_size
+    assert size(4, 1000, None) == INVALID and size(-1, 1000, ctypes.byref(n)) == INVALID
+    assert size(4, 0, ctypes.byref(n)) == INVALID and size(16385, 9, ctypes.byref(n)) == UNSUPPORTED
+    assert size(4, 1000, ctypes.byref(n)) == OK and n.value % 256 == 0 and n.value > 0
+    assert _sample(size=n.value - 1) == WORKSPACE
+    bad = moe.moe_sample_params(FAKE, FAKE, FAKE + 2, FAKE)
+    assert _sample(par=ctypes.byref(bad)) == INVALID
+
+
+def test_sample_binding_refusals():
+    x = torch.zeros((4, 100))
+    u, tok = torch.zeros(4), torch.zeros(4, dtype=torch.int32)
+    ws = torch.zeros(1 << 20, dtype=torch.uint8)
+    call = moe.moe_sample
+    for bad in (
+        lambda: call(x, 4, 100, u, tok, ws),                                    # not on a GPU
+        lambda: call(x, 5, 100, u, tok, ws),
+        lambda: call(x, 4, 101, u, tok, ws),
+        lambda: call(x.double(), 4, 100, u, tok, ws),
+        lambda: call(x, 4, 100, u.double(), tok, ws),
+        lambda: call(x, 4, 100, u, tok.long(), ws),
+        lambda: call(x, 4, 100, u, tok, ws, top_k=u),
+        lambda: call(x, 4, 100, u, tok, ws, temperature=u[:3]),
+        lambda: call(x, 4, 100, u, tok, ws, prob=tok),
+        lambda: moe.moe_verify_sample(x, 4, 100, tok[:2], u, tok, tok, ws),     # 3 drafts wanted
+        lambda: moe.moe_verify_sample(x, 4, 100, tok, u, tok, u, ws),
+    ):
+        with pytest.raises(ValueError):
+            bad()
+
+
+def test_sample_reference_by_hand():
+    """Probabilities 4/8, 2/8, 1/8, 1/8 (logits in powers of two)."""
+    x = np.log(np.array([1.0, 4.0, 2.0, 1.0]))
+    row = around.sample_row
+    assert [row(x, u)[0] for u in (0.0, 0.49, 0.51, 0.74, 0.76, 0.87, 0.88)] == [1, 1, 2, 2, 0, 0, 3]
+    assert row(x, 0.8, top_k=2)[:1] == (2,) and abs(row(x, 0.8, top_k=2)[1] - 1 / 3) < 1e-12
+    assert row(x, 0.99, top_p=0.6)[0] == 2 and row(x, 0.99, top_p=0.4)[0] == 1
+    assert row(x, 0.99, min_p=0.3)[0] == 2 and row(x, 0.99, min_p=2.0)[0] == 1
+    assert row(x, 0.99, temperature=0.0)[0] == 1
+    assert row(np.full(3, -np.inf), 0.5)[0] == -1
+    assert row(x, 0.99)[0] == 3 and row(x, 0.99, temperature=1e-3)[0] == 1
