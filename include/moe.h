@@ -397,6 +397,31 @@ moe_status moe_add_rmsnorm(int32_t T, int32_t H, const void* y, int32_t y_fmt, i
                            int64_t resid_out_stride, uint16_t* x, int64_t x_stride, uint8_t* x8,
                            float* x8_scale, void* stream);
 
+/* Product of 8-bit activations and weights with block scales: the output
+ * head, whose logits moe_verify_accept, moe_sample and moe_verify_sample
+ * take, or another dense projection around the layer ([MD] "問題": besides
+ * the experts, the weights every token uses).
+ *   out[t][n] = sum_b x_scale[t][b] * w_scale[n / 128][b] *
+ *               sum over k in block b of x8[t][k] * w8[n][k]
+ * with blocks b of 128 columns (the last one may be shorter).  x8 [T][K] and
+ * x_scale [T][ceil(K / 128)] are what moe_add_rmsnorm writes; w8 [N][K] and
+ * w_scale [ceil(N / 128)][ceil(K / 128)], one scale per 128 x 128 weights.
+ * Codes are OCP e4m3 (no infinities; a NaN code makes the sums it enters
+ * NaN), scales fp32, all contiguous.  out is MOE_W_F32 or MOE_W_BF16 (rounded
+ * once), out_stride elements from row to row (>= N).  Sums are fp32; for
+ * bf16 outputs of more than 32 tokens the hardware's 8-bit products are used,
+ * which add eight neighbouring ones with 13 bits below the largest of them.
+ * x8 and w8 16-byte aligned, K a multiple of 16, else MOE_ERR_INVALID; N and
+ * T are arbitrary.  The order of the sums depends on (T, N, K) alone: calls
+ * of one shape give identical bits.  Limits: K <= 32768, N <= 2^24, T <= 2^22.
+ * ws: moe_scaled_linear_workspace_size bytes (0 for most shapes; ws may then
+ * be NULL), 256-byte aligned, in use by one call at a time. */
+moe_status moe_scaled_linear_workspace_size(int32_t T, int32_t N, int32_t K, size_t* bytes);
+moe_status moe_scaled_linear(const uint8_t* x8, const float* x_scale, int32_t T,
+                             const uint8_t* w8, const float* w_scale, int32_t N, int32_t K,
+                             void* out, int32_t out_fmt, int64_t out_stride, void* ws,
+                             size_t ws_bytes, void* stream);
+
 /* Sampling: one token per row of logits ([MD] "予測してから検証する" describes
  * greedy drafts and acceptance; the pages name no sampler: the rule below is
  * this library's).  logits: T rows of V entries, MOE_W_F32 or MOE_W_BF16,

@@ -29,7 +29,8 @@ EXPORTS = ("moe_status_string", "moe_version", "moe_workspace_size", "moe_route"
            "moe_prefill_workspace_size", "moe_prefill_layer", "moe_layer_check",
            "moe_set_wait_budget", "moe_set_trace", "moe_layer_noalloc",
            "moe_expert_ffn_accum", "moe_set_deterministic", "moe_add_rmsnorm",
-           "moe_sample_workspace_size", "moe_sample", "moe_verify_sample")
+           "moe_scaled_linear_workspace_size", "moe_scaled_linear", "moe_sample_workspace_size",
+           "moe_sample", "moe_verify_sample")
 MOE_REFRESH_MAX_SWAPS = 1024
 
 
@@ -127,6 +128,10 @@ def _load():
     lib.moe_add_rmsnorm.restype = I32
     lib.moe_add_rmsnorm.argtypes = [I32, I32, P, I32, I64, P, I32, I64, P, I32, F32, P, I64, P, I64,
                                     P, P, P]
+    lib.moe_scaled_linear_workspace_size.restype = I32
+    lib.moe_scaled_linear_workspace_size.argtypes = [I32, I32, I32, ctypes.POINTER(SZ)]
+    lib.moe_scaled_linear.restype = I32
+    lib.moe_scaled_linear.argtypes = [P, P, I32, P, P, I32, I32, P, I32, I64, P, SZ, P]
     SA = ctypes.POINTER(moe_sample_params)
     lib.moe_sample_workspace_size.restype = I32
     lib.moe_sample_workspace_size.argtypes = [I32, I32, ctypes.POINTER(SZ)]
@@ -450,6 +455,34 @@ def moe_add_rmsnorm(T, H, y, resid, weight, eps, resid_out=None, x=None, x8=None
         T, H, _ptr(y), y_fmt, y_row, resid.data_ptr(), r_fmt, r_row, weight.data_ptr(),
         _FMT_OF[weight.dtype], eps, _ptr(resid_out), out_row, _ptr(x), x_row, _ptr(x8),
         _ptr(x8_scale), st), "moe_add_rmsnorm", stream, resid, y, weight, resid_out, x, x8, x8_scale)
+
+
+def moe_scaled_linear_workspace_size(T, N, K):
+    n = ctypes.c_size_t(0)
+    _check(lib.moe_scaled_linear_workspace_size(int(T), int(N), int(K), ctypes.byref(n)),
+           "moe_scaled_linear_workspace_size")
+    return n.value
+
+
+def moe_scaled_linear(x8, x_scale, T, w8, w_scale, N, K, out, ws=None, stream=None):
+    """out [T][N] (fp32 or bf16, rows may be strided) = x8 [T][K] times w8
+    [N][K] transposed, e4m3 codes (uint8 or float8_e4m3fn) with scales
+    x_scale [T][ceil(K/128)] and w_scale [ceil(N/128)][ceil(K/128)] (fp32).
+    ws: uint8 device tensor of at least moe_scaled_linear_workspace_size(T,
+    N, K) bytes (None when that is 0)."""
+    T, N, K = int(T), int(N), int(K)
+    kb = (K + 127) // 128
+    _flat(x8, T * K, "x8", _CODES)
+    _flat(x_scale, T * kb, "x_scale", _F32)
+    _flat(w8, N * K, "w8", _CODES)
+    _flat(w_scale, (N + 127) // 128 * kb, "w_scale", _F32)
+    if ws is not None:
+        _flat(ws, 0, "ws", _U8)
+    fmt, row = _fmt_of(out, "out"), _rows(out, T, N, "out")
+    _on_device(lambda st: lib.moe_scaled_linear(
+        x8.data_ptr(), x_scale.data_ptr(), T, w8.data_ptr(), w_scale.data_ptr(), N, K,
+        out.data_ptr(), fmt, row, _ptr(ws), ws.numel() if ws is not None else 0, st),
+        "moe_scaled_linear", stream, x8, x_scale, w8, w_scale, out, ws)
 
 
 def moe_sample_workspace_size(T, V):

@@ -24,6 +24,8 @@ constexpr int kMaxVocab = 1 << 26;
 constexpr int64_t kMaxT = int64_t(1) << 22;
 constexpr int kMaxNormH = 32768;
 constexpr int kMaxSampleT = 16384;
+constexpr int kMaxLinearK = 32768;
+constexpr int kMaxLinearN = 1 << 24;
 constexpr size_t kAlign = 256;
 constexpr int kRouterGemmMinT = 256;       // tokens from which the router runs on MFMA
 constexpr int64_t kFfnGemmMinPairs = 2048; // pairs from which the FFN runs as grouped GEMMs
@@ -753,6 +755,43 @@ moe_status moe_add_rmsnorm(int32_t T, int32_t H, const void* y, int32_t y_fmt, i
   a.x8 = x8;
   a.x8_scale = x8_scale;
   return device_status(launch_add_rmsnorm(a, static_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_scaled_linear_workspace_size(int32_t T, int32_t N, int32_t K, size_t* bytes) {
+  if (!bytes || T < 0 || N < 1 || K < 16 || K % 16) return MOE_ERR_INVALID;
+  if (T > kMaxT || N > kMaxLinearN || K > kMaxLinearK) return MOE_ERR_UNSUPPORTED;
+  *bytes = 0;
+  return MOE_OK;
+}
+
+moe_status moe_scaled_linear(const uint8_t* x8, const float* x_scale, int32_t T,
+                             const uint8_t* w8, const float* w_scale, int32_t N, int32_t K,
+                             void* out, int32_t out_fmt, int64_t out_stride, void* ws,
+                             size_t ws_bytes, void* stream) {
+  size_t need = 0;
+  const moe_status s = moe_scaled_linear_workspace_size(T, N, K, &need);
+  if (s != MOE_OK) return s;
+  if (!act_fmt(out_fmt)) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (!x8 || !x_scale || !w8 || !w_scale || !out) return MOE_ERR_INVALID;
+  if (!aligned(x8, 16) || !aligned(w8, 16) || !aligned(x_scale, 4) || !aligned(w_scale, 4) ||
+      !act_aligned(out, out_fmt) || out_stride < N)
+    return MOE_ERR_INVALID;
+  if (need && (!ws || !aligned(ws, kAlign))) return MOE_ERR_INVALID;
+  if (ws_bytes < need) return MOE_ERR_WORKSPACE;
+  LinearArgs a;
+  memset(&a, 0, sizeof(a));
+  a.x8 = x8;
+  a.x_scale = x_scale;
+  a.w8 = w8;
+  a.w_scale = w_scale;
+  a.out = out;
+  a.T = T;
+  a.N = N;
+  a.K = K;
+  a.out_fmt = out_fmt;
+  a.out_stride = out_stride;
+  return device_status(launch_scaled_linear(a, static_cast<hipStream_t>(stream)));
 }
 
 moe_status moe_sample_workspace_size(int32_t T, int32_t V, size_t* bytes) {

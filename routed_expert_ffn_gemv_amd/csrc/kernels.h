@@ -141,4 +141,18 @@ struct SampleArgs {
 size_t sample_ws(int T);
 hipError_t launch_sample(SampleArgs a, hipStream_t st);
 
+// product of e4m3 activations and weights with block scales
+struct LinearArgs {
+  const uint8_t* x8;           // [T][K]
+  const float* x_scale;        // [T][ceil(K / 128)]
+  const uint8_t* w8;           // [N][K]
+  const float* w_scale;        // [ceil(N / 128)][ceil(K / 128)]
+  void* out;                   // [T] rows of N
+  int T, N, K, out_fmt;
+  int64_t out_stride;
+  bool wide_out;               // four outputs of a row can be stored at once (set by the launcher)
+  int seg_blocks;              // blocks of K staged at a time (set by the launcher)
+};
+hipError_t launch_scaled_linear(LinearArgs a, hipStream_t st);
+
 }  // namespace moe

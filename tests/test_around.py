@@ -144,3 +144,53 @@ def test_sample_reference_by_hand():
     assert row(x, 0.99, temperature=0.0)[0] == 1
     assert row(np.full(3, -np.inf), 0.5)[0] == -1
     assert row(x, 0.99)[0] == 3 and row(x, 0.99, temperature=1e-3)[0] == 1
+
+
+def _linear(**kw):
+    a = dict(x8=FAKE, xs=FAKE, T=4, w8=FAKE, ws_=FAKE, N=300, K=256, out=FAKE, fmt=F32, stride=300,
+             ws=FAKE, size=1 << 30)
+    a.update(kw)
+    return moe.lib.moe_scaled_linear(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(T=0), OK), (dict(T=-1), INVALID), (dict(N=0, stride=0), INVALID), (dict(K=0), INVALID),
+    (dict(K=200), INVALID), (dict(K=8), INVALID), (dict(K=32784), UNSUPPORTED),
+    (dict(N=(1 << 24) + 1, stride=1 << 25), UNSUPPORTED), (dict(T=(1 << 22) + 1), UNSUPPORTED),
+    (dict(fmt=moe.MOE_W_Q2B32), UNSUPPORTED), (dict(stride=299), INVALID),
+    (dict(x8=None), INVALID), (dict(xs=None), INVALID), (dict(w8=None), INVALID),
+    (dict(ws_=None), INVALID), (dict(out=None), INVALID), (dict(x8=FAKE + 8), INVALID),
+    (dict(w8=FAKE + 8), INVALID), (dict(xs=FAKE + 2), INVALID), (dict(ws_=FAKE + 2), INVALID),
+    (dict(out=FAKE + 2), INVALID), (dict(fmt=BF16, out=FAKE + 1), INVALID),
+])
+def test_linear_refusals(kw, status):
+    assert _linear(**kw) == status
+
+
+def test_linear_binding_refusals():
+    x8, w8 = torch.zeros((4, 256), dtype=torch.uint8), torch.zeros((300, 256), dtype=torch.uint8)
+    xs, ws = torch.zeros((4, 2)), torch.zeros((3, 2))
+    out = torch.zeros((4, 300))
+    call = moe.moe_scaled_linear
+    for bad in (
+        lambda: call(x8, xs, 4, w8, ws, 300, 256, out),                     # not on a GPU
+        lambda: call(x8, xs, 5, w8, ws, 300, 256, out),
+        lambda: call(x8, xs[:, :1], 4, w8, ws, 300, 256, out),
+        lambda: call(x8, xs, 4, w8, ws[:2], 300, 256, out),
+        lambda: call(x8, xs, 4, w8[:299], ws, 300, 256, out),
+        lambda: call(x8, xs, 4, w8, ws, 300, 256, out[:, :299]),
+        lambda: call(x8.float(), xs, 4, w8, ws, 300, 256, out),
+        lambda: call(x8, xs.double(), 4, w8, ws, 300, 256, out),
+        lambda: call(x8, xs, 4, w8, ws, 300, 256, out.half()),
+        lambda: call(x8, xs, 4, w8.t().contiguous().t(), ws, 300, 256, out),
+    ):
+        with pytest.raises(ValueError):
+            bad()
+
+
+def test_linear_reference_by_hand():
+    x8 = np.array([[0x38, 0x40] + [0] * 14], np.uint8)        # 1, 2
+    w8 = np.array([[0x38, 0xB8] + [0] * 14, [0x08, 0x01] + [0] * 14], np.uint8)   # 1, -1; 2^-6, 2^-9
+    out, mag = around.scaled_linear(x8, np.array([[2.0]], np.float32), w8, np.array([[4.0]], np.float32))
+    np.testing.assert_array_equal(out, [[-8.0, 8 * (2.0 ** -6 + 2.0 ** -8)]])
+    np.testing.assert_array_equal(mag, [[24.0, 8 * (2.0 ** -6 + 2.0 ** -8)]])
