@@ -386,45 +386,60 @@ _BF16 = tuple(t for t, f in _FMT_OF.items() if f == MOE_W_BF16)
 
 
 def _fmt_of(t, what):
-    f = _FMT_OF.get(t.dtype)
-    if f is None:
-        raise ValueError(f"{what}: fp32 or bf16 (or bf16 bits as 16-bit integers) wanted, got {t.dtype}")
-    return f
+    try:
+        return _FMT_OF[t.dtype]
+    except KeyError:
+        raise ValueError(f"{what}: fp32 or bf16 (or bf16 bits as 16-bit integers) wanted, "
+                         f"got {t.dtype}") from None
 
 
 def _rows(t, T, n, what):
     """Stride of a [>= T][>= n] tensor whose rows are contiguous."""
-    shape = t.shape
-    if len(shape) != 2 or shape[0] < T or shape[1] < n:
-        raise ValueError(f"{what}: [{T}][{n}] wanted, got {list(shape)}")
-    row, col = t.stride()
-    if col != 1 and n > 1:
-        raise ValueError(f"{what}: the elements of a row must be consecutive")
-    return row if T > 1 else max(row, n)
+    if t.ndim == 2:
+        rows, cols = t.shape
+        row, col = t.stride()
+        if rows >= T and cols >= n and (col == 1 or n == 1):
+            return row if T > 1 or row > n else n
+    raise ValueError(f"{what}: [{T}][{n}] with the elements of a row next to each other wanted, "
+                     f"got {list(t.shape)} with strides {t.stride()}")
 
 
 def _flat(t, n, what, dtypes):
-    if t.dtype not in dtypes:
-        raise ValueError(f"{what}: {' or '.join(map(str, dtypes))} wanted, got {t.dtype}")
-    if t.numel() < n or not t.is_contiguous():
-        raise ValueError(f"{what}: {n} contiguous elements wanted, got {list(t.shape)}")
+    if t.dtype not in dtypes or t.numel() < n or not t.is_contiguous():
+        raise ValueError(f"{what}: {n} contiguous elements of {' or '.join(map(str, dtypes))} wanted, "
+                         f"got {list(t.shape)} of {t.dtype}")
 
 
-def _on_device(call, what, stream, *tensors):
-    """call(stream handle) on the device that holds every one of the tensors
-    (None: left out); stream None: that device's current stream."""
+def _gpu_of(what, first, *others):
+    """The one GPU that holds the tensors (None: left out)."""
+    dev = first.get_device()
+    for t in others:
+        if t is not None and t.get_device() != dev:
+            dev = -1
+    if dev < 0:
+        raise ValueError(f"{what}: every tensor must be on one GPU")
+    return dev
+
+
+def _launch(f, what, dev, stream, *args):
+    """f(*args, stream's handle) on GPU dev; stream None: its current one."""
+    if dev != _current_device():
+        with _device(dev):
+            return _launch(f, what, dev, stream, *args)
+    status = f(*args, _raw_stream(dev) if stream is None else _stream(stream))
+    if status != MOE_OK:
+        raise MoEError(status, what)
+
+
+def _torch_device():
+    # the current stream's handle without a Stream object (2.6 us less per call)
     import torch
-    dev = -1
-    for t in tensors:
-        if t is not None:
-            d = t.get_device()
-            if d < 0 or (dev >= 0 and d != dev):
-                raise ValueError(f"{what}: every tensor must be on one GPU")
-            dev = d
-    if dev == torch.cuda.current_device():
-        return _check(call(_stream(stream)), what)
-    with torch.cuda.device(dev):
-        return _check(call(_stream(stream)), what)
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    raw = raw or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+    return torch.cuda.current_device, torch.cuda.device, raw
+
+
+_current_device, _device, _raw_stream = _torch_device()
 
 
 def moe_add_rmsnorm(T, H, y, resid, weight, eps, resid_out=None, x=None, x8=None, x8_scale=None,
@@ -451,10 +466,10 @@ def moe_add_rmsnorm(T, H, y, resid, weight, eps, resid_out=None, x=None, x8=None
     if x8_scale is not None:
         _flat(x8_scale, T * ((H + 127) // 128), "x8_scale", _F32)
     _flat(weight, H, "weight", _FMT_OF)
-    _on_device(lambda st: lib.moe_add_rmsnorm(
-        T, H, _ptr(y), y_fmt, y_row, resid.data_ptr(), r_fmt, r_row, weight.data_ptr(),
-        _FMT_OF[weight.dtype], eps, _ptr(resid_out), out_row, _ptr(x), x_row, _ptr(x8),
-        _ptr(x8_scale), st), "moe_add_rmsnorm", stream, resid, y, weight, resid_out, x, x8, x8_scale)
+    dev = _gpu_of("moe_add_rmsnorm", resid, y, weight, resid_out, x, x8, x8_scale)
+    _launch(lib.moe_add_rmsnorm, "moe_add_rmsnorm", dev, stream, T, H, _ptr(y), y_fmt, y_row,
+            resid.data_ptr(), r_fmt, r_row, weight.data_ptr(), _FMT_OF[weight.dtype], eps,
+            _ptr(resid_out), out_row, _ptr(x), x_row, _ptr(x8), _ptr(x8_scale))
 
 
 def moe_scaled_linear_workspace_size(T, N, K):
@@ -479,10 +494,10 @@ def moe_scaled_linear(x8, x_scale, T, w8, w_scale, N, K, out, ws=None, stream=No
     if ws is not None:
         _flat(ws, 0, "ws", _U8)
     fmt, row = _fmt_of(out, "out"), _rows(out, T, N, "out")
-    _on_device(lambda st: lib.moe_scaled_linear(
-        x8.data_ptr(), x_scale.data_ptr(), T, w8.data_ptr(), w_scale.data_ptr(), N, K,
-        out.data_ptr(), fmt, row, _ptr(ws), ws.numel() if ws is not None else 0, st),
-        "moe_scaled_linear", stream, x8, x_scale, w8, w_scale, out, ws)
+    dev = _gpu_of("moe_scaled_linear", x8, x_scale, w8, w_scale, out, ws)
+    _launch(lib.moe_scaled_linear, "moe_scaled_linear", dev, stream, x8.data_ptr(),
+            x_scale.data_ptr(), T, w8.data_ptr(), w_scale.data_ptr(), N, K, out.data_ptr(), fmt, row,
+            _ptr(ws), ws.numel() if ws is not None else 0)
 
 
 def moe_sample_workspace_size(T, V):
@@ -497,10 +512,16 @@ def _sample_args(logits, T, V, u, tokens, ws, temperature, top_k, top_p, min_p, 
     _flat(u, T, "u", _F32)
     _flat(tokens, T, "tokens", _I32)
     _flat(ws, 0, "ws", _U8)
-    for t, what, dtypes in ((temperature, "temperature", _F32), (top_k, "top_k", _I32),
-                            (top_p, "top_p", _F32), (min_p, "min_p", _F32), (prob, "prob", _F32)):
-        if t is not None:
-            _flat(t, T, what, dtypes)
+    if temperature is not None:
+        _flat(temperature, T, "temperature", _F32)
+    if top_k is not None:
+        _flat(top_k, T, "top_k", _I32)
+    if top_p is not None:
+        _flat(top_p, T, "top_p", _F32)
+    if min_p is not None:
+        _flat(min_p, T, "min_p", _F32)
+    if prob is not None:
+        _flat(prob, T, "prob", _F32)
     return fmt, row, moe_sample_params(_ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p))
 
 
@@ -513,10 +534,9 @@ def moe_sample(logits, T, V, u, tokens, ws, temperature=None, top_k=None, top_p=
     device tensor of at least moe_sample_workspace_size(T, V) bytes."""
     T, V = int(T), int(V)
     fmt, row, par = _sample_args(logits, T, V, u, tokens, ws, temperature, top_k, top_p, min_p, prob)
-    _on_device(lambda st: lib.moe_sample(
-        logits.data_ptr(), fmt, T, V, row, par, u.data_ptr(), tokens.data_ptr(), _ptr(prob),
-        ws.data_ptr(), ws.numel(), st), "moe_sample", stream, logits, u, tokens, ws, temperature,
-        top_k, top_p, min_p, prob)
+    dev = _gpu_of("moe_sample", logits, u, tokens, ws, temperature, top_k, top_p, min_p, prob)
+    _launch(lib.moe_sample, "moe_sample", dev, stream, logits.data_ptr(), fmt, T, V, row, par,
+            u.data_ptr(), tokens.data_ptr(), _ptr(prob), ws.data_ptr(), ws.numel())
 
 
 def moe_verify_sample(logits, T, V, draft, u, out_tokens, n_out, ws, temperature=None, top_k=None,
@@ -529,10 +549,11 @@ def moe_verify_sample(logits, T, V, draft, u, out_tokens, n_out, ws, temperature
     if draft is not None:
         _flat(draft, max(T - 1, 0), "draft", _I32)
     _flat(n_out, 1, "n_out", _I32)
-    _on_device(lambda st: lib.moe_verify_sample(
-        logits.data_ptr(), fmt, T, V, row, par, u.data_ptr(), _ptr(draft), out_tokens.data_ptr(),
-        _ptr(prob), n_out.data_ptr(), ws.data_ptr(), ws.numel(), st), "moe_verify_sample", stream,
-        logits, draft, u, out_tokens, n_out, ws, temperature, top_k, top_p, min_p, prob)
+    dev = _gpu_of("moe_verify_sample", logits, draft, u, out_tokens, n_out, ws, temperature, top_k,
+                  top_p, min_p, prob)
+    _launch(lib.moe_verify_sample, "moe_verify_sample", dev, stream, logits.data_ptr(), fmt, T, V, row,
+            par, u.data_ptr(), _ptr(draft), out_tokens.data_ptr(), _ptr(prob), n_out.data_ptr(),
+            ws.data_ptr(), ws.numel())
 
 
 def _hptr(a, dtype):
