@@ -370,104 +370,234 @@ __global__ __launch_bounds__(KS * 64) void few_kernel(const LinearArgs a) {
 
 // ---- many tokens
 
-// A tile of BN weight rows and BT tokens; WN x WT waves.  Two LDS buffers:
-// the next block of 128 columns is loaded while one is multiplied.  fp32
-// outputs convert the codes to fp16 on their way from LDS.
-template <int BN, int BT, int WN, int WT, int OUT>
+// Which of a wave's weight rows is operand row m of its i-th group of 16.
+// A lane ends up with rows m = 4 (lane / 16) .. + 3 of every group: for fp32
+// four consecutive outputs (16 bytes); for bf16 groups are taken in pairs of
+// 32 rows so that a lane's four of both are eight consecutive ones.
+template <int OUT>
+__device__ __forceinline__ int weight_row(int i, int m) {
+  return OUT == MOE_W_F32 ? i * 16 + m : (i >> 1) * 32 + (m >> 2) * 8 + (i & 1) * 4 + (m & 3);
+}
+
+// Eight consecutive outputs of one token as bf16.
+__device__ __forceinline__ void store8(const LinearArgs& a, int t, int n, f32x4 u, f32x4 v) {
+  if (t >= a.T || n >= a.N) return;
+  if (a.wide_out && n + 8 <= a.N) {
+    const f32x2 p[4] = {{u[0], u[1]}, {u[2], u[3]}, {v[0], v[1]}, {v[2], v[3]}};
+    u32x4 q;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      q[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(p[i], bf16x2_t));
+    *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.out) + int64_t(t) * a.out_stride + n) = q;
+    return;
+  }
+  store4<MOE_W_BF16>(a, t, n, u);
+  store4<MOE_W_BF16>(a, t, n + 4, v);
+}
+
+// Tiles of BN weight rows and BT tokens, WN x WT waves, a ring of STAGES LDS
+// buffers of one block of 128 columns each: STAGES - 1 blocks are on their way
+// while one is multiplied, across tiles too (workgroups stay and walk over
+// tiles, so that the first blocks of a tile arrive during the stores of the
+// one before).  The loads are buffer loads straight to LDS: rows past the
+// matrices' ends read as zero, and so do columns past K (their lanes' offset
+// is moved out of range).  A row's 16-byte chunks are permuted in LDS by the
+// row, so that the rows a fragment reads together meet no bank twice.
+// fp32 outputs convert the codes to fp16 on their way from LDS.
+template <int BN, int BT, int WN, int WT, int STAGES, int OUT>
+struct Tile {
+  static constexpr int kWaves = WN * WT;
+  static constexpr int NI = BN / WN / 16, TI = BT / WT / 16;
+  static constexpr int kRows = BN + BT;                       // rows of one buffer, 128 bytes each
+  static constexpr int kLoads = kRows / 8 / kWaves;           // 1 KiB loads per wave and block
+  static constexpr int kBuffer = kRows * kBlock + BT * 4;     // and the tokens' scales
+  static constexpr int kStores = OUT == MOE_W_F32 ? NI * TI : NI * TI / 2;   // per wave and tile
+  static_assert(kRows % (8 * kWaves) == 0 && BN % (8 * kLoads) == 0 && BN / WN <= kBlock &&
+                    NI % 2 == 0 && BT <= 64 * kWaves,
+                "tile shape");
+};
+
+template <int N>
+__device__ __forceinline__ void wait_until() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N < 63 ? N : 63) : "memory");
+}
+
+// A barrier that leaves loads and stores under way (__syncthreads waits for
+// them all); this wave's reads of LDS have ended.
+__device__ __forceinline__ void barrier_lds() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+template <int BN, int BT, int WN, int WT, int STAGES, int OUT>
 __global__ __launch_bounds__(WN* WT * 64) void tile_kernel(const LinearArgs a) {
-  constexpr int WAVES = WN * WT;
-  constexpr int NI = BN / WN / 16, TI = BT / WT / 16;
-  constexpr int ROWS = BN + BT;                // rows of one buffer, 128 bytes each
-  constexpr int LOADS = ROWS / 8 / WAVES;      // 1 KiB loads per wave and block
-  static_assert(ROWS % (8 * WAVES) == 0 && BN / WN <= kBlock, "tile shape");
+  using S = Tile<BN, BT, WN, WT, STAGES, OUT>;
+  constexpr int NI = S::NI, TI = S::TI, LOADS = S::kLoads, BUFFER = S::kBuffer;
   extern __shared__ uint8_t lds[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, g = lane >> 4;
-  const int KB = (a.K + kBlock - 1) / kBlock;
-  const int tiles_n = (a.N + BN - 1) / BN;
-  const int n0 = int(blockIdx.x) % tiles_n * BN, t0 = int(blockIdx.x) / tiles_n * BT;
   const int wn = wave % WN, wt = wave / WN;
+  const int KB = (a.K + kBlock - 1) / kBlock;
 
-  // load i of this wave fills rows r .. r + 7 of the buffer, lane l the slot
-  // l % 8 of row r + l / 8, with the row's chunk (l % 8) ^ (l / 8)
-  const int chunk = ((lane & 7) ^ (lane >> 3)) * 16;
-  const uint8_t* src[LOADS];
+  // Tiles: XCD x (blockIdx mod 8) takes a contiguous run; along it, groups of
+  // four token tiles walk over the weights together, so that what an XCD's
+  // CUs read at a time fits its L2.
+  const int tiles_n = (a.N + BN - 1) / BN, tiles_t = (a.T + BT - 1) / BT, tiles = tiles_n * tiles_t;
+  const int run = (tiles + 7) / 8, first = int(blockIdx.x & 7) * run;
+  const int last = min(first + run, tiles), step = int(gridDim.x >> 3);
+  constexpr int kGroup = 4;
+  auto place = [&](int id, int& n0, int& t0) {
+    const int size = kGroup * tiles_n, gi = id / size, rem = id % size;
+    const int rows = min(kGroup, tiles_t - gi * kGroup);
+    t0 = (gi * kGroup + rem % rows) * BT;
+    n0 = rem / rows * BN;
+  };
+
+  // the loads' side: load i of this wave fills rows 8i .. 8i + 7 of its part
+  // of the buffer, lane l the slot l % 8 of row l / 8
+  const bool of_w = wave * LOADS * 8 < BN;
+  const int row0 = wave * LOADS * 8 - (of_w ? 0 : BN);
+  auto wswap = [](int r) { return OUT == MOE_W_F32 ? r & 7 : (r & 3) | ((r >> 1) & 4); };
+  uint32_t off[2], off_last[2];
 #pragma unroll
-  for (int i = 0; i < LOADS; ++i) {
-    const int r = (wave * LOADS + i) * 8 + (lane >> 3);
-    src[i] = r < BN ? a.w8 + int64_t(min(n0 + r, a.N - 1)) * a.K
-                    : a.x8 + int64_t(min(t0 + r - BN, a.T - 1)) * a.K;
+  for (int i = 0; i < 2; ++i) {
+    const int r = i * 8 + (lane >> 3), chunk = (lane & 7) ^ (of_w ? wswap(r) : r & 7);
+    off[i] = uint32_t(lane >> 3) * a.K + chunk * 16;
+    off_last[i] = (KB - 1) * kBlock + chunk * 16 < a.K ? off[i] : 0x7FFFFFFFu;
   }
-  auto load = [&](int kb, int buf) {
-    uint8_t* dst = lds + buf * (ROWS * kBlock) + wave * (LOADS * 1024);
-    if (kb * kBlock + kBlock <= a.K) {
+  int load_id = first + int(blockIdx.x >> 3), load_kb = 0, load_buf = 0;
+  int under_way = 0;     // blocks loaded and not yet multiplied
+  if (load_id >= last) return;
+  __amdgpu_buffer_rsrc_t src;
+  const float* scales;
+  auto source = [&]() {
+    int n0, t0;
+    place(load_id, n0, t0);
+    const int64_t left = (of_w ? int64_t(a.N - n0) : int64_t(a.T - t0)) * a.K;
+    const uint8_t* base = of_w ? a.w8 + int64_t(n0) * a.K : a.x8 + int64_t(t0) * a.K;
+    src = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0,
+                                            int(left < 0x7FFFFFFF ? left : 0x7FFFFFFF), 0x00027000);
+    scales = a.x_scale + int64_t(min(t0 + (wave * 64 + lane) % BT, a.T - 1)) * KB;
+  };
+  auto load = [&]() {
+    if (load_id >= last) return;
+    uint8_t* dst = lds + load_buf * BUFFER;
+    const bool whole = load_kb + 1 < KB;
 #pragma unroll
-      for (int i = 0; i < LOADS; ++i)
-        __builtin_amdgcn_global_load_lds(
-            (const __attribute__((address_space(1))) void*)(src[i] + kb * kBlock + chunk),
-            (__attribute__((address_space(3))) void*)(dst + i * 1024), 16, 0, 0);
-    } else {
-      // the last, shorter block: zeros past the row's end
-      const u32x4 zero = {0u, 0u, 0u, 0u};
-#pragma unroll
-      for (int i = 0; i < LOADS; ++i) {
-        const int k = kb * kBlock + chunk;
-        const u32x4 v = k < a.K ? *reinterpret_cast<const u32x4*>(src[i] + k) : zero;
-        *reinterpret_cast<u32x4*>(dst + i * 1024 + lane * 16) = v;
-      }
+    for (int i = 0; i < LOADS; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          src, (__attribute__((address_space(3))) void*)(dst + wave * (LOADS * 1024) + i * 1024), 16,
+          whole ? off[i & 1] : off_last[i & 1], (row0 + i * 8) * a.K + load_kb * kBlock, 0, 0);
+    if (wave * 64 < BT)
+      __builtin_amdgcn_global_load_lds(
+          (const __attribute__((address_space(1))) void*)(scales + load_kb),
+          (__attribute__((address_space(3))) void*)(dst + S::kRows * kBlock + wave * 256), 4, 0, 0);
+    load_buf = load_buf + 1 == STAGES ? 0 : load_buf + 1;
+    ++under_way;
+    if (++load_kb == KB) {
+      load_kb = 0;
+      load_id += step;
+      if (load_id < last) source();
     }
   };
-
-  const float* wsc = a.w_scale + int64_t(min(n0 + wn * (BN / WN), a.N - 1) / kBlock) * KB;
-  const float* xsc[TI];
+  source();
 #pragma unroll
-  for (int j = 0; j < TI; ++j)
-    xsc[j] = a.x_scale + int64_t(min(t0 + wt * (BT / WT) + j * 16 + col, a.T - 1)) * KB;
+  for (int i = 0; i + 1 < STAGES; ++i) load();
 
-  f32x4 acc[NI][TI];
-#pragma unroll
-  for (int i = 0; i < NI; ++i)
-#pragma unroll
-    for (int j = 0; j < TI; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-
+  // the products' side
   using Frag = std::conditional_t<OUT == MOE_W_F32, Frag16, Frag8>;
-  auto frag = [&](const uint8_t* rows) {
-    const uint8_t* p = rows + col * kBlock;
-    return Frag(*reinterpret_cast<const u32x4*>(p + ((g ^ (col & 7)) * 16)),
-                *reinterpret_cast<const u32x4*>(p + (((g + 4) ^ (col & 7)) * 16)));
+  auto frag = [&](const uint8_t* row, int swap) {
+    return Frag(load16(row + ((g ^ swap) * 16)), load16(row + (((g + 4) ^ swap) * 16)));
   };
-
-  load(0, 0);
-  for (int kb = 0; kb < KB; ++kb) {
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-    if (kb + 1 < KB) load(kb + 1, (kb + 1) & 1);
-    const uint8_t* buf = lds + (kb & 1) * (ROWS * kBlock);
-    const float ws = wsc[kb];
-    float sc[TI];
-    Frag x[TI];
+  const int x_at = (BN + wt * (BT / WT) + col) * kBlock, w_at = wn * (BN / WN) * kBlock;
+  const int s_at = S::kRows * kBlock + (wt * (BT / WT) + col) * 4;
+  int buf = 0;
+  bool stored = false;
+#pragma unroll 1
+  for (int id = first + int(blockIdx.x >> 3); id < last; id += step) {
+    int n0, t0;
+    place(id, n0, t0);
+    const int wave_n = n0 + wn * (BN / WN), wave_t = t0 + wt * (BT / WT);
+    const float* wsc = a.w_scale + int64_t(min(wave_n, a.N - 1) / kBlock) * KB;
+    f32x4 acc[NI][TI];
 #pragma unroll
-    for (int j = 0; j < TI; ++j) {
-      sc[j] = xsc[j][kb] * ws;
-      x[j] = frag(buf + (BN + wt * (BT / WT) + j * 16) * kBlock);
-    }
+    for (int i = 0; i < NI; ++i)
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const Frag w = frag(buf + (wn * (BN / WN) + i * 16) * kBlock);
+      for (int j = 0; j < TI; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    float ws = wsc[0];
+#pragma unroll 1
+    for (int kb = 0; kb < KB; ++kb) {
+      // this block has arrived when no more than the later blocks' loads (and,
+      // behind them, the last tile's stores) are outstanding
+      if (under_way < STAGES - 1)
+        wait_until<0>();
+      else if (stored)
+        wait_until<(STAGES - 2) * LOADS + S::kStores>();
+      else
+        wait_until<(STAGES - 2) * LOADS>();
+      stored = false;
+      --under_way;
+      barrier_lds();
+      const uint8_t* now = lds + buf * BUFFER;
+      auto wfrag = [&](int i) {
+        const int r = weight_row<OUT>(i, col);
+        return frag(now + w_at + r * kBlock, wswap(r));
+      };
+      float sc[TI];
+      Frag x[TI], w = wfrag(0);
 #pragma unroll
       for (int j = 0; j < TI; ++j) {
-        const f32x4 d = product(w, x[j]);
+        x[j] = frag(now + x_at + j * (16 * kBlock), col & 7);
+        sc[j] = *reinterpret_cast<const float*>(now + s_at + j * 64) * ws;
+      }
+      load();      // into the buffer that every wave has left
+      ws = wsc[min(kb + 1, KB - 1)];
+      // the sums of group i - 1 join the accumulators while group i is multiplied
+      f32x4 d[2][TI];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(d[e], sc[j], acc[i][j][e]);
+      for (int i = 0; i < NI; ++i) {
+        Frag next;
+        if (i + 1 < NI) next = wfrag(i + 1);
+#pragma unroll
+        for (int j = 0; j < TI; ++j) {
+          d[i & 1][j] = product(w, x[j]);
+          if (i > 0) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              acc[i - 1][j][e] = fmaf(d[(i - 1) & 1][j][e], sc[j], acc[i - 1][j][e]);
+          }
+          if (OUT == MOE_W_BF16) {
+            // one matrix instruction, four fma, a fragment's read
+            __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x2, 4, 0);
+            if (j < 2) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+          }
+        }
+        w = next;
+        if (OUT == MOE_W_BF16) __builtin_amdgcn_sched_barrier(0);
+      }
+#pragma unroll
+      for (int j = 0; j < TI; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          acc[NI - 1][j][e] = fmaf(d[(NI - 1) & 1][j][e], sc[j], acc[NI - 1][j][e]);
+      buf = buf + 1 == STAGES ? 0 : buf + 1;
+    }
+#pragma unroll
+    for (int j = 0; j < TI; ++j) {
+      const int t = wave_t + j * 16 + col;
+#pragma unroll
+      for (int i = 0; i < NI; i += 2) {
+        if (OUT == MOE_W_F32) {
+          store4<OUT>(a, t, wave_n + i * 16 + g * 4, acc[i][j]);
+          store4<OUT>(a, t, wave_n + i * 16 + 16 + g * 4, acc[i + 1][j]);
+        } else {
+          store8(a, t, wave_n + i * 16 + g * 8, acc[i][j], acc[i + 1][j]);
+        }
       }
     }
+    // with all of them issued as one store each, the next wait can leave them behind
+    stored = a.wide_out && n0 + BN <= a.N && t0 + BT <= a.T;
   }
-#pragma unroll
-  for (int i = 0; i < NI; ++i)
-#pragma unroll
-    for (int j = 0; j < TI; ++j)
-      store4<OUT>(a, t0 + wt * (BT / WT) + j * 16 + col, n0 + wn * (BN / WN) + i * 16 + g * 4,
-                  acc[i][j]);
 }
 
 // Dynamic LDS above 64 KiB has to be asked for.
@@ -512,15 +642,19 @@ hipError_t launch_few_ks(const LinearArgs& a, hipStream_t st) {
   return launch_few<TT, 8, OUT>(a, st);
 }
 
-template <int BN, int BT, int WN, int WT, int OUT>
+template <int BN, int BT, int WN, int WT, int STAGES, int OUT>
 hipError_t launch_tile(const LinearArgs& a, hipStream_t st) {
-  const auto kernel = tile_kernel<BN, BT, WN, WT, OUT>;
-  const int lds = 2 * (BN + BT) * kBlock;
+  using S = Tile<BN, BT, WN, WT, STAGES, OUT>;
+  const auto kernel = tile_kernel<BN, BT, WN, WT, STAGES, OUT>;
+  const int lds = STAGES * S::kBuffer;
   const hipError_t e = allow_lds(kernel, lds);
   if (e != hipSuccess) return e;
   const int64_t tiles = int64_t((a.N + BN - 1) / BN) * ((a.T + BT - 1) / BT);
-  if (tiles > 0x7FFFFFFF) return hipErrorInvalidValue;
-  kernel<<<dim3(uint32_t(tiles)), WN * WT * 64, lds, st>>>(a);
+  if (tiles > 0x7FFFFFF) return hipErrorInvalidValue;
+  // as many workgroups as fit at once (a multiple of the 8 XCDs)
+  const int64_t slots = 256 * (kMaxLds / lds);
+  const int64_t grid = (tiles < slots ? tiles + 7 : slots) / 8 * 8;
+  kernel<<<dim3(uint32_t(grid)), S::kWaves * 64, lds, st>>>(a);
   return hipGetLastError();
 }
 
@@ -532,19 +666,24 @@ hipError_t launch(const LinearArgs& a, hipStream_t st) {
       return launch_ring<OUT>(a, st);
     return launch_few_ks<1, OUT>(a, st);
   }
-  if (a.T <= 32) return launch_few_ks<2, OUT>(a, st);
-  const int64_t big = int64_t((a.N + 255) / 256) * ((a.T + 255) / 256);
-  if (big >= 256) return launch_tile<256, 256, 2, 4, OUT>(a, st);
-  const int64_t mid = int64_t((a.N + 127) / 128) * ((a.T + 127) / 128);
-  if (mid >= 256) return launch_tile<128, 128, 2, 2, OUT>(a, st);
-  return launch_tile<64, 64, 2, 2, OUT>(a, st);
+  if (a.T <= 32 && a.N < 2048 * 16) return launch_few_ks<2, OUT>(a, st);
+  auto tiles = [&](int bn, int bt) {
+    return int64_t((a.N + bn - 1) / bn) * ((a.T + bt - 1) / bt);
+  };
+  if constexpr (OUT == MOE_W_BF16) {
+    if (tiles(256, 256) >= 256) return launch_tile<256, 256, 2, 4, 2, OUT>(a, st);
+  }
+  if (tiles(128, 128) >= 256) return launch_tile<128, 128, 2, 2, 2, OUT>(a, st);
+  if (tiles(64, 64) > 256) return launch_tile<64, 64, 2, 2, 4, OUT>(a, st);
+  return launch_tile<64, 64, 2, 2, 8, OUT>(a, st);
 }
 
 }  // namespace
 
 hipError_t launch_scaled_linear(LinearArgs a, hipStream_t st) {
   const int size = a.out_fmt == MOE_W_F32 ? 4 : 2;
-  a.wide_out = a.out_stride % 4 == 0 && (reinterpret_cast<uintptr_t>(a.out) % (4 * size)) == 0;
+  const int wide = 16 / size;      // outputs of a 16-byte store
+  a.wide_out = a.out_stride % wide == 0 && (reinterpret_cast<uintptr_t>(a.out) % 16) == 0;
   return a.out_fmt == MOE_W_F32 ? launch<MOE_W_F32>(a, st) : launch<MOE_W_BF16>(a, st);
 }
 
