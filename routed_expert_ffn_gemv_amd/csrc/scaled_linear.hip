@@ -404,9 +404,13 @@ __device__ __forceinline__ void store8(const LinearArgs& a, int t, int n, f32x4 
 // is moved out of range).  A row's 16-byte chunks are permuted in LDS by the
 // row, so that the rows a fragment reads together meet no bank twice.
 // fp32 outputs convert the codes to fp16 on their way from LDS.
-template <int BN, int BT, int WN, int WT, int STAGES, int OUT>
+//
+// KS > 1, for few tiles: KS groups of WN x WT waves take every KS-th block each,
+// with rings of their own, and their sums are joined in a fixed order at the
+// end (one tile per workgroup then).
+template <int BN, int BT, int WN, int WT, int STAGES, int KS, int OUT>
 struct Tile {
-  static constexpr int kWaves = WN * WT;
+  static constexpr int kWaves = WN * WT;                      // of one group
   static constexpr int NI = BN / WN / 16, TI = BT / WT / 16;
   static constexpr int kRows = BN + BT;                       // rows of one buffer, 128 bytes each
   static constexpr int kLoads = kRows / 8 / kWaves;           // 1 KiB loads per wave and block
@@ -428,12 +432,14 @@ __device__ __forceinline__ void barrier_lds() {
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
-template <int BN, int BT, int WN, int WT, int STAGES, int OUT>
-__global__ __launch_bounds__(WN* WT * 64) void tile_kernel(const LinearArgs a) {
-  using S = Tile<BN, BT, WN, WT, STAGES, OUT>;
+template <int BN, int BT, int WN, int WT, int STAGES, int KS, int OUT>
+__global__ __launch_bounds__(KS* WN* WT * 64) void tile_kernel(const LinearArgs a) {
+  using S = Tile<BN, BT, WN, WT, STAGES, KS, OUT>;
   constexpr int NI = S::NI, TI = S::TI, LOADS = S::kLoads, BUFFER = S::kBuffer;
-  extern __shared__ uint8_t lds[];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  extern __shared__ uint8_t all_lds[];
+  const int lane = threadIdx.x & 63, all_wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int group = all_wave / S::kWaves, wave = all_wave % S::kWaves;
+  uint8_t* lds = all_lds + group * (STAGES * BUFFER);
   const int col = lane & 15, g = lane >> 4;
   const int wn = wave % WN, wt = wave / WN;
   const int KB = (a.K + kBlock - 1) / kBlock;
@@ -464,7 +470,7 @@ __global__ __launch_bounds__(WN* WT * 64) void tile_kernel(const LinearArgs a) {
     off[i] = uint32_t(lane >> 3) * a.K + chunk * 16;
     off_last[i] = (KB - 1) * kBlock + chunk * 16 < a.K ? off[i] : 0x7FFFFFFFu;
   }
-  int load_id = first + int(blockIdx.x >> 3), load_kb = 0, load_buf = 0;
+  int load_id = first + int(blockIdx.x >> 3), load_kb = group, load_buf = 0;
   int under_way = 0;     // blocks loaded and not yet multiplied
   if (load_id >= last) return;
   __amdgpu_buffer_rsrc_t src;
@@ -479,7 +485,7 @@ __global__ __launch_bounds__(WN* WT * 64) void tile_kernel(const LinearArgs a) {
     scales = a.x_scale + int64_t(min(t0 + (wave * 64 + lane) % BT, a.T - 1)) * KB;
   };
   auto load = [&]() {
-    if (load_id >= last) return;
+    if (load_id >= last || (KS > 1 && load_kb >= KB)) return;
     uint8_t* dst = lds + load_buf * BUFFER;
     const bool whole = load_kb + 1 < KB;
 #pragma unroll
@@ -493,7 +499,8 @@ __global__ __launch_bounds__(WN* WT * 64) void tile_kernel(const LinearArgs a) {
           (__attribute__((address_space(3))) void*)(dst + S::kRows * kBlock + wave * 256), 4, 0, 0);
     load_buf = load_buf + 1 == STAGES ? 0 : load_buf + 1;
     ++under_way;
-    if (++load_kb == KB) {
+    load_kb += KS;
+    if (KS == 1 && load_kb == KB) {
       load_kb = 0;
       load_id += step;
       if (load_id < last) source();
@@ -523,9 +530,9 @@ __global__ __launch_bounds__(WN* WT * 64) void tile_kernel(const LinearArgs a) {
     for (int i = 0; i < NI; ++i)
 #pragma unroll
       for (int j = 0; j < TI; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    float ws = wsc[0];
+    float ws = wsc[min(group, KB - 1)];
 #pragma unroll 1
-    for (int kb = 0; kb < KB; ++kb) {
+    for (int kb = group; kb < KB + group; kb += KS) {   // (all groups take part in the barriers)
       // this block has arrived when no more than the later blocks' loads (and,
       // behind them, the last tile's stores) are outstanding
       if (under_way < STAGES - 1)
@@ -537,6 +544,7 @@ __global__ __launch_bounds__(WN* WT * 64) void tile_kernel(const LinearArgs a) {
       stored = false;
       --under_way;
       barrier_lds();
+      if (KS > 1 && kb >= KB) break;
       const uint8_t* now = lds + buf * BUFFER;
       auto wfrag = [&](int i) {
         const int r = weight_row<OUT>(i, col);
@@ -550,7 +558,7 @@ __global__ __launch_bounds__(WN* WT * 64) void tile_kernel(const LinearArgs a) {
         sc[j] = *reinterpret_cast<const float*>(now + s_at + j * 64) * ws;
       }
       load();      // into the buffer that every wave has left
-      ws = wsc[min(kb + 1, KB - 1)];
+      ws = wsc[min(kb + KS, KB - 1)];
       // the sums of group i - 1 join the accumulators while group i is multiplied
       f32x4 d[2][TI];
 #pragma unroll
@@ -581,6 +589,27 @@ __global__ __launch_bounds__(WN* WT * 64) void tile_kernel(const LinearArgs a) {
         for (int e = 0; e < 4; ++e)
           acc[NI - 1][j][e] = fmaf(d[(NI - 1) & 1][j][e], sc[j], acc[NI - 1][j][e]);
       buf = buf + 1 == STAGES ? 0 : buf + 1;
+    }
+    if constexpr (KS > 1) {
+      // groups 1 .. leave their sums in LDS, group 0 adds them in order
+      static_assert(STAGES * KS * BUFFER >= (KS - 1) * BN * BT * 4, "room for the sums");
+      f32x4* sums = reinterpret_cast<f32x4*>(all_lds);
+      __syncthreads();
+      if (group > 0) {
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+#pragma unroll
+          for (int j = 0; j < TI; ++j)
+            sums[(((group - 1) * S::kWaves + wave) * NI * TI + i * TI + j) * 64 + lane] = acc[i][j];
+      }
+      __syncthreads();
+      if (group > 0) return;
+      for (int k = 0; k + 1 < KS; ++k)
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+#pragma unroll
+          for (int j = 0; j < TI; ++j)
+            acc[i][j] += sums[((k * S::kWaves + wave) * NI * TI + i * TI + j) * 64 + lane];
     }
 #pragma unroll
     for (int j = 0; j < TI; ++j) {
@@ -642,19 +671,21 @@ hipError_t launch_few_ks(const LinearArgs& a, hipStream_t st) {
   return launch_few<TT, 8, OUT>(a, st);
 }
 
-template <int BN, int BT, int WN, int WT, int STAGES, int OUT>
+template <int BN, int BT, int WN, int WT, int STAGES, int KS, int OUT>
 hipError_t launch_tile(const LinearArgs& a, hipStream_t st) {
-  using S = Tile<BN, BT, WN, WT, STAGES, OUT>;
-  const auto kernel = tile_kernel<BN, BT, WN, WT, STAGES, OUT>;
-  const int lds = STAGES * S::kBuffer;
+  using S = Tile<BN, BT, WN, WT, STAGES, KS, OUT>;
+  const auto kernel = tile_kernel<BN, BT, WN, WT, STAGES, KS, OUT>;
+  const int lds = KS * STAGES * S::kBuffer;
+  static_assert(KS * STAGES * S::kBuffer <= kMaxLds, "LDS");
   const hipError_t e = allow_lds(kernel, lds);
   if (e != hipSuccess) return e;
   const int64_t tiles = int64_t((a.N + BN - 1) / BN) * ((a.T + BT - 1) / BT);
   if (tiles > 0x7FFFFFF) return hipErrorInvalidValue;
-  // as many workgroups as fit at once (a multiple of the 8 XCDs)
+  // as many workgroups as fit at once (a multiple of the 8 XCDs); with several
+  // groups of waves one for every tile
   const int64_t slots = 256 * (kMaxLds / lds);
-  const int64_t grid = (tiles < slots ? tiles + 7 : slots) / 8 * 8;
-  kernel<<<dim3(uint32_t(grid)), S::kWaves * 64, lds, st>>>(a);
+  const int64_t grid = (KS > 1 || tiles < slots ? tiles + 7 : slots) / 8 * 8;
+  kernel<<<dim3(uint32_t(grid)), KS * S::kWaves * 64, lds, st>>>(a);
   return hipGetLastError();
 }
 
@@ -670,12 +701,16 @@ hipError_t launch(const LinearArgs& a, hipStream_t st) {
   auto tiles = [&](int bn, int bt) {
     return int64_t((a.N + bn - 1) / bn) * ((a.T + bt - 1) / bt);
   };
-  if constexpr (OUT == MOE_W_BF16) {
-    if (tiles(256, 256) >= 256) return launch_tile<256, 256, 2, 4, 2, OUT>(a, st);
+  if (a.T > 64) {
+    if constexpr (OUT == MOE_W_BF16) {
+      if (tiles(256, 256) >= 256) return launch_tile<256, 256, 2, 4, 2, 1, OUT>(a, st);
+    }
+    if (tiles(128, 128) > 256) return launch_tile<128, 128, 2, 2, 2, 1, OUT>(a, st);
+    if (tiles(128, 128) > 128) return launch_tile<128, 128, 2, 2, 2, 2, OUT>(a, st);
   }
-  if (tiles(128, 128) >= 256) return launch_tile<128, 128, 2, 2, 2, OUT>(a, st);
-  if (tiles(64, 64) > 256) return launch_tile<64, 64, 2, 2, 4, OUT>(a, st);
-  return launch_tile<64, 64, 2, 2, 8, OUT>(a, st);
+  if (tiles(64, 64) > 512) return launch_tile<64, 64, 2, 2, 4, 1, OUT>(a, st);
+  if (tiles(64, 64) > 256) return launch_tile<64, 64, 2, 2, 2, 2, OUT>(a, st);
+  return launch_tile<64, 64, 2, 2, 2, 4, OUT>(a, st);
 }
 
 }  // namespace
