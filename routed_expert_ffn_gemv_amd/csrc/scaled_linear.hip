@@ -136,8 +136,7 @@ __device__ __forceinline__ u32x4 load16(const uint8_t* p) {
 
 // Blocks [s0, s0 + nb) of the tokens into LDS as fp16, [T][row_blocks * 128],
 // each row's 16-byte chunks permuted by the row (t & 7) so that 16 rows read
-// at one column meet no bank twice; and their scales, [nb][TT * 16].
-template <int TT>
+// at one column meet no bank twice; and their scales, [nb][16].
 __device__ __forceinline__ void stage_tokens(const LinearArgs& a, int s0, int nb, int row_blocks,
                                              uint8_t* xl, float* xs) {
   const int KB = (a.K + kBlock - 1) / kBlock;
@@ -163,36 +162,32 @@ __device__ __forceinline__ void stage_tokens(const LinearArgs& a, int s0, int nb
     }
   }
 #pragma unroll 1
-  for (int i = threadIdx.x; i < TT * 16 * nb; i += step) {
+  for (int i = threadIdx.x; i < 16 * nb; i += step) {
     const int t = i / nb, b = i % nb;
-    xs[b * (TT * 16) + t] = t < a.T ? a.x_scale[int64_t(t) * KB + s0 + b] : 0.0f;
+    xs[b * 16 + t] = t < a.T ? a.x_scale[int64_t(t) * KB + s0 + b] : 0.0f;
   }
 }
 
 // One block of 16 weight rows (this lane's two chunks) times the staged tokens.
-template <int TT>
 __device__ __forceinline__ void add_block(const LinearArgs& a, u32x4 wlo, u32x4 whi, float ws, int b,
                                           int row_blocks, const uint8_t* xl, const float* xs,
-                                          f32x4 (&acc)[TT]) {
+                                          f32x4& acc) {
   const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
   const Half16 lo = to_f16(wlo), hi = to_f16(whi);
+  const int t = min(col, a.T - 1);     // columns past T are not stored
+  const uint8_t* p = xl + int64_t(t) * row_blocks * (kBlock * 2);
+  const int c = b * 16 + 2 * g;
+  auto x = [&](int chunk) {
+    return *reinterpret_cast<const f16x8*>(p + ((chunk ^ (t & 7)) * 16));
+  };
+  f32x4 d = {0.0f, 0.0f, 0.0f, 0.0f};
+  d = mfma_f16(lo.lo, x(c), d);
+  d = mfma_f16(lo.hi, x(c + 1), d);
+  d = mfma_f16(hi.lo, x(c + 8), d);
+  d = mfma_f16(hi.hi, x(c + 9), d);
+  const float sc = xs[b * 16 + col] * ws;
 #pragma unroll
-  for (int m = 0; m < TT; ++m) {
-    const int t = min(m * 16 + col, a.T - 1);     // columns past T are not stored
-    const uint8_t* p = xl + int64_t(t) * row_blocks * (kBlock * 2);
-    const int c = b * 16 + 2 * g;
-    auto x = [&](int chunk) {
-      return *reinterpret_cast<const f16x8*>(p + ((chunk ^ (t & 7)) * 16));
-    };
-    f32x4 d = {0.0f, 0.0f, 0.0f, 0.0f};
-    d = mfma_f16(lo.lo, x(c), d);
-    d = mfma_f16(lo.hi, x(c + 1), d);
-    d = mfma_f16(hi.lo, x(c + 8), d);
-    d = mfma_f16(hi.hi, x(c + 9), d);
-    const float sc = xs[b * (TT * 16) + m * 16 + col] * ws;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) acc[m][i] = fmaf(d[i], sc, acc[m][i]);
-  }
+  for (int i = 0; i < 4; ++i) acc[i] = fmaf(d[i], sc, acc[i]);
 }
 
 // Many weight rows: one workgroup per CU stays and its waves walk over tiles
@@ -267,13 +262,13 @@ __global__ __launch_bounds__(kRingWaves * 64) void ring_kernel(const LinearArgs 
     if (++ls == steps) ls = 0, lt += stride;
   };
   load();
-  stage_tokens<1>(a, 0, KB, row_blocks, xl, xs);
+  stage_tokens(a, 0, KB, row_blocks, xl, xs);
   __syncthreads();
 
   int slot = 0, buf = 0;
 #pragma unroll 1
   for (int tile = int(blockIdx.x) * kRingWaves + wave; tile < tiles; tile += stride) {
-    f32x4 acc[1] = {{0.0f, 0.0f, 0.0f, 0.0f}};
+    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 1
     for (int st = 0; st < steps; ++st) {
       wait_loads();         // this slot has arrived, and the tile's scales before it
@@ -289,20 +284,20 @@ __global__ __launch_bounds__(kRingWaves * 64) void ring_kernel(const LinearArgs 
           if (kb * kBlock + g * 16 >= a.K) lo = u32x4{0u, 0u, 0u, 0u};
           if (kb * kBlock + g * 16 + 64 >= a.K) hi = u32x4{0u, 0u, 0u, 0u};
         }
-        add_block<1>(a, lo, hi, wsl[buf * scales + kb], kb, row_blocks, xl, xs, acc);
+        add_block(a, lo, hi, wsl[buf * scales + kb], kb, row_blocks, xl, xs, acc);
       }
       slot ^= 1;
     }
     buf ^= 1;
-    store4<OUT>(a, col, tile * 16 + g * 4, acc[0]);
+    store4<OUT>(a, col, tile * 16 + g * 4, acc);
   }
 }
 
 // Fewer weight rows: KS waves share a tile of 16 rows and split its blocks;
-// their sums are joined in a fixed order.  TT groups of 16 tokens.
+// their sums are joined in a fixed order.
 constexpr int kFewGroup = 4;     // blocks of a tile in flight per wave
 
-template <int TT, int KS, int OUT>
+template <int KS, int OUT>
 __global__ __launch_bounds__(KS * 64) void few_kernel(const LinearArgs a) {
   extern __shared__ uint8_t lds[];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -314,9 +309,7 @@ __global__ __launch_bounds__(KS * 64) void few_kernel(const LinearArgs a) {
   const int seg = a.seg_blocks;                 // blocks of K staged at a time
   uint8_t* xl = lds;
   float* xs = reinterpret_cast<float*>(lds + size_t(a.T) * seg * kBlock * 2);
-  f32x4 acc[TT];
-#pragma unroll
-  for (int m = 0; m < TT; ++m) acc[m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
 
   struct Piece {
     u32x4 lo, hi;
@@ -342,7 +335,7 @@ __global__ __launch_bounds__(KS * 64) void few_kernel(const LinearArgs a) {
     for (int u = 0; u < kFewGroup; ++u)
       if (b0 + u < b1) w[u] = load_w(s0 + b0 + u);
     if (s0) __syncthreads();
-    stage_tokens<TT>(a, s0, nb, seg, xl, xs);
+    stage_tokens(a, s0, nb, seg, xl, xs);
     __syncthreads();
 #pragma unroll 1
     for (int b = b0; b < b1; b += kFewGroup) {
@@ -351,21 +344,18 @@ __global__ __launch_bounds__(KS * 64) void few_kernel(const LinearArgs a) {
         if (b + u < b1) {
           const Piece cur = w[u];
           if (b + u + kFewGroup < b1) w[u] = load_w(s0 + b + u + kFewGroup);
-          add_block<TT>(a, cur.lo, cur.hi, cur.scale, b + u, seg, xl, xs, acc);
+          add_block(a, cur.lo, cur.hi, cur.scale, b + u, seg, xl, xs, acc);
         }
       }
     }
   }
   __syncthreads();
-  f32x4* part = reinterpret_cast<f32x4*>(lds);     // [KS][TT][64]
-#pragma unroll
-  for (int m = 0; m < TT; ++m) part[(wave * TT + m) * 64 + lane] = acc[m];
+  f32x4* part = reinterpret_cast<f32x4*>(lds);     // [KS][64]
+  part[wave * 64 + lane] = acc;
   __syncthreads();
-  for (int m = wave; m < TT; m += KS) {
-    f32x4 v = part[m * 64 + lane];
-    for (int k = 1; k < KS; ++k) v += part[(k * TT + m) * 64 + lane];
-    store4<OUT>(a, m * 16 + col, n0 + g * 4, v);
-  }
+  if (wave > 0) return;
+  for (int k = 1; k < KS; ++k) acc += part[k * 64 + lane];
+  store4<OUT>(a, col, n0 + g * 4, acc);
 }
 
 // ---- many tokens
@@ -629,6 +619,119 @@ __global__ __launch_bounds__(KS* WN* WT * 64) void tile_kernel(const LinearArgs 
   }
 }
 
+// ---- between: outputs too few to fill the chip with tiles
+
+// A workgroup owns 32 weight rows and 32 tokens, and its eight waves split
+// the blocks: each loads its own blocks straight into registers, the next
+// while it multiplies one, and waits for nobody until the sums are joined, in
+// a fixed order, through LDS.  Latency-bound: 64 x 2048 x 2048 takes 7.4 us,
+// 9.5 us as tiles through LDS; with more outputs the loads of every wave for
+// itself cost more than the waits (256 x 2048 x 2048: 12.6 and 9.9 us).
+template <int OUT>
+__global__ __launch_bounds__(512) void direct_kernel(const LinearArgs a) {
+  constexpr int NI = 2, TI = 2, KS = 8;
+  __shared__ f32x4 sums[KS][NI * TI][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int col = lane & 15, g = lane >> 4;
+  const int KB = (a.K + kBlock - 1) / kBlock;
+  const int tiles_n = (a.N + NI * 16 - 1) / (NI * 16);
+  const int n0 = int(blockIdx.x) % tiles_n * (NI * 16), t0 = int(blockIdx.x) / tiles_n * (TI * 16);
+  const uint8_t* wbase = a.w8 + int64_t(n0) * a.K;
+  const uint8_t* xbase = a.x8 + int64_t(t0) * a.K;
+  const float* sbase = a.x_scale + int64_t(t0) * KB;
+  const float* wsc = a.w_scale + int64_t(n0 / kBlock) * KB;
+  uint32_t woff[NI], xoff[TI], soff[TI];     // rows past the ends repeat the last one
+#pragma unroll
+  for (int i = 0; i < NI; ++i)
+    woff[i] = uint32_t(min(i * 16 + col, a.N - 1 - n0)) * a.K + g * 16;
+#pragma unroll
+  for (int j = 0; j < TI; ++j) {
+    const int r = min(j * 16 + col, a.T - 1 - t0);
+    xoff[j] = uint32_t(r) * a.K + g * 16;
+    soff[j] = uint32_t(r) * KB;
+  }
+  struct Raw {
+    u32x4 w[NI][2], x[TI][2];
+    float xs[TI], ws;
+  };
+  auto load = [&](Raw& q, int kb) {
+    const int k = kb * kBlock;
+    if (k + kBlock <= a.K) {
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+        q.w[i][0] = load16(wbase + k + woff[i]), q.w[i][1] = load16(wbase + k + 64 + woff[i]);
+#pragma unroll
+      for (int j = 0; j < TI; ++j)
+        q.x[j][0] = load16(xbase + k + xoff[j]), q.x[j][1] = load16(xbase + k + 64 + xoff[j]);
+    } else {
+      // the last, shorter block: zeros past the row's end
+      const u32x4 zero = {0u, 0u, 0u, 0u};
+      const bool lo = k + g * 16 < a.K, hi = k + g * 16 + 64 < a.K;
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        q.w[i][0] = q.w[i][1] = zero;
+        if (lo) q.w[i][0] = load16(wbase + k + woff[i]);
+        if (hi) q.w[i][1] = load16(wbase + k + 64 + woff[i]);
+      }
+#pragma unroll
+      for (int j = 0; j < TI; ++j) {
+        q.x[j][0] = q.x[j][1] = zero;
+        if (lo) q.x[j][0] = load16(xbase + k + xoff[j]);
+        if (hi) q.x[j][1] = load16(xbase + k + 64 + xoff[j]);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < TI; ++j) q.xs[j] = sbase[soff[j] + kb];
+    q.ws = wsc[kb];
+  };
+  f32x4 acc[NI][TI];
+#pragma unroll
+  for (int i = 0; i < NI; ++i)
+#pragma unroll
+    for (int j = 0; j < TI; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  using Frag = std::conditional_t<OUT == MOE_W_F32, Frag16, Frag8>;
+  auto add = [&](const Raw& q) {
+    Frag x[TI];
+    float sc[TI];
+#pragma unroll
+    for (int j = 0; j < TI; ++j) x[j] = Frag(q.x[j][0], q.x[j][1]), sc[j] = q.xs[j] * q.ws;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const Frag w(q.w[i][0], q.w[i][1]);
+      f32x4 d[TI];
+#pragma unroll
+      for (int j = 0; j < TI; ++j) d[j] = product(w, x[j]);
+#pragma unroll
+      for (int j = 0; j < TI; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(d[j][e], sc[j], acc[i][j][e]);
+    }
+  };
+  Raw q[2];
+  if (wave < KB) load(q[0], wave);
+#pragma unroll 1
+  for (int kb = wave; kb < KB; kb += 2 * KS) {
+    if (kb + KS < KB) load(q[1], kb + KS);
+    add(q[0]);
+    if (kb + KS >= KB) break;
+    if (kb + 2 * KS < KB) load(q[0], kb + 2 * KS);
+    add(q[1]);
+  }
+  // every wave adds up its share of the groups of 16 x 16, waves in order
+#pragma unroll
+  for (int i = 0; i < NI; ++i)
+#pragma unroll
+    for (int j = 0; j < TI; ++j) sums[wave][i * TI + j][lane] = acc[i][j];
+  __syncthreads();
+#pragma unroll
+  for (int m = wave; m < NI * TI; m += KS) {
+    f32x4 v = sums[0][m][lane];
+#pragma unroll
+    for (int k = 1; k < KS; ++k) v += sums[k][m][lane];
+    store4<OUT>(a, t0 + m % TI * 16 + col, n0 + m / TI * 16 + g * 4, v);
+  }
+}
+
 // Dynamic LDS above 64 KiB has to be asked for.
 template <class Kernel>
 hipError_t allow_lds(Kernel kernel, int64_t bytes) {
@@ -639,15 +742,15 @@ hipError_t allow_lds(Kernel kernel, int64_t bytes) {
 
 constexpr int kFewLds = 128 * 1024;   // LDS for staged tokens
 
-template <int TT, int KS, int OUT>
+template <int KS, int OUT>
 hipError_t launch_few(LinearArgs a, hipStream_t st) {
   const int KB = (a.K + kBlock - 1) / kBlock;
-  const int per_block = a.T * kBlock * 2 + TT * 16 * 4;
+  const int per_block = a.T * kBlock * 2 + 16 * 4;
   const int fit = kFewLds / per_block;
   a.seg_blocks = KB < fit ? KB : fit;
   int64_t lds = int64_t(a.seg_blocks) * per_block;
-  if (lds < KS * TT * 1024) lds = KS * TT * 1024;
-  const auto kernel = few_kernel<TT, KS, OUT>;
+  if (lds < KS * 1024) lds = KS * 1024;
+  const auto kernel = few_kernel<KS, OUT>;
   const hipError_t e = allow_lds(kernel, lds);
   if (e != hipSuccess) return e;
   kernel<<<(a.N + 15) / 16, KS * 64, lds, st>>>(a);
@@ -662,13 +765,6 @@ hipError_t launch_ring(const LinearArgs& a, hipStream_t st) {
   const int groups = ((a.N + 15) / 16 + kRingWaves - 1) / kRingWaves;
   ring_kernel<OUT><<<groups < 256 ? groups : 256, kRingWaves * 64, lds, st>>>(a);
   return hipGetLastError();
-}
-
-template <int TT, int OUT>
-hipError_t launch_few_ks(const LinearArgs& a, hipStream_t st) {
-  const int tiles = (a.N + 15) / 16;
-  if (tiles >= 256) return launch_few<TT, 4, OUT>(a, st);
-  return launch_few<TT, 8, OUT>(a, st);
 }
 
 template <int BN, int BT, int WN, int WT, int STAGES, int KS, int OUT>
@@ -690,17 +786,25 @@ hipError_t launch_tile(const LinearArgs& a, hipStream_t st) {
 }
 
 template <int OUT>
+hipError_t launch_direct(const LinearArgs& a, hipStream_t st) {
+  const int tiles = ((a.N + 31) / 32) * ((a.T + 31) / 32);
+  direct_kernel<OUT><<<tiles, 512, 0, st>>>(a);
+  return hipGetLastError();
+}
+
+template <int OUT>
 hipError_t launch(const LinearArgs& a, hipStream_t st) {
   if (a.T <= 16) {
     // enough tiles for every wave of the chip, and tokens that fit LDS
     if (a.N >= 2048 * 16 && ring_lds(a.T, (a.K + kBlock - 1) / kBlock) <= kMaxLds)
       return launch_ring<OUT>(a, st);
-    return launch_few_ks<1, OUT>(a, st);
+    if (a.N >= 256 * 16) return launch_few<4, OUT>(a, st);
+    return launch_few<8, OUT>(a, st);
   }
-  if (a.T <= 32 && a.N < 2048 * 16) return launch_few_ks<2, OUT>(a, st);
   auto tiles = [&](int bn, int bt) {
     return int64_t((a.N + bn - 1) / bn) * ((a.T + bt - 1) / bt);
   };
+  if (tiles(32, 32) <= 160) return launch_direct<OUT>(a, st);
   if (a.T > 64) {
     if constexpr (OUT == MOE_W_BF16) {
       if (tiles(256, 256) >= 256) return launch_tile<256, 256, 2, 4, 2, 1, OUT>(a, st);
