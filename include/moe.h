@@ -409,7 +409,7 @@ moe_status moe_add_rmsnorm(int32_t T, int32_t H, const void* y, int32_t y_fmt, i
  * Codes are OCP e4m3 (no infinities; a NaN code makes the sums it enters
  * NaN), scales fp32, all contiguous.  out is MOE_W_F32 or MOE_W_BF16 (rounded
  * once), out_stride elements from row to row (>= N).  Sums are fp32; for
- * bf16 outputs of more than 32 tokens the hardware's 8-bit products are used,
+ * bf16 outputs of more than 16 tokens the hardware's 8-bit products are used,
  * which add eight neighbouring ones with 13 bits below the largest of them.
  * x8 and w8 16-byte aligned, K a multiple of 16, else MOE_ERR_INVALID; N and
  * T are arbitrary.  The order of the sums depends on (T, N, K) alone: calls

@@ -151,7 +151,6 @@ struct LinearArgs {
   int T, N, K, out_fmt;
   int64_t out_stride;
   bool wide_out;               // rows allow 16-byte stores (set by the launcher)
-  int seg_blocks;              // blocks of K staged at a time (set by the launcher)
 };
 hipError_t launch_scaled_linear(LinearArgs a, hipStream_t st);
 

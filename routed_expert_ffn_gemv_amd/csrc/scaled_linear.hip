@@ -6,9 +6,9 @@
 // 13 bits below the largest of them (measured: truncated towards zero; the
 // sums of eight then join with fp32's bits), a relative error of 1.5e-5 of a
 // product of normal values.  That is far below bf16's rounding and far above
-// fp32's.  So fp32 outputs, and every call with few tokens, use the 16-bit
+// fp32's.  So fp32 outputs, and all of up to 16 tokens, use the 16-bit
 // matrix instructions on codes converted to fp16 (exact, as are the products
-// in fp32; relative error 1e-8 per block), and bf16 outputs of many tokens
+// in fp32; relative error 1e-8 per block), and bf16 outputs of more tokens
 // the 8-bit ones.
 //
 // Operand order: the weight rows are the instruction's rows and the tokens
@@ -20,9 +20,9 @@
 // a block does not matter as long as both sides agree, and a wave's load then
 // covers 64 consecutive bytes of each row.
 //
-// Few tokens: every weight row is read once, straight from HBM into
-// registers; the tokens sit in LDS.  Many tokens: tiles of both operands go
-// through LDS.
+// ring_kernel: few tokens, many weight rows; every row is streamed once, the
+// tokens stay in LDS.  direct_kernel: few outputs; operands straight into
+// registers.  tile_kernel: the rest; tiles of both operands through LDS.
 
 #include <hip/hip_runtime.h>
 
@@ -134,20 +134,20 @@ __device__ __forceinline__ u32x4 load16(const uint8_t* p) {
   return *reinterpret_cast<const u32x4*>(p);
 }
 
-// Blocks [s0, s0 + nb) of the tokens into LDS as fp16, [T][row_blocks * 128],
-// each row's 16-byte chunks permuted by the row (t & 7) so that 16 rows read
-// at one column meet no bank twice; and their scales, [nb][16].
-__device__ __forceinline__ void stage_tokens(const LinearArgs& a, int s0, int nb, int row_blocks,
-                                             uint8_t* xl, float* xs) {
+// The tokens into LDS as fp16, [T][row_blocks * 128], each row's 16-byte
+// chunks permuted by the row (t & 7) so that 16 rows read at one column meet
+// no bank twice; and their scales, [KB][16].
+__device__ __forceinline__ void stage_tokens(const LinearArgs& a, int row_blocks, uint8_t* xl,
+                                             float* xs) {
   const int KB = (a.K + kBlock - 1) / kBlock;
-  const int chunks = nb * 8;                    // 16 codes each: two chunks of fp16
+  const int chunks = KB * 8;                    // 16 codes each: two chunks of fp16
   const int all = a.T * chunks, step = int(blockDim.x);
 #pragma unroll 1
   for (int i0 = threadIdx.x; i0 < all; i0 += 4 * step) {
     u32x4 v[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int i = i0 + j * step, t = i / chunks, k = s0 * kBlock + i % chunks * 16;
+      const int i = i0 + j * step, t = i / chunks, k = i % chunks * 16;
       v[j] = u32x4{0u, 0u, 0u, 0u};
       if (i < all && k < a.K) v[j] = load16(a.x8 + int64_t(t) * a.K + k);
     }
@@ -162,9 +162,9 @@ __device__ __forceinline__ void stage_tokens(const LinearArgs& a, int s0, int nb
     }
   }
 #pragma unroll 1
-  for (int i = threadIdx.x; i < 16 * nb; i += step) {
-    const int t = i / nb, b = i % nb;
-    xs[b * 16 + t] = t < a.T ? a.x_scale[int64_t(t) * KB + s0 + b] : 0.0f;
+  for (int i = threadIdx.x; i < 16 * KB; i += step) {
+    const int t = i / KB, b = i % KB;
+    xs[b * 16 + t] = t < a.T ? a.x_scale[int64_t(t) * KB + b] : 0.0f;
   }
 }
 
@@ -262,7 +262,7 @@ __global__ __launch_bounds__(kRingWaves * 64) void ring_kernel(const LinearArgs 
     if (++ls == steps) ls = 0, lt += stride;
   };
   load();
-  stage_tokens(a, 0, KB, row_blocks, xl, xs);
+  stage_tokens(a, row_blocks, xl, xs);
   __syncthreads();
 
   int slot = 0, buf = 0;
@@ -291,71 +291,6 @@ __global__ __launch_bounds__(kRingWaves * 64) void ring_kernel(const LinearArgs 
     buf ^= 1;
     store4<OUT>(a, col, tile * 16 + g * 4, acc);
   }
-}
-
-// Fewer weight rows: KS waves share a tile of 16 rows and split its blocks;
-// their sums are joined in a fixed order.
-constexpr int kFewGroup = 4;     // blocks of a tile in flight per wave
-
-template <int KS, int OUT>
-__global__ __launch_bounds__(KS * 64) void few_kernel(const LinearArgs a) {
-  extern __shared__ uint8_t lds[];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int col = lane & 15, g = lane >> 4;
-  const int KB = (a.K + kBlock - 1) / kBlock;
-  const int n0 = int(blockIdx.x) * 16;
-  const uint8_t* wrow = a.w8 + int64_t(min(n0 + col, a.N - 1)) * a.K;
-  const float* wsc = a.w_scale + int64_t(n0 / kBlock) * KB;
-  const int seg = a.seg_blocks;                 // blocks of K staged at a time
-  uint8_t* xl = lds;
-  float* xs = reinterpret_cast<float*>(lds + size_t(a.T) * seg * kBlock * 2);
-  f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-
-  struct Piece {
-    u32x4 lo, hi;
-    float scale;
-  };
-  auto load_w = [&](int kb) {
-    const int c = kb * kBlock + g * 16;
-    Piece p;
-    p.lo = p.hi = u32x4{0u, 0u, 0u, 0u};
-    if (c < a.K) p.lo = load16(wrow + c);
-    if (c + 64 < a.K) p.hi = load16(wrow + c + 64);
-    p.scale = wsc[kb];
-    return p;
-  };
-#pragma unroll 1
-  for (int s0 = 0; s0 < KB; s0 += seg) {
-    const int nb = min(seg, KB - s0);
-    // this wave's blocks of the segment; the first are under way before the tokens
-    const int per = (nb + KS - 1) / KS;
-    const int b0 = wave * per, b1 = min(nb, b0 + per);
-    Piece w[kFewGroup];
-#pragma unroll
-    for (int u = 0; u < kFewGroup; ++u)
-      if (b0 + u < b1) w[u] = load_w(s0 + b0 + u);
-    if (s0) __syncthreads();
-    stage_tokens(a, s0, nb, seg, xl, xs);
-    __syncthreads();
-#pragma unroll 1
-    for (int b = b0; b < b1; b += kFewGroup) {
-#pragma unroll
-      for (int u = 0; u < kFewGroup; ++u) {
-        if (b + u < b1) {
-          const Piece cur = w[u];
-          if (b + u + kFewGroup < b1) w[u] = load_w(s0 + b + u + kFewGroup);
-          add_block(a, cur.lo, cur.hi, cur.scale, b + u, seg, xl, xs, acc);
-        }
-      }
-    }
-  }
-  __syncthreads();
-  f32x4* part = reinterpret_cast<f32x4*>(lds);     // [KS][64]
-  part[wave * 64 + lane] = acc;
-  __syncthreads();
-  if (wave > 0) return;
-  for (int k = 1; k < KS; ++k) acc += part[k * 64 + lane];
-  store4<OUT>(a, col, n0 + g * 4, acc);
 }
 
 // ---- many tokens
@@ -619,17 +554,18 @@ __global__ __launch_bounds__(KS* WN* WT * 64) void tile_kernel(const LinearArgs 
   }
 }
 
-// ---- between: outputs too few to fill the chip with tiles
+// ---- few outputs
 
-// A workgroup owns 32 weight rows and 32 tokens, and its eight waves split
-// the blocks: each loads its own blocks straight into registers, the next
-// while it multiplies one, and waits for nobody until the sums are joined, in
-// a fixed order, through LDS.  Latency-bound: 64 x 2048 x 2048 takes 7.4 us,
-// 9.5 us as tiles through LDS; with more outputs the loads of every wave for
-// itself cost more than the waits (256 x 2048 x 2048: 12.6 and 9.9 us).
-template <int OUT>
-__global__ __launch_bounds__(512) void direct_kernel(const LinearArgs a) {
-  constexpr int NI = 2, TI = 2, KS = 8;
+// A workgroup owns NI x 16 weight rows and TI x 16 tokens, and its KS waves
+// split the blocks: each loads its own blocks straight into registers, the
+// next while it multiplies one, and waits for nobody until the sums are
+// joined, in a fixed order, through LDS.  Latency-bound: 1 x 2048 x 2048 takes
+// 3.9 us, 64 x 2048 x 2048 7.4 us (as tiles through LDS 9.1 and 9.5).  With
+// more outputs the loads of every wave for itself cost more than the waits
+// (256 x 2048 x 2048: 12.6 us, 9.9 as tiles); up to 16 tokens the bound is
+// the weights' way from HBM (16 x 16,384 x 4096: 15.8 us, 4.3 TB/s).
+template <int NI, int TI, int KS, int OUT>
+__global__ __launch_bounds__(KS * 64) void direct_kernel(const LinearArgs a) {
   __shared__ f32x4 sums[KS][NI * TI][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, g = lane >> 4;
@@ -689,7 +625,7 @@ __global__ __launch_bounds__(512) void direct_kernel(const LinearArgs a) {
   for (int i = 0; i < NI; ++i)
 #pragma unroll
     for (int j = 0; j < TI; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  using Frag = std::conditional_t<OUT == MOE_W_F32, Frag16, Frag8>;
+  using Frag = std::conditional_t<OUT == MOE_W_F32 || TI == 1, Frag16, Frag8>;
   auto add = [&](const Raw& q) {
     Frag x[TI];
     float sc[TI];
@@ -740,23 +676,6 @@ hipError_t allow_lds(Kernel kernel, int64_t bytes) {
                              hipFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
 }
 
-constexpr int kFewLds = 128 * 1024;   // LDS for staged tokens
-
-template <int KS, int OUT>
-hipError_t launch_few(LinearArgs a, hipStream_t st) {
-  const int KB = (a.K + kBlock - 1) / kBlock;
-  const int per_block = a.T * kBlock * 2 + 16 * 4;
-  const int fit = kFewLds / per_block;
-  a.seg_blocks = KB < fit ? KB : fit;
-  int64_t lds = int64_t(a.seg_blocks) * per_block;
-  if (lds < KS * 1024) lds = KS * 1024;
-  const auto kernel = few_kernel<KS, OUT>;
-  const hipError_t e = allow_lds(kernel, lds);
-  if (e != hipSuccess) return e;
-  kernel<<<(a.N + 15) / 16, KS * 64, lds, st>>>(a);
-  return hipGetLastError();
-}
-
 template <int OUT>
 hipError_t launch_ring(const LinearArgs& a, hipStream_t st) {
   const int64_t lds = ring_lds(a.T, (a.K + kBlock - 1) / kBlock);
@@ -785,10 +704,10 @@ hipError_t launch_tile(const LinearArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
-template <int OUT>
+template <int NI, int TI, int KS, int OUT>
 hipError_t launch_direct(const LinearArgs& a, hipStream_t st) {
-  const int tiles = ((a.N + 31) / 32) * ((a.T + 31) / 32);
-  direct_kernel<OUT><<<tiles, 512, 0, st>>>(a);
+  const int tiles = ((a.N + NI * 16 - 1) / (NI * 16)) * ((a.T + TI * 16 - 1) / (TI * 16));
+  direct_kernel<NI, TI, KS, OUT><<<tiles, KS * 64, 0, st>>>(a);
   return hipGetLastError();
 }
 
@@ -798,13 +717,13 @@ hipError_t launch(const LinearArgs& a, hipStream_t st) {
     // enough tiles for every wave of the chip, and tokens that fit LDS
     if (a.N >= 2048 * 16 && ring_lds(a.T, (a.K + kBlock - 1) / kBlock) <= kMaxLds)
       return launch_ring<OUT>(a, st);
-    if (a.N >= 256 * 16) return launch_few<4, OUT>(a, st);
-    return launch_few<8, OUT>(a, st);
+    if (a.N >= 512 * 32) return launch_direct<2, 1, 4, OUT>(a, st);
+    return launch_direct<1, 1, 8, OUT>(a, st);
   }
   auto tiles = [&](int bn, int bt) {
     return int64_t((a.N + bn - 1) / bn) * ((a.T + bt - 1) / bt);
   };
-  if (tiles(32, 32) <= 160) return launch_direct<OUT>(a, st);
+  if (tiles(32, 32) <= 160) return launch_direct<2, 2, 8, OUT>(a, st);
   if (a.T > 64) {
     if constexpr (OUT == MOE_W_BF16) {
       if (tiles(256, 256) >= 256) return launch_tile<256, 256, 2, 4, 2, 1, OUT>(a, st);

@@ -6,7 +6,7 @@ roundings of at most 2^-24 of the block's share of A, in any order; a
 truncating adder doubles that), the scale's product rounds once, and the
 blocks' sums join with one rounding each: (256 + 2 + K/128 + 1) * 2^-24 * A.
 bf16 outputs add the half step 2^-8 of the value and, where the 8-bit matrix
-instructions sum (more than 32 tokens), their adder's truncation: seven of
+instructions sum (more than 16 tokens), their adder's truncation: seven of
 every eight neighbouring products lose less than 2^-13 of the largest of the
 eight, 7 * 2^-13 * A at most."""
 
@@ -58,7 +58,7 @@ def _check(x8, xs, w8, ws, dtype=torch.float32, **kw):
     want, mag = around.scaled_linear(x8, xs, w8, ws)
     tol = (259 + x8.shape[1] / 128) * 2.0 ** -24 * mag
     if dtype == torch.bfloat16:
-        if x8.shape[0] > 32:
+        if x8.shape[0] > 16:
             tol = tol + 7 * 2.0 ** -13 * mag
         tol = tol + 2.0 ** -8 * (np.abs(want) + tol)
     bad = np.abs(got - want) > tol
@@ -101,6 +101,18 @@ def test_large(T, N):
 def test_formats_strides_and_alignment(dtype, pad, off):
     for T, N in ((4, 260), (90, 258)):
         _check(*_inputs(T, N, 640, 7), dtype=dtype, pad=pad, off=off)
+
+
+@pytest.mark.parametrize("T,N,K", [(16, 17000, 304), (7, 9000, 1008), (16, 33000, 8192 + 272), (2, 32768, 8448)])
+def test_streamed_rows(T, N, K):
+    """Many weight rows and few tokens, long rows too; 600 of the rows are
+    compared, the last ones among them."""
+    x8, xs, w8, ws = _inputs(T, N, K, N + K)
+    got = _run(x8, xs, w8, ws, torch.float32, pad=4)
+    for n0 in (0, N // 256 * 128, (N - 300) // 128 * 128):
+        rows = slice(n0, min(n0 + 300, N))
+        want, mag = around.scaled_linear(x8, xs, w8[rows], ws[n0 // 128:])
+        assert (np.abs(got[:, rows] - want) <= (259 + K / 128) * 2.0 ** -24 * mag).all()
 
 
 def test_ordinary_values():
