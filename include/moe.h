@@ -441,9 +441,10 @@ moe_status moe_scaled_linear(const uint8_t* x8, const float* x_scale, int32_t T,
  * temperature, top_k, top_p, min_p: device arrays [T], each may be NULL: 1, 0,
  * 1, 0.  top_k <= 0, top_p >= 1 (or NaN) and min_p <= 0 (or NaN) filter
  * nothing; infinite temperatures make every token that is left equal; equal
- * +infinity logits share the draw.  w is computed in 64 bits and held to
- * 2^-s, s = min(52, 61 - ceil(log2 V)); weights that round to zero are not
- * drawn.  Sums are exact: results do not depend on T, on the other rows or on
+ * +infinity logits share the draw.  w is held to 2^-(6 + f) of itself, f =
+ * min(28, 63 - 2 ceil(log2 V)) (2^-33 for 151,936 tokens); tokens more than 42
+ * temperatures below the largest logit (w < 6e-19) are not drawn.  Sums are
+ * exact from there on: results do not depend on T, on the other rows or on
  * the run.  tokens [T] int32.  Limits: 1 <= V <= 2^26, T <= 16384.  ws:
  * moe_sample_workspace_size bytes, 256-byte aligned, in use by one call at a
  * time. */

@@ -136,7 +136,7 @@ struct SampleArgs {
   const int32_t* draft;        // [T - 1], with n_out
   int32_t* n_out;              // null: no acceptance
   void* ws;
-  int parts, shift;            // set by launch_sample
+  int parts, shift, frac_bits, q_bits;   // set by launch_sample
 };
 size_t sample_ws(int T);
 hipError_t launch_sample(SampleArgs a, hipStream_t st);
