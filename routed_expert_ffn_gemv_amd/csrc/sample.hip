@@ -109,40 +109,65 @@ struct RowView {
     if (FMT == MOE_W_F32) return reinterpret_cast<const float*>(base)[lead + int64_t(i)];
     return bf16_to_f32(reinterpret_cast<const uint16_t*>(base)[lead + int64_t(i)]);
   }
-  // vector i's logits into x, those outside the row as -infinity
-  __device__ void load(int i, float* x) const {
+  // vector i's 16 bytes, elements outside the row as -infinity
+  __device__ u32x4 load(int i) const {
     const int e = i * kVec<FMT> - lead;
-    if (e >= 0 && e + kVec<FMT> <= V) {
-      const u32x4 q = *reinterpret_cast<const u32x4*>(base + int64_t(i) * 16);
+    if (e >= 0 && e + kVec<FMT> <= V) return *reinterpret_cast<const u32x4*>(base + int64_t(i) * 16);
+    u32x4 q;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (FMT == MOE_W_F32) {
-          x[j] = __uint_as_float(q[j]);
-        } else {
-          x[2 * j] = __uint_as_float(q[j] << 16);
-          x[2 * j + 1] = __uint_as_float(q[j] & 0xFFFF0000u);
-        }
+    for (int j = 0; j < 4; ++j) {
+      if (FMT == MOE_W_F32) {
+        q[j] = __float_as_uint(e + j >= 0 && e + j < V ? at(e + j) : -__builtin_inff());
+      } else {
+        const int k = e + 2 * j;
+        const float lo = k >= 0 && k < V ? at(k) : -__builtin_inff();
+        const float hi = k + 1 >= 0 && k + 1 < V ? at(k + 1) : -__builtin_inff();
+        q[j] = (__float_as_uint(lo) >> 16) | __float_as_uint(hi);
       }
-    } else {
-#pragma unroll
-      for (int j = 0; j < kVec<FMT>; ++j)
-        x[j] = e + j >= 0 && e + j < V ? at(e + j) : -__builtin_inff();
     }
+    return q;
   }
 };
 
-// Vectors [begin, end) of a row, two at a time per thread: f(x, first index).
+// Vectors [begin, end) of a row, four logits at a time: f(x, first index, in),
+// whole waves at once (in: this lane's logits exist).  Two vectors per thread
+// are on their way while two are worked on.
 template <int FMT, class F>
 __device__ __forceinline__ void for_slice(const RowView<FMT>& v, int begin, int end, const F& f) {
-  const int step = int(blockDim.x);
+  constexpr int U = 2;
+  const int step = int(blockDim.x), lane = threadIdx.x & 63;
+  const int wave0 = begin + int(threadIdx.x) - lane;
+  u32x4 next[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (wave0 + u * step + lane < end) next[u] = v.load(wave0 + u * step + lane);
 #pragma unroll 1
-  for (int i = begin + int(threadIdx.x); i < end; i += 2 * step) {
-    float x[2][kVec<FMT>];
-    v.load(i, x[0]);
-    const bool two = i + step < end;
-    if (two) v.load(i + step, x[1]);
-    f(x[0], i * kVec<FMT> - v.lead);
-    if (two) f(x[1], (i + step) * kVec<FMT> - v.lead);
+  for (int i0 = wave0; i0 < end; i0 += U * step) {
+    u32x4 now[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      now[u] = next[u];
+      const int i = i0 + (U + u) * step + lane;
+      if (i < end) next[u] = v.load(i);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * step + lane, at = i * kVec<FMT> - v.lead;
+      const u32x4 q = now[u];
+      if (FMT == MOE_W_F32) {
+        const float x[4] = {__uint_as_float(q[0]), __uint_as_float(q[1]), __uint_as_float(q[2]),
+                            __uint_as_float(q[3])};
+        f(x, at, i < end);
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float x[4] = {__uint_as_float(q[2 * h] << 16), __uint_as_float(q[2 * h] & 0xFFFF0000u),
+                              __uint_as_float(q[2 * h + 1] << 16),
+                              __uint_as_float(q[2 * h + 1] & 0xFFFF0000u)};
+          f(x, at + 4 * h, i < end);
+        }
+      }
+    }
   }
 }
 
@@ -198,17 +223,22 @@ __device__ __forceinline__ uint64_t block_max(uint64_t v, uint64_t* red) {
   return m;
 }
 
-// Inclusive prefix of a over the workgroup.
-__device__ __forceinline__ uint64_t block_scan(uint64_t a, uint64_t* red) {
+// Inclusive prefixes of a and b over the workgroup; red: two words per wave.
+__device__ __forceinline__ void block_scan(uint64_t& a, uint64_t& b, uint64_t* red) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   a = wave_scan(a);
+  b = wave_scan(b);
   __syncthreads();
-  if (lane == 63) red[wave] = a;
+  if (lane == 63) red[2 * wave] = a, red[2 * wave + 1] = b;
   __syncthreads();
-  uint64_t before = 0;
+  uint64_t xa = 0, xb = 0;
 #pragma unroll 4
-  for (int w = 0; w < int(blockDim.x) / kWave; ++w) before += w < wave ? red[w] : 0;
-  return a + before;
+  for (int w = 0; w < int(blockDim.x) / kWave; ++w) {
+    xa += w < wave ? red[2 * w] : 0;
+    xb += w < wave ? red[2 * w + 1] : 0;
+  }
+  a += xa;
+  b += xb;
 }
 
 // What workgroups of one launch hand to each other goes through relaxed
@@ -246,14 +276,16 @@ struct Row {
   double top_p;       // >= 1: all
   double u;
   double inv_tau;
+  double top64;       // the largest logit, 0 if that is infinite
   double bins;        // bins per logit
   double limit;       // bins below the largest logit beyond which nothing is drawn (min-p, kCutoff)
   double v1, v2, v3, v4;   // v's power series in the position within the bin, times S
   double inv_s;       // 1 / S
   double unit;        // 2^s
   uint64_t q_mask;
-  int q_bits;         // the count begins at this bit
+  int q_bits;         // the count begins at this bit, 32 or higher
   float top;          // the largest logit
+  bool top_inf;       // it is infinite: only its equals can be drawn
   uint64_t top_key;   // 0: no usable logit
 };
 
@@ -297,6 +329,8 @@ __device__ Row make_row(const SampleArgs& a, const Given& g, uint64_t top_key) {
   Row r;
   r.top_key = top_key;
   r.top = logit_of(top_key);
+  r.top_inf = r.top == __builtin_inff();
+  r.top64 = r.top_inf ? 0.0 : double(r.top);
   r.top_k = g.top_k;
   r.top_p = g.top_p < 1.0f ? fmax(double(g.top_p), 0.0) : 1.0;     // NaN: no cut
   r.u = g.u > 0.0f ? fmin(double(g.u), 1.0) : 0.0;
@@ -324,7 +358,15 @@ __device__ Row make_row(const SampleArgs& a, const Given& g, uint64_t top_key) {
 
 // (largest - logit) in bins; monotone in x; NaN where x is one.
 __device__ __forceinline__ double bins_below(const Row& r, float x) {
-  return x == r.top ? 0.0 : (double(r.top) - double(x)) * r.bins;
+  if (r.top_inf) return x == r.top ? 0.0 : __builtin_nan("");
+  return (r.top64 - double(x)) * r.bins;
+}
+// A bound of the logits that are at most (side -1) or at least (side 1) t
+// bins below the largest: below, or above, all of them, by a little.
+__device__ __forceinline__ float logit_bound(const Row& r, double t, double side) {
+  const double x = r.top64 - t / r.bins;
+  const double b = x + side * (fabs(x) + fabs(r.top64)) * 0x1p-20;
+  return !r.top_inf && fabs(b) < 3.0e38 ? float(b) : float(side) * __builtin_inff();
 }
 // A token at `t` bins below adds this to its bin int(t): a count of one, and q.
 __device__ __forceinline__ uint64_t packed_of(const Row& r, double t) {
@@ -333,14 +375,18 @@ __device__ __forceinline__ uint64_t packed_of(const Row& r, double t) {
   q = fma(q, f, r.v2);
   q = fma(q, f, r.v1);
   q = fma(q, f, 0.5);
-  return (uint64_t(1) << r.q_bits) | uint64_t(uint32_t(q));
-}
-__device__ __forceinline__ uint64_t packed_of_key(const Row& r, uint64_t key) {
-  return packed_of(r, bins_below(r, logit_of(key)));
+  return (uint64_t(1u << (r.q_bits - 32)) << 32) | uint64_t(uint32_t(q));
 }
 // Mass of tokens of one bin (scale = e^(-bin/96) 2^s) from their packed sum.
+__device__ __forceinline__ double bin_step(int j) {   // e^(-j/96), 0 <= j < 8
+  const double e = 0x1.fab1c0ce7a11bp-1, e2 = e * e, e4 = e2 * e2;   // e = e^(-1/96)
+  return (j & 1 ? e : 1.0) * (j & 2 ? e2 : 1.0) * (j & 4 ? e4 : 1.0);
+}
+__device__ __forceinline__ double bin_scale8(const Row& r, int bin) {   // of bin's run of eight
+  return exp_minus(double(bin & ~7) / kBinsPerUnit) * r.unit;
+}
 __device__ __forceinline__ double bin_scale(const Row& r, int bin) {
-  return exp_minus(double(bin) / kBinsPerUnit) * r.unit;
+  return bin_scale8(r, bin) * bin_step(bin & 7);
 }
 __device__ __forceinline__ uint64_t mass_of(const Row& r, double scale, uint64_t packed) {
   const double n = double(packed >> r.q_bits) - double(packed & r.q_mask) * r.inv_s;
@@ -364,10 +410,10 @@ template <int FMT>
 __device__ __forceinline__ uint64_t largest_key(const RowView<FMT>& v, int begin, int end, uint64_t* red) {
   float best = -__builtin_inff();
   int at = 0;
-  for_slice<FMT>(v, begin, end, [&](const float* x, int first) {
+  for_slice<FMT>(v, begin, end, [&](const float (&x)[4], int first, bool in) {
 #pragma unroll
-    for (int j = 0; j < kVec<FMT>; ++j)
-      if (x[j] > best) best = x[j], at = first + j;   // the first of equal ones
+    for (int j = 0; j < 4; ++j)
+      if (in && x[j] > best) best = x[j], at = first + j;   // the first of equal ones
   });
   return block_max(best > -__builtin_inff() ? key_of(best, at) : 0, red);
 }
@@ -376,25 +422,30 @@ __device__ __forceinline__ uint64_t largest_key(const RowView<FMT>& v, int begin
 template <int FMT>
 __device__ __forceinline__ void fill_bins(const Row& r, const RowView<FMT>& v, int begin, int end,
                                           uint64_t* bins) {
-  for_slice<FMT>(v, begin, end, [&](const float* x, int) {
+  const float low = logit_bound(r, r.limit, -1.0);
+  for_slice<FMT>(v, begin, end, [&](const float (&x)[4], int, bool in) {
+    // (NaN and -infinity fail the comparisons)
+    const bool any = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) >= low;
+    if (__ballot(in && any) == 0) return;
 #pragma unroll
-    for (int j = 0; j < kVec<FMT>; ++j) {
+    for (int j = 0; j < 4; ++j) {
       const double t = bins_below(r, x[j]);
-      if (t <= r.limit)
+      if (in && t <= r.limit)
         atomicAdd(reinterpret_cast<unsigned long long*>(&bins[int(t)]),
                   (unsigned long long)packed_of(r, t));
     }
   });
 }
 
-// First bin whose inclusive prefix reaches target (kBins - 1 if none does).
+// First bin whose inclusive prefix reaches target (the last one if none does), found
+// by every wave for itself: 64 ends of 64 bins each, then those 64 bins.
 template <class Tp>
 __device__ __forceinline__ int first_reaching(const Tp* prefix, Tp target) {
-  int b = -1;
-#pragma unroll 1
-  for (int step = kBins / 2; step; step >>= 1)
-    if (prefix[b + step] < target) b += step;
-  return b + 1;
+  static_assert(kBins == 64 * 64, "two steps");
+  const int lane = threadIdx.x & 63;
+  const int run = __popcll(__ballot(prefix[lane * 64 + 63] < target));
+  if (run == 64) return kBins - 1;
+  return run * 64 + __popcll(__ballot(prefix[run * 64 + lane] < target));
 }
 
 // From the bins' packed sums (PER per thread, from bin threadIdx.x * PER) the
@@ -404,23 +455,22 @@ template <int PER>
 __device__ __forceinline__ void bound_targets(const Row& r, const uint64_t* packed, uint64_t* mass,
                                               uint32_t* count, uint64_t* red, int* lo, int* hi) {
   const int b0 = int(threadIdx.x) * PER;
-  uint64_t m[PER], msum = 0;
-  uint32_t csum = 0;
+  static_assert(8 % PER == 0, "a thread's bins lie in one run of eight");
+  uint64_t m[PER], mp = 0, cp = 0;
+  const double scale = bin_scale8(r, b0);
 #pragma unroll
   for (int j = 0; j < PER; ++j) {
-    m[j] = 0;
-    if (packed[j]) m[j] = mass_of(r, bin_scale(r, b0 + j), packed[j]);
-    msum += m[j];
-    csum += uint32_t(packed[j] >> r.q_bits);
+    m[j] = mass_of(r, scale * bin_step((b0 + j) & 7), packed[j]);
+    mp += m[j];
+    cp += packed[j] >> r.q_bits;
   }
-  uint64_t mp = block_scan(msum, red);
-  uint32_t cp = uint32_t(block_scan(uint64_t(csum), red));
+  block_scan(mp, cp, red);
 #pragma unroll
   for (int j = PER - 1; j >= 0; --j) {
     mass[b0 + j] = mp;
-    count[b0 + j] = cp;
+    count[b0 + j] = uint32_t(cp);
     mp -= m[j];
-    cp -= uint32_t(packed[j] >> r.q_bits);
+    cp -= packed[j] >> r.q_bits;
   }
   __syncthreads();
   uint64_t z0 = mass[kBins - 1], z1 = z0;      // bounds of the sum kept so far
@@ -445,17 +495,41 @@ __device__ __forceinline__ void bound_targets(const Row& r, const uint64_t* pack
 // Whether a token lies in one of the bins that matter.
 struct Wanted {
   int lo[3], hi[3];
-  double deepest;        // none lies beyond
+  float from[3], to[3];      // every wanted logit lies in one of these ranges (not only those)
+  float lowest;              // and at or above this
   __device__ Wanted(const Row& r, const int* l, const int* h) {
 #pragma unroll
-    for (int q = 0; q < 3; ++q) lo[q] = l[q], hi[q] = h[q];
-    deepest = double(max(max(hi[0], hi[1]), hi[2]) + 1);
+    for (int q = 0; q < 3; ++q) {
+      lo[q] = l[q], hi[q] = h[q];
+      from[q] = hi[q] < lo[q] ? __builtin_inff() : logit_bound(r, double(hi[q] + 1), -1.0);
+      to[q] = hi[q] < lo[q] ? __builtin_inff() : logit_bound(r, double(lo[q]), 1.0);
+    }
+    lowest = fminf(fminf(from[0], from[1]), from[2]);
+  }
+  // 0 if x lies in one of the ranges: its distance from the nearest
+  __device__ __forceinline__ float outside(float x) const {
+    const float a = fabsf(__builtin_amdgcn_fmed3f(x, from[0], to[0]) - x);
+    const float b = fabsf(__builtin_amdgcn_fmed3f(x, from[1], to[1]) - x);
+    const float c = fabsf(__builtin_amdgcn_fmed3f(x, from[2], to[2]) - x);
+    return fminf(fminf(a, b), c);
   }
   __device__ __forceinline__ bool operator()(const Row& r, float x) const {
     const double t = bins_below(r, x);
-    if (!(t < deepest) || !(t <= r.limit)) return false;
+    if (!(t <= r.limit)) return false;
     const int b = int(t);
     return (b >= lo[0] && b <= hi[0]) || (b >= lo[1] && b <= hi[1]) || (b >= lo[2] && b <= hi[2]);
+  }
+  // of four logits, whole waves at once; false if no lane of the wave wants any
+  __device__ __forceinline__ bool four(const Row& r, const float (&x)[4], bool in, bool (&want)[4]) const {
+    // (NaN and -infinity fail the first comparison; equal infinities have
+    // no distance, and pass the second)
+    const bool high = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) >= lowest;
+    if (__ballot(in && high) == 0) return false;
+    const float off = fminf(fminf(outside(x[0]), outside(x[1])), fminf(outside(x[2]), outside(x[3])));
+    if (__ballot(in && !(off > 0.0f)) == 0) return false;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) want[j] = in && (*this)(r, x[j]);
+    return true;
   }
 };
 
@@ -465,44 +539,24 @@ struct Wanted {
 template <int FMT, class Flush>
 __device__ __forceinline__ void list_wanted(const Row& r, const Wanted& wanted, const RowView<FMT>& v,
                                             int begin, int end, uint64_t* space, const Flush& flush) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, step = int(blockDim.x);
-  const uint32_t room = uint32_t(kLdsList) / uint32_t(step / kWave);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const uint32_t room = uint32_t(kLdsList) / uint32_t(int(blockDim.x) / kWave);
   uint64_t* seg = space + wave * room;
   uint32_t n = 0;
-  auto take = [&](const float* x, int first, bool in) {
-#pragma unroll 1
-    for (int half = 0; half < kVec<FMT>; half += 4) {
-      bool want[4], any = false;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float xj = half == 0 ? x[j] : x[(kVec<FMT> - 4) + j];
-        want[j] = in && wanted(r, xj);
-        any |= want[j];
-      }
-      if (__ballot(any) == 0) continue;
-      if (n + 4 * kWave > room) {
-        flush(seg, n);
-        n = 0;
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint64_t mask = __ballot(want[j]);
-        const float xj = half == 0 ? x[j] : x[(kVec<FMT> - 4) + j];
-        if (want[j]) seg[n + __popcll(mask & ((uint64_t(1) << lane) - 1))] = key_of(xj, first + half + j);
-        n += uint32_t(__popcll(mask));
-      }
+  for_slice<FMT>(v, begin, end, [&](const float (&x)[4], int first, bool in) {
+    bool want[4];
+    if (!wanted.four(r, x, in, want)) return;
+    if (n + 4 * kWave > room) {
+      flush(seg, n);
+      n = 0;
     }
-  };
-  // whole waves take part in every step
-#pragma unroll 1
-  for (int i0 = begin + wave * kWave; i0 < end; i0 += 2 * step) {
-    float x[2][kVec<FMT>];
-    const int i = i0 + lane, i2 = i + step;
-    if (i < end) v.load(i, x[0]);
-    if (i2 < end) v.load(i2, x[1]);
-    take(x[0], i * kVec<FMT> - v.lead, i < end);
-    take(x[1], i2 * kVec<FMT> - v.lead, i2 < end);
-  }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint64_t mask = __ballot(want[j]);
+      if (want[j]) seg[n + __popcll(mask & ((uint64_t(1) << lane) - 1))] = key_of(x[j], first + j);
+      n += uint32_t(__popcll(mask));
+    }
+  });
   if (n) flush(seg, n);
 }
 
@@ -510,13 +564,14 @@ struct PickLds {
   uint64_t hsum[256];
   uint64_t few[64];
   uint64_t all_or, all_and, key, sum, prefix, base;
-  uint32_t n;
+  uint32_t n, left;
   int32_t bin;
 };
 
 // The three questions of one row among its candidates (for_each(f) calls
-// f(key) for each): the drawn token's key, and the kept sum.  mass_before(b)
-// and count_before(b): sums of the bins in front of b; total: the row's.
+// f(key, have) for each, whole waves at once): the drawn token's key, and the
+// kept sum.  mass_before(b) and count_before(b): sums of the bins in front of
+// b; total: the row's.
 template <class Mass, class Count, class ForEach>
 __device__ __forceinline__ uint64_t draw_token(const Row& r, const int* lo, const int* hi, uint64_t total,
                                                const Mass& mass_before, const Count& count_before,
@@ -530,6 +585,7 @@ __device__ __forceinline__ uint64_t draw_token(const Row& r, const int* lo, cons
                                                                  : draw_target(r.u, z);
     __syncthreads();
     if (threadIdx.x == 0) s.all_or = 0, s.all_and = ~0ull, s.n = 0, s.bin = lo[q], s.base = 0;
+    if (threadIdx.x < 256) s.hsum[threadIdx.x] = 0;
     __syncthreads();
     // the bin, and the sum in front of it
 #pragma unroll 1
@@ -544,46 +600,49 @@ __device__ __forceinline__ uint64_t draw_token(const Row& r, const int* lo, cons
     const double scale = bin_scale(r, bin);
     // the sum through tokens whose packed sum from the bin's front is p
     auto sum_of = [&](uint64_t p) { return base + (by_count ? p >> r.q_bits : mass_of(r, scale, p)); };
-    // narrow the key range to at most 64 tokens, 8 bits at a time from the
-    // highest bit in which the bin's keys differ
-    int sh = 64;
-    uint64_t prefix = 0, front = 0;      // front: packed sum of the bin's tokens ahead of the range
-    auto active = [&](uint64_t key) {
-      return (sh == 64 || (key >> sh) == prefix) && int(bins_below(r, logit_of(key))) == bin;
+    // Narrow the bin to at most 64 tokens: first by the position within the
+    // bin, in 256 parts, then (equal logits) by the key, 8 bits at a time
+    // from the highest bit in which the keys differ.
+    uint32_t left = count_before(bin + 1) - count_before(bin);
+    uint64_t front = 0;      // packed sum of the bin's tokens ahead of the range
+    int part = -1;           // the part, -1: all
+    int sh = 64;             // the keys' bits from sh up are prefix, 64: any
+    uint64_t prefix = 0;
+    auto active = [&](uint64_t key, double* t) {
+      *t = bins_below(r, logit_of(key));
+      return int(*t) == bin && (part < 0 || int((*t - double(bin)) * 256.0) == part) &&
+             (sh == 64 || (key >> sh) == prefix);
     };
-    uint32_t left = 0;
 #pragma unroll 1
-    for (;;) {
-      uint64_t o = 0, n = ~0ull;
-      for_each([&](uint64_t key) {
-        if (active(key)) {
-          o |= key, n &= key;
-          const uint32_t i = atomicAdd(&s.n, 1u);
-          if (i < 64) s.few[i] = key;
+    while (left > 64 && sh > 0) {
+      const bool by_part = part < 0;
+      int next = 0;
+      if (!by_part) {
+        if (sh == 64) {
+          uint64_t o = 0, n = ~0ull;
+          for_each([&](uint64_t key, bool have) {
+            double t;
+            if (have && active(key, &t)) o |= key, n &= key;
+          });
+          if (n != ~0ull) {
+            atomicOr(reinterpret_cast<unsigned long long*>(&s.all_or), (unsigned long long)o);
+            atomicAnd(reinterpret_cast<unsigned long long*>(&s.all_and), (unsigned long long)n);
+          }
+          __syncthreads();
+          const uint64_t differ = s.all_or & ~s.all_and;   // not 0: keys are unique
+          sh = 64 - __clzll((long long)differ);
+          prefix = sh == 64 ? 0 : s.all_or >> sh;
         }
-      });
-      if (sh == 64 && n != ~0ull) {
-        atomicOr(reinterpret_cast<unsigned long long*>(&s.all_or), (unsigned long long)o);
-        atomicAnd(reinterpret_cast<unsigned long long*>(&s.all_and), (unsigned long long)n);
+        next = sh > 8 ? sh - 8 : 0;
+        if (threadIdx.x < 256) s.hsum[threadIdx.x] = 0;
+        __syncthreads();
       }
-      __syncthreads();
-      left = s.n;
-      if (left <= 64 || sh == 0) break;
-      if (sh == 64) {
-        const uint64_t differ = s.all_or & ~s.all_and;   // not 0: keys are unique
-        sh = 64 - __clzll((long long)differ);
-        prefix = sh == 64 ? 0 : s.all_or >> sh;
-      }
-      const int next = sh > 8 ? sh - 8 : 0;
       const uint64_t digits = (uint64_t(1) << (sh - next)) - 1;
-      __syncthreads();
-      if (threadIdx.x < 256) s.hsum[threadIdx.x] = 0;
-      if (threadIdx.x == 0) s.n = 0;
-      __syncthreads();
-      for_each([&](uint64_t key) {
-        if (active(key))
-          atomicAdd(reinterpret_cast<unsigned long long*>(&s.hsum[(key >> next) & digits]),
-                    (unsigned long long)packed_of_key(r, key));
+      for_each([&](uint64_t key, bool have) {
+        double t;
+        if (!have || !active(key, &t)) return;
+        const int d = by_part ? 255 - int((t - double(bin)) * 256.0) : int((key >> next) & digits);
+        atomicAdd(reinterpret_cast<unsigned long long*>(&s.hsum[d]), (unsigned long long)packed_of(r, t));
       });
       __syncthreads();
       if (threadIdx.x < 64) {
@@ -596,22 +655,40 @@ __device__ __forceinline__ uint64_t draw_token(const Row& r, const int* lo, cons
         for (int j = 0; j < 4; ++j) {
           const uint64_t vj = j == 0 ? v[0] : j == 1 ? v[1] : j == 2 ? v[2] : v[3];
           if (vj && sum_of(before) < target && sum_of(before + vj) >= target) {
-            s.prefix = ((sh == 64 ? 0 : prefix) << (sh - next)) | uint64_t(255 - 4 * int(threadIdx.x) - j);
+            s.prefix = uint64_t(255 - 4 * int(threadIdx.x) - j);
             s.sum = before;
+            s.left = uint32_t(vj >> r.q_bits);
           }
           before += vj;
         }
       }
       __syncthreads();
-      prefix = s.prefix;
       front = s.sum;
-      sh = next;
+      left = s.left;
+      if (by_part) {
+        part = 255 - int(s.prefix);
+      } else {
+        prefix = ((sh == 64 ? 0 : prefix) << (sh - next)) | s.prefix;
+        sh = next;
+      }
     }
+    for_each([&](uint64_t key, bool have) {
+      double t;
+      const bool take = have && active(key, &t);
+      const uint64_t mask = __ballot(take);
+      if (mask == 0) return;
+      const int lane = threadIdx.x & 63;
+      uint32_t at = 0;
+      if (lane == 0) at = atomicAdd(&s.n, uint32_t(__popcll(mask)));
+      at = __shfl(at, 0, kWave) + uint32_t(__popcll(mask & ((uint64_t(1) << lane) - 1)));
+      if (take && at < 64) s.few[at] = key;
+    });
+    __syncthreads();
     if (threadIdx.x < 64) {
-      const uint32_t n = min(left, 64u);
+      const uint32_t n = min(s.n, 64u);
       const bool have = threadIdx.x < n;
       const uint64_t key = have ? s.few[threadIdx.x] : 0;
-      const uint64_t mine = have ? packed_of_key(r, key) : 0;
+      const uint64_t mine = have ? packed_of(r, bins_below(r, logit_of(key))) : 0;
       uint64_t ahead = front;
 #pragma unroll 1
       for (uint32_t j = 0; j < n; ++j) {
@@ -625,11 +702,49 @@ __device__ __forceinline__ uint64_t draw_token(const Row& r, const int* lo, cons
     }
     __syncthreads();
     if (q == 2) break;
-    z = (by_count ? mass_before(bin) : base) + mass_of(r, scale, s.sum);
-    if (z < 1) z = 1;
+    z = max_u64(mass_before(bin) + mass_of(r, scale, s.sum), 1);
   }
   *kept = z;
   return s.key;
+}
+
+// The same by one wave, for up to 64 candidates: lane i holds the i-th (key 0:
+// none).
+template <class Mass, class Count>
+__device__ __forceinline__ uint64_t draw_token_wave(const Row& r, const int* lo, const int* hi,
+                                                    uint64_t total, const Mass& mass_before,
+                                                    const Count& count_before, uint32_t n, uint64_t key,
+                                                    uint64_t* kept) {
+  const int lane = threadIdx.x & 63;
+  const double t = bins_below(r, logit_of(key));
+  const int my_bin = key ? int(t) : -1;
+  const uint64_t mine = key ? packed_of(r, t) : 0;
+  // packed sum of the candidates of this one's bin in front of it
+  uint64_t ahead = 0;
+#pragma unroll 1
+  for (uint32_t j = 0; j < n; ++j) {
+    const uint64_t ok = shfl_u64(key, int(j)), op = shfl_u64(mine, int(j));
+    const int ob = __shfl(my_bin, int(j), kWave);
+    if (ok > key && ob == my_bin) ahead += op;
+  }
+  const double scale = bin_scale(r, max(my_bin, 0));
+  const uint64_t m0 = mass_before(max(my_bin, 0)), c0 = count_before(max(my_bin, 0));
+  const uint64_t mass_to = m0 + mass_of(r, scale, ahead), mass_thru = m0 + mass_of(r, scale, ahead + mine);
+  const uint64_t count_to = c0 + (ahead >> r.q_bits);
+  uint64_t z = total;
+  if (hi[0] >= lo[0]) {
+    const uint64_t hit = __ballot(key && count_to + 1 == uint64_t(r.top_k));
+    z = max_u64(shfl_u64(mass_thru, __ffsll((long long)hit) - 1), 1);
+  }
+  if (hi[1] >= lo[1]) {
+    const uint64_t target = top_p_target(r.top_p, z);
+    const uint64_t hit = __ballot(key && mass_to < target && mass_thru >= target);
+    z = max_u64(shfl_u64(mass_thru, __ffsll((long long)hit) - 1), 1);
+  }
+  const uint64_t target = draw_target(r.u, z);
+  const uint64_t hit = __ballot(key && mass_to < target && mass_thru >= target);
+  *kept = z;
+  return shfl_u64(key, __ffsll((long long)hit) - 1);
 }
 
 // The drawn token's probability.
@@ -646,7 +761,7 @@ __global__ __launch_bounds__(kRowThreads) void sample_row_kernel(const SampleArg
   __shared__ uint64_t mass[kBins];
   __shared__ uint32_t count[kBins];
   __shared__ uint64_t list[kLdsList];
-  __shared__ uint64_t red[kRowThreads / kWave];
+  __shared__ uint64_t red[2 * kRowThreads / kWave];
   __shared__ PickLds s;
   __shared__ uint32_t listed;
   const int row = blockIdx.x;
@@ -673,47 +788,50 @@ __global__ __launch_bounds__(kRowThreads) void sample_row_kernel(const SampleArg
   bound_targets<PER>(r, packed, mass, count, red, lo, hi);
   const Wanted wanted(r, lo, hi);
   // the wanted tokens, as far as they fit
-  const int lane = threadIdx.x & 63;
-  {
-    auto add = [&](const float* x, int first, bool in) {
+  for_slice<FMT>(v, 0, v.vecs, [&](const float (&x)[4], int first, bool in) {
+    const int lane = threadIdx.x & 63;
+    bool want[4];
+    if (!wanted.four(r, x, in, want)) return;
+    uint64_t mask[4];
+    uint32_t n = 0;
 #pragma unroll
-      for (int j = 0; j < kVec<FMT>; ++j) {
-        const bool want = in && wanted(r, x[j]);
-        const uint64_t mask = __ballot(want);
-        if (mask == 0) continue;
-        uint32_t at = 0;
-        if (lane == 0) at = atomicAdd(&listed, uint32_t(__popcll(mask)));
-        at = __shfl(at, 0, kWave) + uint32_t(__popcll(mask & ((uint64_t(1) << lane) - 1)));
-        if (want && at < uint32_t(kLdsList)) list[at] = key_of(x[j], first + j);
-      }
-    };
-#pragma unroll 1
-    for (int i0 = int(threadIdx.x) - lane; i0 < v.vecs; i0 += 2 * kRowThreads) {
-      float x[2][kVec<FMT>];
-      const int i = i0 + lane, i2 = i + kRowThreads;
-      if (i < v.vecs) v.load(i, x[0]);
-      if (i2 < v.vecs) v.load(i2, x[1]);
-      add(x[0], i * kVec<FMT> - v.lead, i < v.vecs);
-      add(x[1], i2 * kVec<FMT> - v.lead, i2 < v.vecs);
+    for (int j = 0; j < 4; ++j) {
+      mask[j] = __ballot(want[j]);
+      n += uint32_t(__popcll(mask[j]));
     }
-  }
+    if (n == 0) return;
+    uint32_t at = 0;
+    if (lane == 0) at = atomicAdd(&listed, n);
+    at = __shfl(at, 0, kWave);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t k = at + uint32_t(__popcll(mask[j] & ((uint64_t(1) << lane) - 1)));
+      if (want[j] && k < uint32_t(kLdsList)) list[k] = key_of(x[j], first + j);
+      at += uint32_t(__popcll(mask[j]));
+    }
+  });
   __syncthreads();
   const uint32_t n = listed;
   auto mass_before = [&](int b) { return b ? mass[b - 1] : uint64_t(0); };
   auto count_before = [&](int b) { return b ? count[b - 1] : 0u; };
   uint64_t key, kept;
-  if (n <= uint32_t(kLdsList)) {
+  if (n <= uint32_t(kWave)) {
+    if (threadIdx.x >= kWave) return;
+    key = draw_token_wave(r, lo, hi, mass[kBins - 1], mass_before, count_before, n,
+                          threadIdx.x < n ? list[threadIdx.x] : 0, &kept);
+  } else if (n <= uint32_t(kLdsList)) {
     key = draw_token(r, lo, hi, mass[kBins - 1], mass_before, count_before, s, &kept, [&](auto&& f) {
 #pragma unroll 1
-      for (uint32_t k = threadIdx.x; k < n; k += kRowThreads) f(list[k]);
+      for (uint32_t k = threadIdx.x; k - (threadIdx.x & 63) < n; k += kRowThreads)
+        f(k < n ? list[k] : 0, k < n);
     });
   } else {
     // more candidates than the list holds (long runs of equal logits): the row itself
     key = draw_token(r, lo, hi, mass[kBins - 1], mass_before, count_before, s, &kept, [&](auto&& f) {
 #pragma unroll 1
-      for (int i = threadIdx.x; i < a.V; i += kRowThreads) {
-        const float x = v.at(i);
-        if (wanted(r, x)) f(key_of(x, i));
+      for (int i = threadIdx.x; i - int(threadIdx.x & 63) < a.V; i += kRowThreads) {
+        const float x = i < a.V ? v.at(i) : -__builtin_inff();
+        f(key_of(x, i), i < a.V && wanted(r, x));
       }
     });
   }
@@ -743,7 +861,7 @@ __device__ __forceinline__ Row read_row(const SampleArgs& a, const Ws& w, int ro
 // 1. Largest logit of every slice; clears the row's sums.
 template <int FMT>
 __global__ __launch_bounds__(kThreads) void sample_max_kernel(const SampleArgs a) {
-  __shared__ uint64_t red[kThreads / kWave];
+  __shared__ uint64_t red[2 * kThreads / kWave];
   Ws w;
   ws_layout(a.T, static_cast<uint8_t*>(a.ws), &w);
   const int p = blockIdx.x, row = blockIdx.y;
@@ -765,7 +883,7 @@ __global__ __launch_bounds__(kThreads) void sample_hist_kernel(const SampleArgs 
   constexpr int PER = kBins / kThreads;
   __shared__ uint64_t mass[kBins];
   __shared__ uint32_t count[kBins];
-  __shared__ uint64_t red[kThreads / kWave];
+  __shared__ uint64_t red[2 * kThreads / kWave];
   __shared__ uint32_t flag;
   Ws w;
   ws_layout(a.T, static_cast<uint8_t*>(a.ws), &w);
@@ -819,7 +937,7 @@ __device__ void finish_row(const SampleArgs& a, const Ws& w, int row, int token,
 template <int FMT>
 __global__ __launch_bounds__(kThreads) void sample_pick_kernel(const SampleArgs a) {
   __shared__ uint64_t space[kLdsList];
-  __shared__ uint64_t red[kThreads / kWave];
+  __shared__ uint64_t red[2 * kThreads / kWave];
   __shared__ PickLds s;
   __shared__ uint32_t flag;
   Ws w;
@@ -860,21 +978,26 @@ __global__ __launch_bounds__(kThreads) void sample_pick_kernel(const SampleArgs 
   auto mass_before = [&](int b) { return gm[b]; };
   auto count_before = [&](int b) { return gc[b]; };
   uint64_t key, kept;
-  if (n <= uint32_t(kListCap)) {
+  if (n <= uint32_t(kWave)) {
+    const uint32_t i = threadIdx.x & 63;      // (every wave finds the same)
+    key = draw_token_wave(r, lo, hi, gm[kBins], mass_before, count_before, n,
+                          i < n ? get(&list[i]) : 0, &kept);
+  } else if (n <= uint32_t(kListCap)) {
     const bool in_lds = n <= uint32_t(kLdsList);
     if (in_lds)
       for (uint32_t k = threadIdx.x; k < n; k += kThreads) space[k] = get(&list[k]);
     key = draw_token(r, lo, hi, gm[kBins], mass_before, count_before, s, &kept, [&](auto&& f) {
 #pragma unroll 1
-      for (uint32_t k = threadIdx.x; k < n; k += kThreads) f(in_lds ? space[k] : get(&list[k]));
+      for (uint32_t k = threadIdx.x; k - (threadIdx.x & 63) < n; k += kThreads)
+        f(k >= n ? 0 : in_lds ? space[k] : get(&list[k]), k < n);
     });
   } else {
     // more candidates than the list holds (long runs of equal logits): the row itself
     key = draw_token(r, lo, hi, gm[kBins], mass_before, count_before, s, &kept, [&](auto&& f) {
 #pragma unroll 1
-      for (int i = threadIdx.x; i < a.V; i += kThreads) {
-        const float x = v.at(i);
-        if (wanted(r, x)) f(key_of(x, i));
+      for (int i = threadIdx.x; i - int(threadIdx.x & 63) < a.V; i += kThreads) {
+        const float x = i < a.V ? v.at(i) : -__builtin_inff();
+        f(key_of(x, i), i < a.V && wanted(r, x));
       }
     });
   }
@@ -919,7 +1042,7 @@ hipError_t launch_sample(SampleArgs a, hipStream_t st) {
   // to 2^bits above 2^bits values of frac_bits bits
   a.shift = min(52, 61 - bits);
   a.frac_bits = min(28, 63 - 2 * bits);
-  a.q_bits = bits + a.frac_bits;
+  a.q_bits = max(32, bits + a.frac_bits);
   return a.fmt == MOE_W_F32 ? launch<MOE_W_F32>(a, st) : launch<MOE_W_BF16>(a, st);
 }
 
