@@ -19,7 +19,7 @@
 //     answered exactly among them: by 8 key bits at a time, then among at most
 //     64 tokens within one wave.
 //
-// Sums.  Within bin b, w = e^(-b/96) (1 - v) with 0 <= v < 0.0104.  v is
+// Sums.  Within bin b, w = e^(-b/96) (1 - v) with 0 <= v < 0.0105.  v is
 // evaluated in 64 bits and held as an integer q (27 bits for 151,936 tokens:
 // w to 2^-34 of itself), and a token adds (1, q) to its bin as one 64-bit
 // integer, the count in the high bits: one LDS atomic per token, no
@@ -46,6 +46,7 @@ constexpr int kThreads = 512;           // of the kernels over slices
 constexpr int kRowThreads = 1024;       // of the kernel over rows
 constexpr int kBins = 4096;
 constexpr double kBinsPerUnit = 96.0;
+constexpr double kToInt = 0x1.8p52;     // added: the low 32 bits are the nearest integer
 constexpr double kCutoff = 42.0;        // units below the largest logit from which on nothing is drawn
 constexpr int kMaxParts = 256;
 constexpr int kSlice = 4096;            // logits of a row per workgroup
@@ -90,39 +91,53 @@ template <int FMT>
 constexpr int kVec = FMT == MOE_W_F32 ? 4 : 8;
 
 // Row `row` as a range of 16-byte vectors: vector i holds elements
-// [i * kVec - lead, ...).
+// [i * kVec - lead, ...); the first and the last may lie partly outside.
 template <int FMT>
 struct RowView {
-  const uint8_t* base;   // address of vector 0 (16-byte aligned; not read before the row)
+  typedef const __attribute__((address_space(1))) uint8_t* Bytes;
+  typedef const __attribute__((address_space(1))) float* Floats;
+  typedef const __attribute__((address_space(1))) uint16_t* Halves;
+  typedef const __attribute__((address_space(1))) u32x4* Vectors;
+  Bytes base;            // address of vector 0 (16-byte aligned; not read before the row)
   int lead;              // elements of vector 0 in front of the row
   int V;
   int vecs;
+  int inner0, inner1;    // vectors wholly inside: [inner0, inner1]
   __device__ RowView(const void* logits, int64_t stride, int row, int v) {
     constexpr int size = FMT == MOE_W_F32 ? 4 : 2;
     const uintptr_t a = reinterpret_cast<uintptr_t>(logits) + uintptr_t(row) * stride * size;
-    base = reinterpret_cast<const uint8_t*>(a & ~uintptr_t(15));
+    base = (Bytes)(a & ~uintptr_t(15));
     lead = int(a & 15) / size;
     V = v;
     vecs = (V + lead + kVec<FMT> - 1) / kVec<FMT>;
+    inner0 = lead ? 1 : 0;
+    inner1 = (V + lead) / kVec<FMT> - 1;
   }
   __device__ float at(int i) const {
-    if (FMT == MOE_W_F32) return reinterpret_cast<const float*>(base)[lead + int64_t(i)];
-    return bf16_to_f32(reinterpret_cast<const uint16_t*>(base)[lead + int64_t(i)]);
+    if (FMT == MOE_W_F32) return ((Floats)base)[lead + int64_t(i)];
+    return bf16_to_f32(((Halves)base)[lead + int64_t(i)]);
   }
   // vector i's 16 bytes, elements outside the row as -infinity
-  __device__ u32x4 load(int i) const {
-    const int e = i * kVec<FMT> - lead;
-    if (e >= 0 && e + kVec<FMT> <= V) return *reinterpret_cast<const u32x4*>(base + int64_t(i) * 16);
+  __device__ __forceinline__ u32x4 load(int i) const {
     u32x4 q;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (FMT == MOE_W_F32) {
-        q[j] = __float_as_uint(e + j >= 0 && e + j < V ? at(e + j) : -__builtin_inff());
-      } else {
-        const int k = e + 2 * j;
-        const float lo = k >= 0 && k < V ? at(k) : -__builtin_inff();
-        const float hi = k + 1 >= 0 && k + 1 < V ? at(k + 1) : -__builtin_inff();
-        q[j] = (__float_as_uint(lo) >> 16) | __float_as_uint(hi);
+    if (inner1 >= inner0) q = ((Vectors)base)[int64_t(max(inner0, min(i, inner1)))];
+    if (i < inner0 || i > inner1) {
+      const int e = i * kVec<FMT> - lead;
+#pragma unroll 1
+      for (int j = 0; j < 4; ++j) {
+        uint32_t w;
+        if (FMT == MOE_W_F32) {
+          w = __float_as_uint(e + j >= 0 && e + j < V ? at(e + j) : -__builtin_inff());
+        } else {
+          const int k = e + 2 * j;
+          const float lo = k >= 0 && k < V ? at(k) : -__builtin_inff();
+          const float hi = k + 1 >= 0 && k + 1 < V ? at(k + 1) : -__builtin_inff();
+          w = (__float_as_uint(lo) >> 16) | __float_as_uint(hi);
+        }
+        if (j == 0) q[0] = w;
+        else if (j == 1) q[1] = w;
+        else if (j == 2) q[2] = w;
+        else q[3] = w;
       }
     }
     return q;
@@ -130,11 +145,10 @@ struct RowView {
 };
 
 // Vectors [begin, end) of a row, four logits at a time: f(x, first index, in),
-// whole waves at once (in: this lane's logits exist).  Two vectors per thread
-// are on their way while two are worked on.
-template <int FMT, class F>
+// whole waves at once (in: this lane's logits exist).  U vectors per thread
+// are on their way while U are worked on.
+template <int FMT, int U, class F>
 __device__ __forceinline__ void for_slice(const RowView<FMT>& v, int begin, int end, const F& f) {
-  constexpr int U = 2;
   const int step = int(blockDim.x), lane = threadIdx.x & 63;
   const int wave0 = begin + int(threadIdx.x) - lane;
   u32x4 next[U];
@@ -278,8 +292,8 @@ struct Row {
   double inv_tau;
   double top64;       // the largest logit, 0 if that is infinite
   double bins;        // bins per logit
-  double limit;       // bins below the largest logit beyond which nothing is drawn (min-p, kCutoff)
-  double v1, v2, v3, v4;   // v's power series in the position within the bin, times S
+  double limit;       // place beyond which nothing is drawn (min-p, kCutoff)
+  double v0, v1, v2, v3, v4;   // S v as a power series of the place's distance from the bin's middle
   double inv_s;       // 1 / S
   double unit;        // 2^s
   uint64_t q_mask;
@@ -343,10 +357,13 @@ __device__ Row make_row(const SampleArgs& a, const Given& g, uint64_t top_key) {
     const double m = double(g.min_p), d = fmax(double(-logf(g.min_p)), 0.0);
     r.limit = fmin(r.limit, (d - (m / exp_minus(d) - 1.0)) * kBinsPerUnit);
   }
-  // v(f) = 1 - exp(-f / 96), to f^4 (the rest is below 1e-12), and S
+  r.limit -= 0.5;
+  // v = 1 - exp(-(f + 1/2) / 96), to f^4 (the rest is below 1e-13), and S
   const double s = __longlong_as_double((int64_t)(1023 + a.frac_bits + 6) << 52);   // v < 2^-6 * 0.67
+  const double middle = 0x1.fd571ba7c4ef1p-1;                                        // exp(-1 / 192)
   r.inv_s = 1.0 / s;
-  r.v1 = s / kBinsPerUnit;
+  r.v0 = s * (1.0 - middle);
+  r.v1 = s * middle / kBinsPerUnit;
   r.v2 = r.v1 / (-2.0 * kBinsPerUnit);
   r.v3 = r.v2 / (-3.0 * kBinsPerUnit);
   r.v4 = r.v3 / (-4.0 * kBinsPerUnit);
@@ -356,11 +373,22 @@ __device__ Row make_row(const SampleArgs& a, const Given& g, uint64_t top_key) {
   return r;
 }
 
-// (largest - logit) in bins; monotone in x; NaN where x is one.
-__device__ __forceinline__ double bins_below(const Row& r, float x) {
-  if (r.top_inf) return x == r.top ? 0.0 : __builtin_nan("");
-  return (r.top64 - double(x)) * r.bins;
+// A row whose largest logit is infinite draws among its equals alone: these
+// as 0, the others as -infinity.
+__device__ __forceinline__ float seen(const Row& r, float x) {
+  return !r.top_inf ? x : x == r.top ? 0.0f : -__builtin_inff();
 }
+// Place of a logit: (largest - logit) in bins, less 1/2; monotone in x, NaN
+// where x is one.  The nearest integer is its bin (0 .. kBins - 1 if the
+// place is at most r.limit).
+__device__ __forceinline__ double place_of(const Row& r, float x) {
+  return fma(r.top64 - double(x), r.bins, -0.5);
+}
+__device__ __forceinline__ int bin_at(double place) {
+  return int(uint32_t(__double_as_longlong(place + kToInt)));
+}
+// Position within the bin, 0 to 1.
+__device__ __forceinline__ double within(double place) { return place - ((place + kToInt) - kToInt) + 0.5; }
 // A bound of the logits that are at most (side -1) or at least (side 1) t
 // bins below the largest: below, or above, all of them, by a little.
 __device__ __forceinline__ float logit_bound(const Row& r, double t, double side) {
@@ -368,14 +396,14 @@ __device__ __forceinline__ float logit_bound(const Row& r, double t, double side
   const double b = x + side * (fabs(x) + fabs(r.top64)) * 0x1p-20;
   return !r.top_inf && fabs(b) < 3.0e38 ? float(b) : float(side) * __builtin_inff();
 }
-// A token at `t` bins below adds this to its bin int(t): a count of one, and q.
-__device__ __forceinline__ uint64_t packed_of(const Row& r, double t) {
-  const double f = t - double(int(t));
+// A token adds this to its bin: a count of one, and q.
+__device__ __forceinline__ uint64_t packed_of(const Row& r, double place) {
+  const double f = place - ((place + kToInt) - kToInt);
   double q = fma(r.v4, f, r.v3);
   q = fma(q, f, r.v2);
   q = fma(q, f, r.v1);
-  q = fma(q, f, 0.5);
-  return (uint64_t(1u << (r.q_bits - 32)) << 32) | uint64_t(uint32_t(q));
+  q = fma(q, f, r.v0);
+  return (uint64_t(1u << (r.q_bits - 32)) << 32) | uint64_t(uint32_t(__double_as_longlong(q + kToInt)));
 }
 // Mass of tokens of one bin (scale = e^(-bin/96) 2^s) from their packed sum.
 __device__ __forceinline__ double bin_step(int j) {   // e^(-j/96), 0 <= j < 8
@@ -410,7 +438,7 @@ template <int FMT>
 __device__ __forceinline__ uint64_t largest_key(const RowView<FMT>& v, int begin, int end, uint64_t* red) {
   float best = -__builtin_inff();
   int at = 0;
-  for_slice<FMT>(v, begin, end, [&](const float (&x)[4], int first, bool in) {
+  for_slice<FMT, 4>(v, begin, end, [&](const float (&x)[4], int first, bool in) {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       if (in && x[j] > best) best = x[j], at = first + j;   // the first of equal ones
@@ -422,18 +450,25 @@ __device__ __forceinline__ uint64_t largest_key(const RowView<FMT>& v, int begin
 template <int FMT>
 __device__ __forceinline__ void fill_bins(const Row& r, const RowView<FMT>& v, int begin, int end,
                                           uint64_t* bins) {
-  const float low = logit_bound(r, r.limit, -1.0);
-  for_slice<FMT>(v, begin, end, [&](const float (&x)[4], int, bool in) {
+  const float low = logit_bound(r, r.limit + 0.5, -1.0);
+  for_slice<FMT, 2>(v, begin, end, [&](const float (&x)[4], int, bool in) {
     // (NaN and -infinity fail the comparisons)
     const bool any = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) >= low;
     if (__ballot(in && any) == 0) return;
+    float y[4] = {x[0], x[1], x[2], x[3]};
+    if (__builtin_expect(r.top_inf, 0)) {
+      asm volatile("");      // a branch, not four selections
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const double t = bins_below(r, x[j]);
-      if (in && t <= r.limit)
-        atomicAdd(reinterpret_cast<unsigned long long*>(&bins[int(t)]),
-                  (unsigned long long)packed_of(r, t));
+      for (int j = 0; j < 4; ++j) y[j] = seen(r, x[j]);
     }
+    double place[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) place[j] = place_of(r, y[j]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (in && place[j] <= r.limit)
+        atomicAdd(reinterpret_cast<unsigned long long*>(&bins[bin_at(place[j])]),
+                  (unsigned long long)packed_of(r, place[j]));
   });
 }
 
@@ -514,50 +549,43 @@ struct Wanted {
     return fminf(fminf(a, b), c);
   }
   __device__ __forceinline__ bool operator()(const Row& r, float x) const {
-    const double t = bins_below(r, x);
-    if (!(t <= r.limit)) return false;
-    const int b = int(t);
+    const double place = place_of(r, seen(r, x));
+    if (!(place <= r.limit)) return false;
+    const int b = bin_at(place);
     return (b >= lo[0] && b <= hi[0]) || (b >= lo[1] && b <= hi[1]) || (b >= lo[2] && b <= hi[2]);
-  }
-  // of four logits, whole waves at once; false if no lane of the wave wants any
-  __device__ __forceinline__ bool four(const Row& r, const float (&x)[4], bool in, bool (&want)[4]) const {
-    // (NaN and -infinity fail the first comparison; equal infinities have
-    // no distance, and pass the second)
-    const bool high = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) >= lowest;
-    if (__ballot(in && high) == 0) return false;
-    const float off = fminf(fminf(outside(x[0]), outside(x[1])), fminf(outside(x[2]), outside(x[3])));
-    if (__ballot(in && !(off > 0.0f)) == 0) return false;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) want[j] = in && (*this)(r, x[j]);
-    return true;
   }
 };
 
 // Lists the wanted tokens of vectors [begin, end): each wave fills its own
-// segment of `space` (LDS, kLdsList keys for the workgroup) and empties it
-// with flush(keys, n), which the whole wave calls.
-template <int FMT, class Flush>
-__device__ __forceinline__ void list_wanted(const Row& r, const Wanted& wanted, const RowView<FMT>& v,
-                                            int begin, int end, uint64_t* space, const Flush& flush) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const uint32_t room = uint32_t(kLdsList) / uint32_t(int(blockDim.x) / kWave);
-  uint64_t* seg = space + wave * room;
+// segment (LDS, room keys) and calls full(n) before it would overflow, which
+// returns how many it still holds.  Returns the number in the segment.
+template <int FMT, class Full>
+__device__ __forceinline__ uint32_t list_wanted(const Row& r, const Wanted& wanted, const RowView<FMT>& v,
+                                                int begin, int end, uint64_t* segment, uint32_t room,
+                                                const Full& full) {
+  const uint64_t below = (uint64_t(1) << (threadIdx.x & 63)) - 1;
   uint32_t n = 0;
-  for_slice<FMT>(v, begin, end, [&](const float (&x)[4], int first, bool in) {
-    bool want[4];
-    if (!wanted.four(r, x, in, want)) return;
-    if (n + 4 * kWave > room) {
-      flush(seg, n);
-      n = 0;
-    }
+  for_slice<FMT, 2>(v, begin, end, [&](const float (&x)[4], int first, bool in) {
+    // (NaN and -infinity fail the first comparison; equal infinities have
+    // no distance, and pass the second)
+    const bool high = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) >= wanted.lowest;
+    if (__ballot(in && high) == 0) return;
+    float off[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) off[j] = wanted.outside(x[j]);
+    if (__ballot(in && !(fminf(fminf(off[0], off[1]), fminf(off[2], off[3])) > 0.0f)) == 0) return;
+    if (n + 4 * kWave > room) n = full(n);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const uint64_t mask = __ballot(want[j]);
-      if (want[j]) seg[n + __popcll(mask & ((uint64_t(1) << lane) - 1))] = key_of(x[j], first + j);
+      bool want = in && !(off[j] > 0.0f);
+      if (want) want = wanted(r, x[j]);
+      const uint64_t mask = __ballot(want);
+      const uint32_t at = n + uint32_t(__popcll(mask & below));
+      if (want && at < room) segment[at] = key_of(x[j], first + j);
       n += uint32_t(__popcll(mask));
     }
   });
-  if (n) flush(seg, n);
+  return n;
 }
 
 struct PickLds {
@@ -608,9 +636,10 @@ __device__ __forceinline__ uint64_t draw_token(const Row& r, const int* lo, cons
     int part = -1;           // the part, -1: all
     int sh = 64;             // the keys' bits from sh up are prefix, 64: any
     uint64_t prefix = 0;
-    auto active = [&](uint64_t key, double* t) {
-      *t = bins_below(r, logit_of(key));
-      return int(*t) == bin && (part < 0 || int((*t - double(bin)) * 256.0) == part) &&
+    auto part_of = [](double place) { return min(int(within(place) * 256.0), 255); };
+    auto active = [&](uint64_t key, double* place) {
+      *place = place_of(r, seen(r, logit_of(key)));
+      return bin_at(*place) == bin && (part < 0 || part_of(*place) == part) &&
              (sh == 64 || (key >> sh) == prefix);
     };
 #pragma unroll 1
@@ -641,7 +670,7 @@ __device__ __forceinline__ uint64_t draw_token(const Row& r, const int* lo, cons
       for_each([&](uint64_t key, bool have) {
         double t;
         if (!have || !active(key, &t)) return;
-        const int d = by_part ? 255 - int((t - double(bin)) * 256.0) : int((key >> next) & digits);
+        const int d = by_part ? 255 - part_of(t) : int((key >> next) & digits);
         atomicAdd(reinterpret_cast<unsigned long long*>(&s.hsum[d]), (unsigned long long)packed_of(r, t));
       });
       __syncthreads();
@@ -688,7 +717,7 @@ __device__ __forceinline__ uint64_t draw_token(const Row& r, const int* lo, cons
       const uint32_t n = min(s.n, 64u);
       const bool have = threadIdx.x < n;
       const uint64_t key = have ? s.few[threadIdx.x] : 0;
-      const uint64_t mine = have ? packed_of(r, bins_below(r, logit_of(key))) : 0;
+      const uint64_t mine = have ? packed_of(r, place_of(r, seen(r, logit_of(key)))) : 0;
       uint64_t ahead = front;
 #pragma unroll 1
       for (uint32_t j = 0; j < n; ++j) {
@@ -716,9 +745,9 @@ __device__ __forceinline__ uint64_t draw_token_wave(const Row& r, const int* lo,
                                                     const Count& count_before, uint32_t n, uint64_t key,
                                                     uint64_t* kept) {
   const int lane = threadIdx.x & 63;
-  const double t = bins_below(r, logit_of(key));
-  const int my_bin = key ? int(t) : -1;
-  const uint64_t mine = key ? packed_of(r, t) : 0;
+  const double place = place_of(r, seen(r, logit_of(key)));
+  const int my_bin = key ? bin_at(place) : -1;
+  const uint64_t mine = key ? packed_of(r, place) : 0;
   // packed sum of the candidates of this one's bin in front of it
   uint64_t ahead = 0;
 #pragma unroll 1
@@ -749,8 +778,8 @@ __device__ __forceinline__ uint64_t draw_token_wave(const Row& r, const int* lo,
 
 // The drawn token's probability.
 __device__ __forceinline__ float prob_of(const Row& r, uint64_t key, uint64_t kept) {
-  const double t = bins_below(r, logit_of(key));
-  return float(exp_minus(fmin(t, kCutoff * kBinsPerUnit) / kBinsPerUnit) * r.unit / double(kept));
+  const double t = place_of(r, seen(r, logit_of(key))) + 0.5;
+  return float(exp_minus(fmax(0.0, fmin(t / kBinsPerUnit, kCutoff))) * r.unit / double(kept));
 }
 
 // ---- one workgroup per row
@@ -763,13 +792,12 @@ __global__ __launch_bounds__(kRowThreads) void sample_row_kernel(const SampleArg
   __shared__ uint64_t list[kLdsList];
   __shared__ uint64_t red[2 * kRowThreads / kWave];
   __shared__ PickLds s;
-  __shared__ uint32_t listed;
+  __shared__ uint32_t listed[kRowThreads / kWave];
   const int row = blockIdx.x;
   const Given given = load_given(a, row);
   const RowView<FMT> v(a.logits, a.stride, row, a.V);
 #pragma unroll
   for (int j = 0; j < PER; ++j) mass[j * kRowThreads + threadIdx.x] = 0;
-  if (threadIdx.x == 0) listed = 0;
   const uint64_t top = largest_key<FMT>(v, 0, v.vecs, red);
   const Row r = make_row(a, given, top);
   if (r.greedy) {
@@ -787,49 +815,41 @@ __global__ __launch_bounds__(kRowThreads) void sample_row_kernel(const SampleArg
   int lo[3], hi[3];
   bound_targets<PER>(r, packed, mass, count, red, lo, hi);
   const Wanted wanted(r, lo, hi);
-  // the wanted tokens, as far as they fit
-  for_slice<FMT>(v, 0, v.vecs, [&](const float (&x)[4], int first, bool in) {
-    const int lane = threadIdx.x & 63;
-    bool want[4];
-    if (!wanted.four(r, x, in, want)) return;
-    uint64_t mask[4];
-    uint32_t n = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      mask[j] = __ballot(want[j]);
-      n += uint32_t(__popcll(mask[j]));
-    }
-    if (n == 0) return;
-    uint32_t at = 0;
-    if (lane == 0) at = atomicAdd(&listed, n);
-    at = __shfl(at, 0, kWave);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t k = at + uint32_t(__popcll(mask[j] & ((uint64_t(1) << lane) - 1)));
-      if (want[j] && k < uint32_t(kLdsList)) list[k] = key_of(x[j], first + j);
-      at += uint32_t(__popcll(mask[j]));
-    }
-  });
+  // the wanted tokens, every wave's in its own segment
+  constexpr int kWaves = kRowThreads / kWave, kRoom = kLdsList / kWaves;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  uint64_t* segment = list + wave * kRoom;
+  const uint32_t mine = list_wanted<FMT>(r, wanted, v, 0, v.vecs, segment, kRoom,
+                                         [](uint32_t n) { return n; });
+  if (lane == 0) listed[wave] = mine;
   __syncthreads();
-  const uint32_t n = listed;
+  uint32_t n = 0, before = 0, most = 0;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    before += w < wave ? listed[w] : 0;
+    n += listed[w];
+    most = max(most, listed[w]);
+  }
   auto mass_before = [&](int b) { return b ? mass[b - 1] : uint64_t(0); };
   auto count_before = [&](int b) { return b ? count[b - 1] : 0u; };
   uint64_t key, kept;
   if (n <= uint32_t(kWave)) {
-    if (threadIdx.x >= kWave) return;
+    if (uint32_t(lane) < mine) s.few[before + lane] = segment[lane];
+    __syncthreads();
+    if (wave > 0) return;
     key = draw_token_wave(r, lo, hi, mass[kBins - 1], mass_before, count_before, n,
-                          threadIdx.x < n ? list[threadIdx.x] : 0, &kept);
-  } else if (n <= uint32_t(kLdsList)) {
+                          uint32_t(lane) < n ? s.few[lane] : 0, &kept);
+  } else if (most <= uint32_t(kRoom)) {
     key = draw_token(r, lo, hi, mass[kBins - 1], mass_before, count_before, s, &kept, [&](auto&& f) {
 #pragma unroll 1
-      for (uint32_t k = threadIdx.x; k - (threadIdx.x & 63) < n; k += kRowThreads)
-        f(k < n ? list[k] : 0, k < n);
+      for (uint32_t k = 0; k < mine; k += kWave)
+        f(k + lane < mine ? segment[k + lane] : 0, k + lane < mine);
     });
   } else {
     // more candidates than the list holds (long runs of equal logits): the row itself
     key = draw_token(r, lo, hi, mass[kBins - 1], mass_before, count_before, s, &kept, [&](auto&& f) {
 #pragma unroll 1
-      for (int i = threadIdx.x; i - int(threadIdx.x & 63) < a.V; i += kRowThreads) {
+      for (int i = threadIdx.x; i - lane < a.V; i += kRowThreads) {
         const float x = i < a.V ? v.at(i) : -__builtin_inff();
         f(key_of(x, i), i < a.V && wanted(r, x));
       }
@@ -958,18 +978,25 @@ __global__ __launch_bounds__(kThreads) void sample_pick_kernel(const SampleArgs 
   const RowView<FMT> v(a.logits, a.stride, row, a.V);
   const int per = (v.vecs + a.parts - 1) / a.parts;
   const int begin = int(blockIdx.x) * per, end = min(v.vecs, begin + per);
-  list_wanted<FMT>(r, wanted, v, begin, end, space, [&](const uint64_t* keys, uint32_t n) {
+  {
+    constexpr uint32_t kRoom = kLdsList / (kThreads / kWave);
     const int lane = threadIdx.x & 63;
-    uint32_t at = 0;
-    if (lane == 0)
-      at = __hip_atomic_fetch_add(&ctl.listed, n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    at = __shfl(at, 0, kWave);
-    __builtin_amdgcn_wave_barrier();   // the segment's writes stay in front of its reads
+    uint64_t* segment = space + (threadIdx.x >> 6) * kRoom;
+    auto empty = [&](uint32_t n) {
+      uint32_t at = 0;
+      if (lane == 0)
+        at = __hip_atomic_fetch_add(&ctl.listed, n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      at = __shfl(at, 0, kWave);
+      __builtin_amdgcn_wave_barrier();   // the segment's writes stay in front of its reads
 #pragma unroll 1
-    for (uint32_t k = lane; k < n; k += kWave)
-      if (at + k < uint32_t(kListCap)) put(&list[at + k], keys[k]);
-    __builtin_amdgcn_wave_barrier();
-  });
+      for (uint32_t k = lane; k < n; k += kWave)
+        if (at + k < uint32_t(kListCap)) put(&list[at + k], segment[k]);
+      __builtin_amdgcn_wave_barrier();
+      return 0u;
+    };
+    const uint32_t n = list_wanted<FMT>(r, wanted, v, begin, end, segment, kRoom, empty);
+    if (n) empty(n);
+  }
   if (!arrive_last(&ctl.pick_done, a.parts, &flag)) return;
 
   const uint64_t* gm = w.mass + int64_t(row) * (kBins + 1);
