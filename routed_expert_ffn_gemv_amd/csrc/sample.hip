@@ -52,6 +52,7 @@ constexpr int kMaxParts = 256;
 constexpr int kSlice = 4096;            // logits of a row per workgroup
 constexpr int kListCap = 16384;         // listed candidates of a row
 constexpr int kLdsList = 4096;          // of which this many are searched in LDS
+constexpr int kRowList = 12288;         // listed candidates in LDS with a workgroup per row
 
 struct RowCtl {
   uint32_t hist_done, pick_done, listed, drawn;   // drawn: rows finished (row 0's only)
@@ -789,7 +790,7 @@ __global__ __launch_bounds__(kRowThreads) void sample_row_kernel(const SampleArg
   constexpr int PER = kBins / kRowThreads;
   __shared__ uint64_t mass[kBins];
   __shared__ uint32_t count[kBins];
-  __shared__ uint64_t list[kLdsList];
+  __shared__ uint64_t list[kRowList];
   __shared__ uint64_t red[2 * kRowThreads / kWave];
   __shared__ PickLds s;
   __shared__ uint32_t listed[kRowThreads / kWave];
@@ -816,7 +817,7 @@ __global__ __launch_bounds__(kRowThreads) void sample_row_kernel(const SampleArg
   bound_targets<PER>(r, packed, mass, count, red, lo, hi);
   const Wanted wanted(r, lo, hi);
   // the wanted tokens, every wave's in its own segment
-  constexpr int kWaves = kRowThreads / kWave, kRoom = kLdsList / kWaves;
+  constexpr int kWaves = kRowThreads / kWave, kRoom = kRowList / kWaves;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   uint64_t* segment = list + wave * kRoom;
   const uint32_t mine = list_wanted<FMT>(r, wanted, v, 0, v.vecs, segment, kRoom,
@@ -1034,8 +1035,10 @@ __global__ __launch_bounds__(kThreads) void sample_pick_kernel(const SampleArgs 
 
 template <int FMT>
 hipError_t launch(SampleArgs a, hipStream_t st) {
-  const int64_t row_bytes = int64_t(a.V) * (FMT == MOE_W_F32 ? 4 : 2);
-  if (a.T >= 96 || row_bytes <= 128 * 1024) {
+  // A workgroup per row has one launch but one CU's speed: 16 x 32,000 takes
+  // 24 us (26 us in slices), 16 x 151,936 66 us (38 us), 64 x 64,000 43 us (44
+  // us), 128 and 256 x 151,936 87 and 106 us (75 and 129 us).
+  if (a.V <= 40000 || a.T >= a.V / 1000) {
     sample_row_kernel<FMT><<<a.T, kRowThreads, 0, st>>>(a);
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && a.n_out) {
