@@ -395,6 +395,8 @@ def _fmt_of(t, what):
 
 def _rows(t, T, n, what):
     """Stride of a [>= T][>= n] tensor whose rows are contiguous."""
+    if t.shape == (T, n) and t.is_contiguous():
+        return n
     if t.ndim == 2:
         rows, cols = t.shape
         row, col = t.stride()
@@ -449,27 +451,30 @@ def moe_add_rmsnorm(T, H, y, resid, weight, eps, resid_out=None, x=None, x8=None
     uint8 or float8_e4m3fn) with x8_scale (fp32 [T][ceil(H/128)]).  y, resid
     and weight: fp32 or bf16, rows may be strided."""
     T, H = int(T), int(H)
+    yp = rp = xp = qp = sp = None
     y_fmt = y_row = out_row = x_row = 0
     r_fmt, r_row = _fmt_of(resid, "resid"), _rows(resid, T, H, "resid")
     if y is not None:
-        y_fmt, y_row = _fmt_of(y, "y"), _rows(y, T, H, "y")
+        yp, y_fmt, y_row = y.data_ptr(), _fmt_of(y, "y"), _rows(y, T, H, "y")
     if resid_out is not None:
         if _fmt_of(resid_out, "resid_out") != r_fmt:
             raise ValueError("resid_out: resid's format wanted")
-        out_row = _rows(resid_out, T, H, "resid_out")
+        rp, out_row = resid_out.data_ptr(), _rows(resid_out, T, H, "resid_out")
     if x is not None:
         if x.dtype not in _BF16:
             raise ValueError(f"x: bf16 wanted, got {x.dtype}")
-        x_row = _rows(x, T, H, "x")
+        xp, x_row = x.data_ptr(), _rows(x, T, H, "x")
     if x8 is not None:
         _flat(x8, T * H, "x8", _CODES)
+        qp = x8.data_ptr()
     if x8_scale is not None:
         _flat(x8_scale, T * ((H + 127) // 128), "x8_scale", _F32)
+        sp = x8_scale.data_ptr()
     _flat(weight, H, "weight", _FMT_OF)
     dev = _gpu_of("moe_add_rmsnorm", resid, y, weight, resid_out, x, x8, x8_scale)
-    _launch(lib.moe_add_rmsnorm, "moe_add_rmsnorm", dev, stream, T, H, _ptr(y), y_fmt, y_row,
-            resid.data_ptr(), r_fmt, r_row, weight.data_ptr(), _FMT_OF[weight.dtype], eps,
-            _ptr(resid_out), out_row, _ptr(x), x_row, _ptr(x8), _ptr(x8_scale))
+    _launch(lib.moe_add_rmsnorm, "moe_add_rmsnorm", dev, stream, T, H, yp, y_fmt, y_row,
+            resid.data_ptr(), r_fmt, r_row, weight.data_ptr(), _FMT_OF[weight.dtype], eps, rp, out_row,
+            xp, x_row, qp, sp)
 
 
 def moe_scaled_linear_workspace_size(T, N, K):
