@@ -409,13 +409,13 @@ moe_status moe_add_rmsnorm(int32_t T, int32_t H, const void* y, int32_t y_fmt, i
  * Codes are OCP e4m3 (no infinities; a NaN code makes the sums it enters
  * NaN), scales fp32, all contiguous.  out is MOE_W_F32 or MOE_W_BF16 (rounded
  * once), out_stride elements from row to row (>= N).  Sums are fp32; for
- * bf16 outputs of more than 16 tokens the hardware's 8-bit products are used,
- * which add eight neighbouring ones with 13 bits below the largest of them.
+ * bf16 outputs of more than 16 tokens the hardware's 8-bit products may be
+ * used, which add eight neighbouring ones with 13 bits below the largest.
  * x8 and w8 16-byte aligned, K a multiple of 16, else MOE_ERR_INVALID; N and
- * T are arbitrary.  The order of the sums depends on (T, N, K) alone: calls
- * of one shape give identical bits.  Limits: K <= 32768, N <= 2^24, T <= 2^22.
- * ws: moe_scaled_linear_workspace_size bytes (0 for most shapes; ws may then
- * be NULL), 256-byte aligned, in use by one call at a time. */
+ * T are arbitrary.  The order of the sums depends on (T, N, K) and out_fmt alone:
+ * calls of one shape give identical bits.  Limits: K <= 32768, N <= 2^24, T <= 2^22.
+ * ws: moe_scaled_linear_workspace_size bytes (at present 0 for every shape;
+ * ws may then be NULL), 256-byte aligned, in use by one call at a time. */
 moe_status moe_scaled_linear_workspace_size(int32_t T, int32_t N, int32_t K, size_t* bytes);
 moe_status moe_scaled_linear(const uint8_t* x8, const float* x_scale, int32_t T,
                              const uint8_t* w8, const float* w_scale, int32_t N, int32_t K,

@@ -150,7 +150,7 @@ struct LinearArgs {
   void* out;                   // [T] rows of N
   int T, N, K, out_fmt;
   int64_t out_stride;
-  bool wide_out;               // rows allow 16-byte stores (set by the launcher)
+  int wide_out;                // stores that rows allow: 2: 16 bytes, 1: 8, 0: elements (set by the launcher)
 };
 hipError_t launch_scaled_linear(LinearArgs a, hipStream_t st);
 

@@ -97,6 +97,18 @@ def test_large(T, N):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,N", [
+    (20, 500), (40, 1500), (9, 9001), (13, 16400), (1, 20004), (200, 1004), (400, 1001),     # operands in registers
+    (17, 17003), (32, 33004), (33, 33001), (50, 60004),                                      # one tile of tokens
+    (777, 1000), (310, 4100), (129, 10001), (300, 14004), (1201, 4100), (3900, 4001),        # more
+])
+def test_every_shape_of_workgroup(T, N, dtype):
+    """Sizes that end inside every kernel's tiles, one to three blocks."""
+    for K in (48, 272):
+        _check(*_inputs(T, N, K, T + N + K), dtype=dtype, pad=4 if N % 4 == 0 else 3)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("pad,off", [(0, 0), (4, 0), (1, 0), (8, 1), (3, 2)])
 def test_formats_strides_and_alignment(dtype, pad, off):
     for T, N in ((4, 260), (90, 258)):
