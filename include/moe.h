@@ -58,7 +58,7 @@ typedef enum {
  * weight affine block is this library's definition. */
 typedef enum {
   MOE_W_F32 = 0,   /* fp32, [rows][cols] */
-  MOE_W_BF16 = 1,  /* bf16 bits, [rows][cols] (router only) */
+  MOE_W_BF16 = 1,  /* bf16 bits, [rows][cols] (router, activations, logits) */
   MOE_W_Q2B32 = 2, /* 2-bit codes, 3.0 bits per weight with scale and min */
   MOE_W_Q4B32 = 3  /* 4-bit codes, 5.0 bits per weight with scale and min */
 } moe_wfmt;

@@ -294,7 +294,7 @@ struct Row {
   double top64;       // the largest logit, 0 if that is infinite
   double bins;        // bins per logit
   double limit;       // place beyond which nothing is drawn (min-p, kCutoff)
-  double v0, v1, v2, v3, v4;   // S v as a power series of the place's distance from the bin's middle
+  double v0, v1, v2, v3;      // S v as a polynomial of the place's distance from the bin's middle
   double inv_s;       // 1 / S
   double unit;        // 2^s
   uint64_t q_mask;
@@ -359,7 +359,8 @@ __device__ Row make_row(const SampleArgs& a, const Given& g, uint64_t top_key) {
     r.limit = fmin(r.limit, (d - (m / exp_minus(d) - 1.0)) * kBinsPerUnit);
   }
   r.limit -= 0.5;
-  // v = 1 - exp(-(f + 1/2) / 96), to f^4 (the rest is below 1e-13), and S
+  // v = 1 - exp(-(f + 1/2) / 96), |f| <= 1/2, to f^3, and S; f^4 as f^2 / 4 -
+  // 1 / 128, which is within 1 / 128 of it there (4e-12 of v's unit)
   const double s = __longlong_as_double((int64_t)(1023 + a.frac_bits + 6) << 52);   // v < 2^-6 * 0.67
   const double middle = 0x1.fd571ba7c4ef1p-1;                                        // exp(-1 / 192)
   r.inv_s = 1.0 / s;
@@ -367,7 +368,9 @@ __device__ Row make_row(const SampleArgs& a, const Given& g, uint64_t top_key) {
   r.v1 = s * middle / kBinsPerUnit;
   r.v2 = r.v1 / (-2.0 * kBinsPerUnit);
   r.v3 = r.v2 / (-3.0 * kBinsPerUnit);
-  r.v4 = r.v3 / (-4.0 * kBinsPerUnit);
+  const double v4 = r.v3 / (-4.0 * kBinsPerUnit);
+  r.v2 += 0.25 * v4;
+  r.v0 -= v4 / 128.0;
   r.unit = __longlong_as_double((int64_t)(1023 + a.shift) << 52);
   r.q_bits = a.q_bits;
   r.q_mask = (uint64_t(1) << a.q_bits) - 1;
@@ -400,8 +403,7 @@ __device__ __forceinline__ float logit_bound(const Row& r, double t, double side
 // A token adds this to its bin: a count of one, and q.
 __device__ __forceinline__ uint64_t packed_of(const Row& r, double place) {
   const double f = place - ((place + kToInt) - kToInt);
-  double q = fma(r.v4, f, r.v3);
-  q = fma(q, f, r.v2);
+  double q = fma(r.v3, f, r.v2);
   q = fma(q, f, r.v1);
   q = fma(q, f, r.v0);
   return (uint64_t(1u << (r.q_bits - 32)) << 32) | uint64_t(uint32_t(__double_as_longlong(q + kToInt)));
@@ -447,7 +449,9 @@ __device__ __forceinline__ uint64_t largest_key(const RowView<FMT>& v, int begin
   return block_max(best > -__builtin_inff() ? key_of(best, at) : 0, red);
 }
 
-// Adds the tokens of vectors [begin, end) to the bins in LDS.
+// Adds the tokens of vectors [begin, end) to the bins in LDS.  Bound by the
+// LDS atomics, which meet in the dense bins (151,936 tokens: 27 us of one CU,
+// 14 where min-p leaves few; without branches, four tokens at a time, the same).
 template <int FMT>
 __device__ __forceinline__ void fill_bins(const Row& r, const RowView<FMT>& v, int begin, int end,
                                           uint64_t* bins) {
@@ -528,62 +532,87 @@ __device__ __forceinline__ void bound_targets(const Row& r, const uint64_t* pack
   hi[2] = first_reaching(mass, draw_target(r.u, z1));
 }
 
-// Whether a token lies in one of the bins that matter.
+// Which tokens matter: those of the bins [lo, hi], and few others.
 struct Wanted {
-  int lo[3], hi[3];
-  float from[3], to[3];      // every wanted logit lies in one of these ranges (not only those)
-  float lowest;              // and at or above this
-  __device__ Wanted(const Row& r, const int* l, const int* h) {
+  // every logit x of the bins of question q has |x scale - middle| <= kNear
+  // (and few others do): the half width is 2^-18 of the logits there at
+  // least, so that scale, middle and the fma are off by 2^-6 each at most
+  static constexpr float kNear = 1.0625f;
+  float scale[3], middle[3];
+  float lowest;              // and is at or above this
+  bool asked[2];             // questions 0 and 1
+  bool open;                 // a range has no end: infinities could pass
+  __device__ Wanted(const Row& r, const int* lo, const int* hi) {
+    open = false;
+    lowest = __builtin_inff();
 #pragma unroll
     for (int q = 0; q < 3; ++q) {
-      lo[q] = l[q], hi[q] = h[q];
-      from[q] = hi[q] < lo[q] ? __builtin_inff() : logit_bound(r, double(hi[q] + 1), -1.0);
-      to[q] = hi[q] < lo[q] ? __builtin_inff() : logit_bound(r, double(lo[q]), 1.0);
+      if (q < 2) asked[q] = hi[q] >= lo[q];
+      scale[q] = middle[q] = 0.0f;
+      if (hi[q] < lo[q]) continue;
+      const float from = logit_bound(r, double(hi[q] + 1), -1.0), to = logit_bound(r, double(lo[q]), 1.0);
+      const float c = 0.5f * from + 0.5f * to;
+      const float half = fmaxf(0.5f * to - 0.5f * from, fmaxf(fabsf(c) * 0x1p-18f, 0x1p-100f));
+      scale[q] = 1.0f / half;
+      middle[q] = c / half;
+      lowest = fminf(lowest, from);
+      open |= from == -__builtin_inff();
     }
-    lowest = fminf(fminf(from[0], from[1]), from[2]);
   }
-  // 0 if x lies in one of the ranges: its distance from the nearest
-  __device__ __forceinline__ float outside(float x) const {
-    const float a = fabsf(__builtin_amdgcn_fmed3f(x, from[0], to[0]) - x);
-    const float b = fabsf(__builtin_amdgcn_fmed3f(x, from[1], to[1]) - x);
-    const float c = fabsf(__builtin_amdgcn_fmed3f(x, from[2], to[2]) - x);
-    return fminf(fminf(a, b), c);
-  }
+  // at most kNear: x is wanted (NaN is not)
+  __device__ __forceinline__ float away(int q, float x) const { return fabsf(fmaf(x, scale[q], -middle[q])); }
   __device__ __forceinline__ bool operator()(const Row& r, float x) const {
-    const double place = place_of(r, seen(r, x));
-    if (!(place <= r.limit)) return false;
-    const int b = bin_at(place);
-    return (b >= lo[0] && b <= hi[0]) || (b >= lo[1] && b <= hi[1]) || (b >= lo[2] && b <= hi[2]);
+    if (open) return place_of(r, seen(r, x)) <= r.limit;
+    return away(2, x) <= kNear || (asked[1] && away(1, x) <= kNear) || (asked[0] && away(0, x) <= kNear);
   }
 };
 
 // Lists the wanted tokens of vectors [begin, end): each wave fills its own
 // segment (LDS, room keys) and calls full(n) before it would overflow, which
 // returns how many it still holds.  Returns the number in the segment.
+// Tokens of bins next to the wanted ones may be listed, in part, and tokens
+// beyond the limit: the sums through the former miss every target, and the
+// latter are left out where candidates are used.  (A row of 151,936 with 1000
+// candidates: 25 us; 36 with the exact bins, in 64 bits, here.)
 template <int FMT, class Full>
 __device__ __forceinline__ uint32_t list_wanted(const Row& r, const Wanted& wanted, const RowView<FMT>& v,
                                                 int begin, int end, uint64_t* segment, uint32_t room,
                                                 const Full& full) {
-  const uint64_t below = (uint64_t(1) << (threadIdx.x & 63)) - 1;
+  const uint64_t self = uint64_t(1) << (threadIdx.x & 63), below = self - 1;
   uint32_t n = 0;
   for_slice<FMT, 2>(v, begin, end, [&](const float (&x)[4], int first, bool in) {
-    // (NaN and -infinity fail the first comparison; equal infinities have
-    // no distance, and pass the second)
+    // (NaN and -infinity fail the comparison, where the ranges have ends)
     const bool high = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) >= wanted.lowest;
     if (__ballot(in && high) == 0) return;
     float off[4];
+    if (__builtin_expect(wanted.open, 0)) {
+      asm volatile("");      // a branch, not four selections
 #pragma unroll
-    for (int j = 0; j < 4; ++j) off[j] = wanted.outside(x[j]);
-    if (__ballot(in && !(fminf(fminf(off[0], off[1]), fminf(off[2], off[3])) > 0.0f)) == 0) return;
+      for (int j = 0; j < 4; ++j) off[j] = wanted(r, x[j]) ? 0.0f : 2.0f;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) off[j] = wanted.away(2, x[j]);
+      if (wanted.asked[1]) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) off[j] = fminf(off[j], wanted.away(1, x[j]));
+      }
+      if (wanted.asked[0]) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) off[j] = fminf(off[j], wanted.away(0, x[j]));
+      }
+    }
+    const float least = fminf(fminf(off[0], off[1]), fminf(off[2], off[3]));
+    if (__ballot(in && least <= Wanted::kNear) == 0) return;
+    uint64_t mask[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) mask[j] = __ballot(in && off[j] <= Wanted::kNear);
     if (n + 4 * kWave > room) n = full(n);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      bool want = in && !(off[j] > 0.0f);
-      if (want) want = wanted(r, x[j]);
-      const uint64_t mask = __ballot(want);
-      const uint32_t at = n + uint32_t(__popcll(mask & below));
-      if (want && at < room) segment[at] = key_of(x[j], first + j);
-      n += uint32_t(__popcll(mask));
+      if (mask[j] == 0) continue;
+      const uint32_t at = n + uint32_t(__popcll(mask[j] & below));
+      if ((mask[j] & self) && at < room) segment[at] = key_of(x[j], first + j);
+      n += uint32_t(__popcll(mask[j]));
     }
   });
   return n;
@@ -640,7 +669,7 @@ __device__ __forceinline__ uint64_t draw_token(const Row& r, const int* lo, cons
     auto part_of = [](double place) { return min(int(within(place) * 256.0), 255); };
     auto active = [&](uint64_t key, double* place) {
       *place = place_of(r, seen(r, logit_of(key)));
-      return bin_at(*place) == bin && (part < 0 || part_of(*place) == part) &&
+      return *place <= r.limit && bin_at(*place) == bin && (part < 0 || part_of(*place) == part) &&
              (sh == 64 || (key >> sh) == prefix);
     };
 #pragma unroll 1
@@ -747,6 +776,7 @@ __device__ __forceinline__ uint64_t draw_token_wave(const Row& r, const int* lo,
                                                     uint64_t* kept) {
   const int lane = threadIdx.x & 63;
   const double place = place_of(r, seen(r, logit_of(key)));
+  if (!(place <= r.limit)) key = 0;
   const int my_bin = key ? bin_at(place) : -1;
   const uint64_t mine = key ? packed_of(r, place) : 0;
   // packed sum of the candidates of this one's bin in front of it
@@ -1036,8 +1066,8 @@ __global__ __launch_bounds__(kThreads) void sample_pick_kernel(const SampleArgs 
 template <int FMT>
 hipError_t launch(SampleArgs a, hipStream_t st) {
   // A workgroup per row has one launch but one CU's speed: 16 x 32,000 takes
-  // 24 us (26 us in slices), 16 x 151,936 66 us (38 us), 64 x 64,000 43 us (44
-  // us), 128 and 256 x 151,936 87 and 106 us (75 and 129 us).
+  // 24 us (26 us in slices), 16 x 151,936 62 us (39 us), 64 x 64,000 40 us (44
+  // us), 128 and 256 x 151,936 75 and 94 us (73 and 125 us).
   if (a.V <= 40000 || a.T >= a.V / 1000) {
     sample_row_kernel<FMT><<<a.T, kRowThreads, 0, st>>>(a);
     hipError_t e = hipGetLastError();
