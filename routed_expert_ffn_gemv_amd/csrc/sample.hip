@@ -51,20 +51,18 @@ constexpr double kCutoff = 42.0;        // units below the largest logit from wh
 constexpr int kMaxParts = 256;
 constexpr int kSlice = 4096;            // logits of a row per workgroup
 constexpr int kListCap = 16384;         // listed candidates of a row
-constexpr int kLdsList = 4096;          // of which this many are searched in LDS
+constexpr int kLdsList = 3072;          // of which this many are searched in LDS
 constexpr int kRowList = 12288;         // listed candidates in LDS with a workgroup per row
 
 struct RowCtl {
-  uint32_t hist_done, pick_done, listed, drawn;   // drawn: rows finished (row 0's only)
-  int32_t lo[3], hi[3];       // bins in which the three targets can fall (hi < lo: not asked)
+  uint32_t pick_done, listed, drawn;   // drawn: rows finished (row 0's only)
 };
 
 // The workspace, from SampleArgs.ws (256-byte aligned).
 struct Ws {
   uint64_t* part;    // [T][kMaxParts] largest keys of the slices
   RowCtl* ctl;       // [T]
-  uint64_t* mass;    // [T][kBins + 1] packed sums per bin, later the masses' exclusive prefix
-  uint32_t* count;   // [T][kBins + 1] the counts' exclusive prefix
+  uint64_t* bins;    // [T][kBins] packed sums per bin
   uint64_t* list;    // [T][kListCap] candidates' keys
 };
 
@@ -79,8 +77,7 @@ __host__ __device__ inline size_t ws_layout(int T, uint8_t* base, Ws* w) {
   };
   w->part = reinterpret_cast<uint64_t*>(take(size_t(T) * kMaxParts * 8));
   w->ctl = reinterpret_cast<RowCtl*>(take(size_t(T) * sizeof(RowCtl)));
-  w->mass = reinterpret_cast<uint64_t*>(take(size_t(T) * (kBins + 1) * 8));
-  w->count = reinterpret_cast<uint32_t*>(take(size_t(T) * (kBins + 1) * 4));
+  w->bins = reinterpret_cast<uint64_t*>(take(size_t(T) * kBins * 8));
   w->list = reinterpret_cast<uint64_t*>(take(size_t(T) * kListCap * 8));
   return o;
 }
@@ -916,10 +913,9 @@ __global__ __launch_bounds__(kThreads) void sample_max_kernel(const SampleArgs a
   Ws w;
   ws_layout(a.T, static_cast<uint8_t*>(a.ws), &w);
   const int p = blockIdx.x, row = blockIdx.y;
-  const int per_bins = (kBins + 1 + a.parts - 1) / a.parts;
-  const int b1 = min(kBins + 1, (p + 1) * per_bins);
-  for (int b = p * per_bins + threadIdx.x; b < b1; b += kThreads)
-    w.mass[int64_t(row) * (kBins + 1) + b] = 0;
+  const int per_bins = (kBins + a.parts - 1) / a.parts;
+  const int b1 = min(kBins, (p + 1) * per_bins);
+  for (int b = p * per_bins + threadIdx.x; b < b1; b += kThreads) w.bins[int64_t(row) * kBins + b] = 0;
   if (p == 0 && threadIdx.x < sizeof(RowCtl) / 4)
     reinterpret_cast<uint32_t*>(&w.ctl[row])[threadIdx.x] = 0;
   const RowView<FMT> v(a.logits, a.stride, row, a.V);
@@ -928,43 +924,27 @@ __global__ __launch_bounds__(kThreads) void sample_max_kernel(const SampleArgs a
   if (threadIdx.x == 0) w.part[int64_t(row) * kMaxParts + p] = k;
 }
 
-// 2. Sums per bin, then the bins that matter.
+// 2. Sums per bin.
 template <int FMT>
 __global__ __launch_bounds__(kThreads) void sample_hist_kernel(const SampleArgs a) {
   constexpr int PER = kBins / kThreads;
-  __shared__ uint64_t mass[kBins];
-  __shared__ uint32_t count[kBins];
+  __shared__ uint64_t bins[kBins];
   __shared__ uint64_t red[2 * kThreads / kWave];
-  __shared__ uint32_t flag;
   Ws w;
   ws_layout(a.T, static_cast<uint8_t*>(a.ws), &w);
   const int row = blockIdx.y;
 #pragma unroll
-  for (int j = 0; j < PER; ++j) mass[j * kThreads + threadIdx.x] = 0;
+  for (int j = 0; j < PER; ++j) bins[j * kThreads + threadIdx.x] = 0;
   const Row r = read_row(a, w, row, red);
   if (r.greedy) return;
   const RowView<FMT> v(a.logits, a.stride, row, a.V);
   const int per = (v.vecs + a.parts - 1) / a.parts;
-  fill_bins<FMT>(r, v, int(blockIdx.x) * per, min(v.vecs, (int(blockIdx.x) + 1) * per), mass);
+  fill_bins<FMT>(r, v, int(blockIdx.x) * per, min(v.vecs, (int(blockIdx.x) + 1) * per), bins);
   __syncthreads();
-  uint64_t* gm = w.mass + int64_t(row) * (kBins + 1);
-  uint32_t* gc = w.count + int64_t(row) * (kBins + 1);
+  uint64_t* sums = w.bins + int64_t(row) * kBins;
 #pragma unroll 1
   for (int b = threadIdx.x; b < kBins; b += kThreads)
-    if (mass[b]) __hip_atomic_fetch_add(&gm[b], mass[b], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  if (!arrive_last(&w.ctl[row].hist_done, a.parts, &flag)) return;
-  uint64_t packed[PER];
-#pragma unroll
-  for (int j = 0; j < PER; ++j) packed[j] = get(&gm[threadIdx.x * PER + j]);
-  int lo[3], hi[3];
-  bound_targets<PER>(r, packed, mass, count, red, lo, hi);
-#pragma unroll 1
-  for (int b = threadIdx.x; b < kBins; b += kThreads) gm[b + 1] = mass[b], gc[b + 1] = count[b];
-  if (threadIdx.x == 0) {
-    gm[0] = 0, gc[0] = 0;
-#pragma unroll
-    for (int q = 0; q < 3; ++q) w.ctl[row].lo[q] = lo[q], w.ctl[row].hi[q] = hi[q];
-  }
+    if (bins[b]) __hip_atomic_fetch_add(&sums[b], bins[b], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
 // A finished row: its token; with drafts, the last row to finish counts the
@@ -984,9 +964,13 @@ __device__ void finish_row(const SampleArgs& a, const Ws& w, int row, int token,
   }
 }
 
-// 3. The tokens of those bins, and the three answers.
+// 3. The bins that matter (every workgroup finds them for itself: one hand-over
+// less), their tokens, and the three answers.
 template <int FMT>
 __global__ __launch_bounds__(kThreads) void sample_pick_kernel(const SampleArgs a) {
+  constexpr int PER = kBins / kThreads;
+  __shared__ uint64_t mass[kBins];
+  __shared__ uint32_t count[kBins];
   __shared__ uint64_t space[kLdsList];
   __shared__ uint64_t red[2 * kThreads / kWave];
   __shared__ PickLds s;
@@ -995,15 +979,17 @@ __global__ __launch_bounds__(kThreads) void sample_pick_kernel(const SampleArgs 
   ws_layout(a.T, static_cast<uint8_t*>(a.ws), &w);
   const int row = blockIdx.y;
   RowCtl& ctl = w.ctl[row];
-  int lo[3], hi[3];
+  uint64_t packed[PER];
 #pragma unroll
-  for (int q = 0; q < 3; ++q) lo[q] = ctl.lo[q], hi[q] = ctl.hi[q];
+  for (int j = 0; j < PER; ++j) packed[j] = w.bins[int64_t(row) * kBins + threadIdx.x * PER + j];
   const Row r = read_row(a, w, row, red);
   if (r.greedy) {
     if (blockIdx.x == 0)
       finish_row(a, w, row, r.top_key ? index_of(r.top_key) : -1, r.top_key ? 1.0f : 0.0f, &flag);
     return;
   }
+  int lo[3], hi[3];
+  bound_targets<PER>(r, packed, mass, count, red, lo, hi);
   const Wanted wanted(r, lo, hi);
   uint64_t* list = w.list + int64_t(row) * kListCap;
   const RowView<FMT> v(a.logits, a.stride, row, a.V);
@@ -1030,28 +1016,26 @@ __global__ __launch_bounds__(kThreads) void sample_pick_kernel(const SampleArgs 
   }
   if (!arrive_last(&ctl.pick_done, a.parts, &flag)) return;
 
-  const uint64_t* gm = w.mass + int64_t(row) * (kBins + 1);
-  const uint32_t* gc = w.count + int64_t(row) * (kBins + 1);
   const uint32_t n = get(&ctl.listed);
-  auto mass_before = [&](int b) { return gm[b]; };
-  auto count_before = [&](int b) { return gc[b]; };
+  auto mass_before = [&](int b) { return b ? mass[b - 1] : uint64_t(0); };
+  auto count_before = [&](int b) { return b ? count[b - 1] : 0u; };
   uint64_t key, kept;
   if (n <= uint32_t(kWave)) {
     const uint32_t i = threadIdx.x & 63;      // (every wave finds the same)
-    key = draw_token_wave(r, lo, hi, gm[kBins], mass_before, count_before, n,
+    key = draw_token_wave(r, lo, hi, mass[kBins - 1], mass_before, count_before, n,
                           i < n ? get(&list[i]) : 0, &kept);
   } else if (n <= uint32_t(kListCap)) {
     const bool in_lds = n <= uint32_t(kLdsList);
     if (in_lds)
       for (uint32_t k = threadIdx.x; k < n; k += kThreads) space[k] = get(&list[k]);
-    key = draw_token(r, lo, hi, gm[kBins], mass_before, count_before, s, &kept, [&](auto&& f) {
+    key = draw_token(r, lo, hi, mass[kBins - 1], mass_before, count_before, s, &kept, [&](auto&& f) {
 #pragma unroll 1
       for (uint32_t k = threadIdx.x; k - (threadIdx.x & 63) < n; k += kThreads)
         f(k >= n ? 0 : in_lds ? space[k] : get(&list[k]), k < n);
     });
   } else {
     // more candidates than the list holds (long runs of equal logits): the row itself
-    key = draw_token(r, lo, hi, gm[kBins], mass_before, count_before, s, &kept, [&](auto&& f) {
+    key = draw_token(r, lo, hi, mass[kBins - 1], mass_before, count_before, s, &kept, [&](auto&& f) {
 #pragma unroll 1
       for (int i = threadIdx.x; i - int(threadIdx.x & 63) < a.V; i += kThreads) {
         const float x = i < a.V ? v.at(i) : -__builtin_inff();
@@ -1066,9 +1050,10 @@ __global__ __launch_bounds__(kThreads) void sample_pick_kernel(const SampleArgs 
 template <int FMT>
 hipError_t launch(SampleArgs a, hipStream_t st) {
   // A workgroup per row has one launch but one CU's speed: 16 x 32,000 takes
-  // 24 us (26 us in slices), 16 x 151,936 62 us (39 us), 64 x 64,000 40 us (44
-  // us), 128 and 256 x 151,936 75 and 94 us (73 and 125 us).
-  if (a.V <= 40000 || a.T >= a.V / 1000) {
+  // 24 us (25 us in slices), 16 x 151,936 61 us (29 us), 64 x 48,000 34 us (34
+  // us), 128 x 64,000 44 us (46 us), 128 and 256 x 151,936 75 and 94 us (64 and
+  // 108 us).
+  if (a.V <= 36000 || a.T >= a.V / 650) {
     sample_row_kernel<FMT><<<a.T, kRowThreads, 0, st>>>(a);
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && a.n_out) {
@@ -1077,10 +1062,11 @@ hipError_t launch(SampleArgs a, hipStream_t st) {
     }
     return e;
   }
-  // a slice per workgroup for few rows; for many, as many workgroups as the
-  // 256 CUs hold at once (three each, by the bins' LDS)
+  // a slice per workgroup for few rows; else one workgroup per CU or two, as
+  // many as the bins' LDS lets in (16, 32, 64 x 151,936: 29, 32, 46 us with one,
+  // 32, 34, 44 with two; three, in turns, 42, 48, 59)
   const int slices = (a.V + kSlice - 1) / kSlice;
-  a.parts = max(1, min(min(slices, kMaxParts), max(1, 768 / a.T)));
+  a.parts = max(1, min(min(slices, kMaxParts), max(1, (a.T <= 40 ? 256 : 512) / a.T)));
   const dim3 grid(a.parts, a.T);
   sample_max_kernel<FMT><<<grid, kThreads, 0, st>>>(a);
   sample_hist_kernel<FMT><<<grid, kThreads, 0, st>>>(a);
