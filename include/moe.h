@@ -388,8 +388,7 @@ moe_status moe_verify_accept(const float* logits, int32_t T, int32_t V, const in
  * moe_layer or moe_prefill_layer wrote, for example.  Strides are in elements
  * from row to row, at least H; x8 [T][H] and x8_scale [T][ceil(H / 128)] are contiguous.  No
  * output overlaps an input, except resid_out equal to resid with the same
- * stride.  Pointers need their element's alignment only (x8 none); rows whose
- * pointers, strides and H allow 16-byte accesses are read that way.  Limits:
+ * stride.  Pointers need their element's alignment only (x8 none).  Limits:
  * H <= 32768, T <= 2^22.  Results do not depend on T or on the run. */
 moe_status moe_add_rmsnorm(int32_t T, int32_t H, const void* y, int32_t y_fmt, int64_t y_stride,
                            const void* resid, int32_t resid_fmt, int64_t resid_stride,

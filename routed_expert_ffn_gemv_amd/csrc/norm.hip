@@ -16,7 +16,9 @@
 // One pass: a row stays in registers between the sums and the outputs.  Each
 // lane holds chunks of 8 consecutive columns, so the 128 columns that share
 // a scale are 16 neighbouring lanes of one chunk and their maximum is four
-// DPP steps.  HBM-bound for many rows, latency-bound for few.
+// DPP steps.  HBM-bound for many rows (32,768 x 2048, fp32 y, bf16 residual,
+// both outputs: 129 us, 5.7 TB/s; a copy of 1 GiB runs at 5.15), latency-bound
+// for few (1 x 2048: 2.8 us).
 
 #include <hip/hip_runtime.h>
 
@@ -28,6 +30,7 @@ namespace {
 typedef __attribute__((ext_vector_type(4))) float f32x4;
 typedef __attribute__((ext_vector_type(2))) float f32x2;
 
+constexpr int kMaxGrid = 1 << 20;
 constexpr float kE4m3Max = 448.0f;
 constexpr float kScaleFloor = 448.0f * 0x1p-126f;   // keeps every scale a normal number
 
@@ -40,9 +43,11 @@ __device__ __forceinline__ float row16_max(float v) {
   return v;
 }
 
-__device__ __forceinline__ double wave_sum_f64(double v) {
+// Sum over aligned groups of LANES lanes.
+template <int LANES>
+__device__ __forceinline__ double lanes_sum(double v) {
 #pragma unroll
-  for (int m = 1; m < kWave; m <<= 1) v += __shfl_xor(v, m, kWave);
+  for (int m = 1; m < LANES; m <<= 1) v += __shfl_xor(v, m, kWave);
   return v;
 }
 
@@ -56,17 +61,24 @@ __device__ __forceinline__ float round_bf16(float a) {
   return bf16_to_f32(pack_bf16(a, 0.0f) & 0xFFFFu);
 }
 
-// 8 consecutive elements from p + i; VEC: 16-byte loads, all in range.
-template <bool VEC>
+// 16 and 8 bytes at any element's address: rows of odd length take the same
+// accesses, which the hardware splits (32,768 x 2047: 181 us, element by element
+// 409; 2048 columns: 129).
+typedef f32x4 __attribute__((aligned(4))) f32x4_any;
+typedef u32x4 __attribute__((aligned(2))) u32x4_any;
+typedef uint2 __attribute__((aligned(1))) uint2_any;
+
+// 8 consecutive elements from p + i, of which n exist (1 .. 8; WHOLE: 8).
+template <bool WHOLE>
 __device__ __forceinline__ void load8(const void* p, int fmt, int64_t i, int n, float* v) {
-  if (VEC) {
+  if (WHOLE || n == 8) {
     if (fmt == MOE_W_F32) {
-      const f32x4* q = reinterpret_cast<const f32x4*>(static_cast<const float*>(p) + i);
+      const f32x4_any* q = reinterpret_cast<const f32x4_any*>(static_cast<const float*>(p) + i);
       const f32x4 a = q[0], b = q[1];
 #pragma unroll
       for (int j = 0; j < 4; ++j) v[j] = a[j], v[4 + j] = b[j];
     } else {
-      const u32x4 a = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p) + i);
+      const u32x4 a = *reinterpret_cast<const u32x4_any*>(static_cast<const uint16_t*>(p) + i);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         v[2 * j] = __uint_as_float(a[j] << 16);
@@ -84,15 +96,15 @@ __device__ __forceinline__ void load8(const void* p, int fmt, int64_t i, int n, 
   }
 }
 
-template <bool VEC>
+template <bool WHOLE>
 __device__ __forceinline__ void store8(void* p, int fmt, int64_t i, int n, const float* v) {
-  if (VEC) {
+  if (WHOLE || n == 8) {
     if (fmt == MOE_W_F32) {
-      f32x4* q = reinterpret_cast<f32x4*>(static_cast<float*>(p) + i);
+      f32x4_any* q = reinterpret_cast<f32x4_any*>(static_cast<float*>(p) + i);
       q[0] = f32x4{v[0], v[1], v[2], v[3]};
       q[1] = f32x4{v[4], v[5], v[6], v[7]};
     } else {
-      *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p) + i) =
+      *reinterpret_cast<u32x4_any*>(static_cast<uint16_t*>(p) + i) =
           u32x4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
                 pack_bf16(v[6], v[7])};
     }
@@ -108,26 +120,28 @@ __device__ __forceinline__ void store8(void* p, int fmt, int64_t i, int n, const
     }
 }
 
-// WPR waves per row, ROWS rows per workgroup, NCH chunks of 8 columns per lane.
-template <int WPR, int ROWS, int NCH, bool VEC>
-__global__ __launch_bounds__(WPR* ROWS* kWave) void norm_kernel(const NormArgs a) {
-  __shared__ double part[WPR * ROWS];
+// LPR lanes per row (a wave's half, a wave or several), ROWS rows per
+// workgroup, NCH chunks of 8 columns per lane; WHOLE: H is a multiple of 8.
+template <int LPR, int ROWS, int NCH, bool WHOLE>
+__global__ __launch_bounds__(LPR* ROWS) void norm_kernel(const NormArgs a) {
+  constexpr int WPR = LPR / kWave;      // waves per row
+  __shared__ double part[LPR * ROWS / kWave];
   const int wave = threadIdx.x / kWave;
-  const int sub = threadIdx.x % (WPR * kWave);       // lane within the row's waves
-  const int64_t t = int64_t(blockIdx.x) * ROWS + wave / WPR;
+  const int sub = threadIdx.x % LPR;       // lane within the row's
+  const int64_t t = (int64_t(blockIdx.y) * gridDim.x + blockIdx.x) * ROWS + threadIdx.x / LPR;
   const bool live = t < a.T;
 
   float v[NCH][8];
   double ss = 0.0;
 #pragma unroll
   for (int c = 0; c < NCH; ++c) {
-    const int col = (c * WPR * kWave + sub) * 8;
+    const int col = (c * LPR + sub) * 8;
     const int n = live ? min(8, a.H - col) : 0;
     if (n > 0) {
-      load8<VEC>(a.resid, a.resid_fmt, t * a.resid_stride + col, n, v[c]);
+      load8<WHOLE>(a.resid, a.resid_fmt, t * a.resid_stride + col, n, v[c]);
       if (a.y) {
         float y[8];
-        load8<VEC>(a.y, a.y_fmt, t * a.y_stride + col, n, y);
+        load8<WHOLE>(a.y, a.y_fmt, t * a.y_stride + col, n, y);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           v[c][j] += y[j];
@@ -141,12 +155,12 @@ __global__ __launch_bounds__(WPR* ROWS* kWave) void norm_kernel(const NormArgs a
       for (int j = 0; j < 8; ++j) v[c][j] = 0.0f;
     }
   }
-  ss = wave_sum_f64(ss);
+  ss = lanes_sum<(LPR < kWave ? LPR : kWave)>(ss);
   if (WPR > 1) {
     if ((threadIdx.x & (kWave - 1)) == 0) part[wave] = ss;
     __syncthreads();
     ss = 0.0;
-    const int first = wave / WPR * WPR;
+    const int first = wave / (WPR > 1 ? WPR : 1) * WPR;
 #pragma unroll
     for (int w = 0; w < WPR; ++w) ss += part[first + w];
   }
@@ -154,19 +168,19 @@ __global__ __launch_bounds__(WPR* ROWS* kWave) void norm_kernel(const NormArgs a
 
 #pragma unroll
   for (int c = 0; c < NCH; ++c) {
-    const int col = (c * WPR * kWave + sub) * 8;
+    const int col = (c * LPR + sub) * 8;
     const int n = live ? min(8, a.H - col) : 0;
-    if (n > 0 && a.resid_out) store8<VEC>(a.resid_out, a.resid_fmt, t * a.resid_out_stride + col, n, v[c]);
+    if (n > 0 && a.resid_out) store8<WHOLE>(a.resid_out, a.resid_fmt, t * a.resid_out_stride + col, n, v[c]);
     float o[8];
     if (n > 0) {
-      load8<VEC>(a.weight, a.weight_fmt, col, n, o);
+      load8<WHOLE>(a.weight, a.weight_fmt, col, n, o);
 #pragma unroll
       for (int j = 0; j < 8; ++j) o[j] = v[c][j] * inv * o[j];
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) o[j] = 0.0f;
     }
-    if (n > 0 && a.x) store8<VEC>(a.x, MOE_W_BF16, t * a.x_stride + col, n, o);
+    if (n > 0 && a.x) store8<WHOLE>(a.x, MOE_W_BF16, t * a.x_stride + col, n, o);
     if (a.x8) {
       float m = 0.0f;
 #pragma unroll
@@ -182,8 +196,8 @@ __global__ __launch_bounds__(WPR* ROWS* kWave) void norm_kernel(const NormArgs a
           q[h] = uint32_t(p);
         }
         uint8_t* dst = a.x8 + t * a.H + col;
-        if (VEC) {
-          *reinterpret_cast<uint2*>(dst) = make_uint2(q[0], q[1]);
+        if (WHOLE || n == 8) {
+          *reinterpret_cast<uint2_any*>(dst) = make_uint2(q[0], q[1]);
         } else {
 #pragma unroll
           for (int j = 0; j < 8; ++j)
@@ -195,31 +209,33 @@ __global__ __launch_bounds__(WPR* ROWS* kWave) void norm_kernel(const NormArgs a
   }
 }
 
-template <int WPR, int ROWS, int NCH>
-hipError_t launch(const NormArgs& a, bool vec, hipStream_t st) {
-  const dim3 grid((a.T + ROWS - 1) / ROWS), block(WPR * ROWS * kWave);
-  if (vec)
-    norm_kernel<WPR, ROWS, NCH, true><<<grid, block, 0, st>>>(a);
+template <int LPR, int ROWS, int NCH>
+hipError_t launch(const NormArgs& a, hipStream_t st) {
+  // two dimensions: one holds less than 2^32 threads
+  const int groups = (a.T + ROWS - 1) / ROWS, wide = groups < kMaxGrid ? groups : kMaxGrid;
+  const dim3 grid(wide, (groups + wide - 1) / wide);
+  if (a.H % 8 == 0)
+    norm_kernel<LPR, ROWS, NCH, true><<<grid, LPR * ROWS, 0, st>>>(a);
   else
-    norm_kernel<WPR, ROWS, NCH, false><<<grid, block, 0, st>>>(a);
+    norm_kernel<LPR, ROWS, NCH, false><<<grid, LPR * ROWS, 0, st>>>(a);
   return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_add_rmsnorm(const NormArgs& a, hipStream_t st) {
-  // 16-byte accesses need whole chunks of 8 columns and aligned rows
-  auto ok16 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
-  const bool vec = a.H % 8 == 0 && a.resid_stride % 8 == 0 && a.y_stride % 8 == 0 &&
-                   a.resid_out_stride % 8 == 0 && a.x_stride % 8 == 0 && ok16(a.resid) && ok16(a.resid_out) && ok16(a.y) &&
-                   ok16(a.x) && ok16(a.weight) && (reinterpret_cast<uintptr_t>(a.x8) & 7) == 0;
-  if (a.H <= 512) return launch<1, 4, 1>(a, vec, st);
-  if (a.H <= 1024) return launch<1, 4, 2>(a, vec, st);
-  if (a.H <= 2048) return launch<4, 1, 1>(a, vec, st);
-  if (a.H <= 4096) return launch<4, 1, 2>(a, vec, st);
-  if (a.H <= 8192) return launch<4, 1, 4>(a, vec, st);
-  if (a.H <= 16384) return launch<16, 1, 2>(a, vec, st);
-  return launch<16, 1, 4>(a, vec, st);
+  // As few lanes as hold a row in at most 4 chunks of 8 columns each, so that
+  // few idle; from 1025 columns on four waves rather than one, for the loads of a
+  // row to be under way together.  300,000 x 200: 119 us with half a wave per
+  // row, 182 with a whole one.
+  if (a.H <= 256) return launch<32, 8, 1>(a, st);
+  if (a.H <= 512) return launch<64, 4, 1>(a, st);
+  if (a.H <= 1024) return launch<64, 4, 2>(a, st);
+  if (a.H <= 2048) return launch<256, 1, 1>(a, st);
+  if (a.H <= 4096) return launch<256, 1, 2>(a, st);
+  if (a.H <= 8192) return launch<256, 1, 4>(a, st);
+  if (a.H <= 16384) return launch<1024, 1, 2>(a, st);
+  return launch<1024, 1, 4>(a, st);
 }
 
 }  // namespace moe

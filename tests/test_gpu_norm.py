@@ -124,6 +124,31 @@ def test_many_rows():
     _check(y, r, w)
 
 
+@pytest.mark.parametrize("H", [9, 100, 250, 255, 256, 257, 513, 2049, 4099])
+@pytest.mark.parametrize("T", [1, 3, 8, 21])
+def test_rows_that_share_a_workgroup_or_start_anywhere(T, H):
+    for y, r in ((F32, BF16), (BF16, F32)):
+        _check(*_inputs(T, H, y, r, BF16, T + H))
+
+
+def test_more_rows_than_one_grid_dimension_takes():
+    """One workgroup per row, 2^20 + 5 rows: rows at both ends and around the
+    border against the definition, and no row left out."""
+    import routed_expert_ffn_gemv_amd as moe
+    T, H = 2 ** 20 + 5, 1032
+    resid = torch.empty((T, H), dtype=BF16, device="cuda")
+    resid.copy_((torch.arange(T, device="cuda") % 251 + 1).to(BF16)[:, None].expand(T, H))
+    resid[:, 7] = -3.0
+    weight = torch.ones(H, device="cuda")
+    x = torch.zeros((T, H), dtype=BF16, device="cuda")
+    moe.moe_add_rmsnorm(T, H, None, resid, weight, EPS, x=x)
+    torch.cuda.synchronize()
+    rows = [0, 1, 2 ** 20 - 1, 2 ** 20, 2 ** 20 + 1, T - 1]
+    want = _cpu(None, resid[rows].cpu(), weight.cpu())[2]
+    assert torch.equal(x[rows].cpu(), want)
+    assert bool((x[:, 0] != 0).all())
+
+
 def test_outputs_one_by_one():
     y, r, w = _inputs(3, 384, F32, BF16, BF16, 4)
     v, n, x, x8, scale = _cpu(y, r, w)
