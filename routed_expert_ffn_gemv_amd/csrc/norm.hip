@@ -224,16 +224,17 @@ hipError_t launch(const NormArgs& a, hipStream_t st) {
 }  // namespace
 
 hipError_t launch_add_rmsnorm(const NormArgs& a, hipStream_t st) {
-  // As few lanes as hold a row in at most 4 chunks of 8 columns each, so that
-  // few idle; from 1025 columns on four waves rather than one, for the loads of a
-  // row to be under way together.  300,000 x 200: 119 us with half a wave per
-  // row, 182 with a whole one.
+  // One chunk of 8 columns per lane as long as a workgroup holds the row: few
+  // idle lanes, and all loads of a row under way together.  32,768 x 2048: 129 us
+  // with four waves per row, 135 with two, 148 with one (1 x 2048: 3.2, 4.0, 5.9);
+  // 8000 x 8192: 133 with 16, 143 with four; 300,000 x 200: 119 with half a wave,
+  // 182 with one.
   if (a.H <= 256) return launch<32, 8, 1>(a, st);
   if (a.H <= 512) return launch<64, 4, 1>(a, st);
-  if (a.H <= 1024) return launch<64, 4, 2>(a, st);
+  if (a.H <= 1024) return launch<128, 2, 1>(a, st);
   if (a.H <= 2048) return launch<256, 1, 1>(a, st);
-  if (a.H <= 4096) return launch<256, 1, 2>(a, st);
-  if (a.H <= 8192) return launch<256, 1, 4>(a, st);
+  if (a.H <= 4096) return launch<512, 1, 1>(a, st);
+  if (a.H <= 8192) return launch<1024, 1, 1>(a, st);
   if (a.H <= 16384) return launch<1024, 1, 2>(a, st);
   return launch<1024, 1, 4>(a, st);
 }
