@@ -342,7 +342,8 @@ struct Tile {
   static constexpr int kRows = BN + BT;                       // rows of one buffer, 128 bytes each
   static constexpr int kWLoads = BN / 8 / kWaves, kXLoads = BT / 8 / kWaves;
   static constexpr int kLoads = kWLoads + kXLoads;            // 1 KiB loads per wave and block
-  static constexpr int kBuffer = kRows * kBlock + BT * 4;     // and the tokens' scales
+  static constexpr int kBuffer = kRows * kBlock + (BT > 64 ? BT : 64) * 4;   // and the tokens' scales,
+                                                              // which whole waves load
   static constexpr int kStores = OUT == MOE_W_F32 ? NI * TI : NI * TI / 2;   // per wave and tile
   static_assert(BN % (8 * kWaves) == 0 && BT % (8 * kWaves) == 0 && kBlock % (BN / WN) == 0 &&
                     NI % 2 == 0 && BT <= 64 * kWaves,
