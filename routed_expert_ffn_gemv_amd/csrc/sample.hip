@@ -771,7 +771,6 @@ __device__ __forceinline__ uint64_t draw_token_wave(const Row& r, const int* lo,
                                                     uint64_t total, const Mass& mass_before,
                                                     const Count& count_before, uint32_t n, uint64_t key,
                                                     uint64_t* kept) {
-  const int lane = threadIdx.x & 63;
   const double place = place_of(r, seen(r, logit_of(key)));
   if (!(place <= r.limit)) key = 0;
   const int my_bin = key ? bin_at(place) : -1;

@@ -21,9 +21,9 @@
 // a block does not matter as long as both sides agree, and a wave's load then
 // covers 64 consecutive bytes of each row.
 //
-// ring_kernel: few tokens, many weight rows; every row is streamed once, the
-// tokens stay in LDS.  direct_kernel: few outputs; operands straight into
-// registers.  tile_kernel: the rest; tiles of both operands through LDS.
+// direct_kernel: few outputs; operands straight into registers.  tile_kernel:
+// the rest; tiles of both operands through LDS, in shapes from 32 x 16 to 256 x
+// 256.
 
 #include <hip/hip_runtime.h>
 
@@ -41,6 +41,7 @@ typedef __attribute__((ext_vector_type(2))) _Float16 f16x2;
 typedef __attribute__((ext_vector_type(8))) _Float16 f16x8;
 
 constexpr int kBlock = 128;
+constexpr int kMaxLds = 160 * 1024;
 
 __device__ __forceinline__ f32x4 mfma_block(i32x8 w, i32x8 x) {
   const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -100,6 +101,10 @@ __device__ __forceinline__ f32x4 product(const Frag16& w, const Frag16& x) {
   return mfma_f16(w.hi.hi, x.hi.hi, d);
 }
 
+__device__ __forceinline__ u32x4 load16(const uint8_t* p) {
+  return *reinterpret_cast<const u32x4*>(p);
+}
+
 // Four consecutive outputs of one token.
 template <int OUT>
 __device__ __forceinline__ void store4(const LinearArgs& a, int t, int n, f32x4 v) {
@@ -129,172 +134,53 @@ __device__ __forceinline__ void store4(const LinearArgs& a, int t, int n, f32x4 
     }
 }
 
-// ---- few tokens
+// ---- loads straight to LDS
+//
+// In assembly, because the compiler does not know which part of LDS a load
+// fills and waits for all of them before the next read of any part: the loads
+// of the blocks ahead then run in turn with the products (32,768 x 4096 x 2048:
+// 330 us, 290 so).  Every wait for them is in this file (vmcnt counts the
+// compiler's own loads and stores too, in the order of issue, so its waits are
+// only ever longer than it thinks).  A load writes no register.  Reads of what
+// they fill stay behind a wait that clobbers memory, and they stay behind the
+// wait or barrier after the last reads of what they overwrite, as volatile
+// assembly keeps its order.  M0: the LDS address, for the wave (nothing else here
+// uses M0, which the compiler only sets next to its uses); the s_nop: 5 wait
+// states between a vector write of a scalar operand and its use here.
+#pragma clang diagnostic ignored "-Winline-asm"     // M0 among the clobbered registers
 
-__device__ __forceinline__ u32x4 load16(const uint8_t* p) {
-  return *reinterpret_cast<const u32x4*>(p);
+__device__ __forceinline__ uint32_t lds_address(const uint8_t* p) {
+  return __builtin_amdgcn_readfirstlane(
+      uint32_t(reinterpret_cast<uintptr_t>((const __attribute__((address_space(3))) uint8_t*)p)));
 }
 
-// The tokens into LDS as fp16, [T][row_blocks * 128], each row's 16-byte
-// chunks permuted by the row (t & 7) so that 16 rows read at one column meet
-// no bank twice; and their scales, [KB][16].
-__device__ __forceinline__ void stage_tokens(const LinearArgs& a, int row_blocks, uint8_t* xl,
-                                             float* xs) {
-  const int KB = (a.K + kBlock - 1) / kBlock;
-  const int chunks = KB * 8;                    // 16 codes each: two chunks of fp16
-  const int all = a.T * chunks, step = int(blockDim.x);
-#pragma unroll 1
-  for (int i0 = threadIdx.x; i0 < all; i0 += 4 * step) {
-    u32x4 v[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int i = i0 + j * step, t = i / chunks, k = i % chunks * 16;
-      v[j] = u32x4{0u, 0u, 0u, 0u};
-      if (i < all && k < a.K) v[j] = load16(a.x8 + int64_t(t) * a.K + k);
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int i = i0 + j * step, t = i / chunks, c = i % chunks;
-      if (i >= all) break;
-      const Half16 h = to_f16(v[j]);
-      uint8_t* p = xl + int64_t(t) * row_blocks * (kBlock * 2);
-      *reinterpret_cast<f16x8*>(p + ((2 * c) ^ (t & 7)) * 16) = h.lo;
-      *reinterpret_cast<f16x8*>(p + ((2 * c + 1) ^ (t & 7)) * 16) = h.hi;
-    }
-  }
-#pragma unroll 1
-  for (int i = threadIdx.x; i < 16 * KB; i += step) {
-    const int t = i / KB, b = i % KB;
-    xs[b * 16 + t] = t < a.T ? a.x_scale[int64_t(t) * KB + b] : 0.0f;
-  }
+// A buffer of `bytes` bytes at p: what lies beyond reads as zero.
+__device__ __forceinline__ u32x4 buffer_at(const uint8_t* p, uint32_t bytes) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+  return u32x4{uint32_t(__builtin_amdgcn_readfirstlane(uint32_t(a))),
+               uint32_t(__builtin_amdgcn_readfirstlane(uint32_t(a >> 32) & 0xFFFFu)),
+               uint32_t(__builtin_amdgcn_readfirstlane(bytes)), 0x00027000u};
 }
 
-// One block of 16 weight rows (this lane's two chunks) times the staged tokens.
-__device__ __forceinline__ void add_block(const LinearArgs& a, u32x4 wlo, u32x4 whi, float ws, int b,
-                                          int row_blocks, const uint8_t* xl, const float* xs,
-                                          f32x4& acc) {
-  const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
-  const Half16 lo = to_f16(wlo), hi = to_f16(whi);
-  const int t = min(col, a.T - 1);     // columns past T are not stored
-  const uint8_t* p = xl + int64_t(t) * row_blocks * (kBlock * 2);
-  const int c = b * 16 + 2 * g;
-  auto x = [&](int chunk) {
-    return *reinterpret_cast<const f16x8*>(p + ((chunk ^ (t & 7)) * 16));
-  };
-  f32x4 d = {0.0f, 0.0f, 0.0f, 0.0f};
-  d = mfma_f16(lo.lo, x(c), d);
-  d = mfma_f16(lo.hi, x(c + 1), d);
-  d = mfma_f16(hi.lo, x(c + 8), d);
-  d = mfma_f16(hi.hi, x(c + 9), d);
-  const float sc = xs[b * 16 + col] * ws;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) acc[i] = fmaf(d[i], sc, acc[i]);
+// 16 bytes per lane, lane l's to lds + 16 l: from offset at + base of a buffer.
+// NT: read once.
+template <bool NT>
+__device__ __forceinline__ void buffer_to_lds(u32x4 src, uint32_t at, uint32_t base, uint32_t lds) {
+  if (NT)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen nt lds" ::"s"(lds), "v"(at),
+                 "s"(src), "s"(base)
+                 : "m0");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds), "v"(at),
+                 "s"(src), "s"(base)
+                 : "m0");
+}
+// 4 bytes per lane, lane l's to lds + 4 l.
+__device__ __forceinline__ void global_to_lds4(const void* p, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(p) : "m0");
 }
 
-// Many weight rows: one workgroup per CU stays and its waves walk over tiles
-// of 16 rows.  Each wave owns two LDS slots of two blocks (4 KiB) and loads
-// one while it multiplies the other; nothing waits for another wave.  The
-// loads go straight to LDS because a matrix operand's layout would split
-// every row's line between two instructions: eight lanes fetch 128
-// consecutive bytes of a row instead, non-temporal (each byte is used once).
-// Measured on 151,936 x 2048 weights, 1 token: 47 us (6.6 TB/s; a bare
-// read of the same bytes takes 45 us), against 55 us with loads into
-// registers, and 51-57 us with more slots, more workgroups or ordinary loads.
-constexpr int kRingWaves = 8;
-constexpr int kRingBlocks = 2;                        // blocks per slot
-constexpr int kRingSlot = kRingBlocks * 16 * kBlock;  // bytes
-constexpr int kRingLoads = kRingSlot / 1024;
-constexpr int kMaxLds = 160 * 1024;
-
-// Every load of this wave has arrived, and its reads of LDS have ended (the
-// next loads may overwrite what they read).
-__device__ __forceinline__ void wait_loads() {
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-}
-
-// LDS of a workgroup: slots, two tiles' weight scales per wave, tokens, their scales.
-inline int ring_scales(int KB) { return (KB + 63) / 64 * 64; }
-inline int64_t ring_lds(int T, int KB) {
-  const int row_blocks = (KB + kRingBlocks - 1) / kRingBlocks * kRingBlocks;
-  return kRingWaves * (2 * kRingSlot + 2 * ring_scales(KB) * 4) +
-         int64_t(T) * row_blocks * (kBlock * 2) + int64_t(row_blocks) * 16 * 4;
-}
-
-template <int OUT>
-__global__ __launch_bounds__(kRingWaves * 64) void ring_kernel(const LinearArgs a) {
-  extern __shared__ uint8_t lds[];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int col = lane & 15, g = lane >> 4;
-  const int KB = (a.K + kBlock - 1) / kBlock;
-  const int steps = (KB + kRingBlocks - 1) / kRingBlocks, row_blocks = steps * kRingBlocks;
-  const int tiles = (a.N + 15) / 16, stride = int(gridDim.x) * kRingWaves;
-  const int scales = (KB + 63) / 64 * 64;
-  uint8_t* slots = lds + wave * (2 * kRingSlot);
-  float* wsl = reinterpret_cast<float*>(lds + kRingWaves * 2 * kRingSlot) + wave * 2 * scales;
-  float* xs = reinterpret_cast<float*>(lds + kRingWaves * 2 * kRingSlot) + kRingWaves * 2 * scales;
-  uint8_t* xl = reinterpret_cast<uint8_t*>(xs + row_blocks * 16);
-
-  // load i of a slot fills rows 4i .. 4i + 3, 16 lanes (256 bytes) each; slot
-  // s of a row holds the row's chunk s ^ (row & 7).  Chunks past the row's
-  // end are read at its end and not used.
-  constexpr int kLanes = kRingBlocks * 8, kRows = 64 / kLanes;
-  const int lrow = lane / kLanes, lslot = lane % kLanes;
-  int lt = int(blockIdx.x) * kRingWaves + wave, ls = 0, lslotno = 0, lbuf = 0;
-  auto load = [&]() {
-    if (lt >= tiles) return;
-    if (ls == 0) {
-      const float* src = a.w_scale + int64_t(lt * 16 / kBlock) * KB;
-      for (int i = 0; i < scales; i += 64)
-        __builtin_amdgcn_global_load_lds(
-            (const __attribute__((address_space(1))) void*)(src + min(i + lane, KB - 1)),
-            (__attribute__((address_space(3))) void*)(wsl + lbuf * scales + i), 4, 0, 0);
-      lbuf ^= 1;
-    }
-#pragma unroll
-    for (int i = 0; i < kRingLoads; ++i) {
-      const int r = i * kRows + lrow;
-      const int k = min(ls * (kRingBlocks * kBlock) + ((lslot ^ (r & 7)) * 16), a.K - 16);
-      __builtin_amdgcn_global_load_lds(
-          (const __attribute__((address_space(1))) void*)(a.w8 + int64_t(min(lt * 16 + r, a.N - 1)) * a.K + k),
-          (__attribute__((address_space(3))) void*)(slots + lslotno * kRingSlot + i * 1024), 16, 0,
-          2 /* non-temporal */);
-    }
-    lslotno ^= 1;
-    if (++ls == steps) ls = 0, lt += stride;
-  };
-  load();
-  stage_tokens(a, row_blocks, xl, xs);
-  __syncthreads();
-
-  int slot = 0, buf = 0;
-#pragma unroll 1
-  for (int tile = int(blockIdx.x) * kRingWaves + wave; tile < tiles; tile += stride) {
-    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 1
-    for (int st = 0; st < steps; ++st) {
-      wait_loads();         // this slot has arrived, and the tile's scales before it
-      load();
-      const uint8_t* p = slots + slot * kRingSlot + col * (kRingBlocks * kBlock);
-#pragma unroll
-      for (int b = 0; b < kRingBlocks; ++b) {
-        const int kb = st * kRingBlocks + b;
-        if (kb >= KB) break;
-        u32x4 lo = load16(p + ((b * 8 + g) ^ (col & 7)) * 16);
-        u32x4 hi = load16(p + ((b * 8 + g + 4) ^ (col & 7)) * 16);
-        if (kb * kBlock + kBlock > a.K) {
-          if (kb * kBlock + g * 16 >= a.K) lo = u32x4{0u, 0u, 0u, 0u};
-          if (kb * kBlock + g * 16 + 64 >= a.K) hi = u32x4{0u, 0u, 0u, 0u};
-        }
-        add_block(a, lo, hi, wsl[buf * scales + kb], kb, row_blocks, xl, xs, acc);
-      }
-      slot ^= 1;
-    }
-    buf ^= 1;
-    store4<OUT>(a, col, tile * 16 + g * 4, acc);
-  }
-}
-
-// ---- many tokens
+// ---- tiles through LDS
 
 // Which of a wave's weight rows is operand row m of its i-th group of 16.
 // A lane ends up with rows m = 4 (lane / 16) .. + 3 of every group: for fp32
@@ -322,15 +208,18 @@ __device__ __forceinline__ void store8(const LinearArgs& a, int t, int n, f32x4 
 }
 
 // Tiles of BN weight rows and BT tokens, WN x WT waves, NT: weights are read
-// once (non-temporal), a ring of STAGES LDS
-// buffers of one block of 128 columns each: STAGES - 1 blocks are on their way
-// while one is multiplied, across tiles too (workgroups stay and walk over
-// tiles, so that the first blocks of a tile arrive during the stores of the
-// one before).  The loads are buffer loads straight to LDS: rows past the
-// matrices' ends read as zero, and so do columns past K (their lanes' offset
-// is moved out of range).  A row's 16-byte chunks are permuted in LDS by the
-// row, so that the rows a fragment reads together meet no bank twice.
-// fp32 outputs convert the codes to fp16 on their way from LDS.
+// once (non-temporal), a ring of STAGES LDS buffers of one block of 128 columns
+// each: STAGES - 1 blocks are on their way while one is multiplied, across tiles
+// too (workgroups stay and walk over tiles, so that the first blocks of a tile
+// arrive during the stores of the one before).  The loads are buffer loads
+// straight to LDS: rows past the matrices' ends read as zero, and so do columns
+// past K (their lanes' offset is moved out of range).  A row's 16-byte chunks are
+// permuted in LDS by the row, so that the rows a fragment reads together meet
+// no bank twice.  fp32 outputs, and those of 16 tokens, convert the codes to
+// fp16 on their way from LDS.  Few tokens stream the weights (1 x 151,936 x 2048:
+// 48 us, 6.5 TB/s; a bare read of the same bytes takes 45), many are bound by LDS,
+// matrix instructions and the fma of the scales together (32,768 x 4096 x 2048:
+// 283-297 us on two cards, 1.85-1.94 PFLOP/s).
 //
 // KS > 1, for few tiles: KS groups of WN x WT waves take every KS-th block each,
 // with rings of their own, and their sums are joined in a fixed order at the
@@ -402,7 +291,8 @@ __global__ __launch_bounds__(KS* WN* WT * 64) void tile_kernel(const LinearArgs 
   int load_id = first + int(blockIdx.x >> 3), load_kb = group, load_buf = 0;
   int under_way = 0;     // blocks loaded and not yet multiplied
   if (load_id >= last) return;
-  __amdgpu_buffer_rsrc_t wsrc, xsrc;
+  u32x4 wsrc, xsrc;
+  const uint32_t lds_at = lds_address(lds);
   const float* scales;
   auto source = [&]() {
     int n0, t0;
@@ -410,8 +300,7 @@ __global__ __launch_bounds__(KS* WN* WT * 64) void tile_kernel(const LinearArgs 
     // (a load whose scalar offset passes the end reads zeros too)
     auto rows = [&](const uint8_t* p, int r0, int n) {
       const int64_t left = int64_t(n - r0) * a.K;
-      return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p + int64_t(r0) * a.K), 0,
-                                               int(left < 0x7FFFFFFF ? left : 0x7FFFFFFF), 0x00027000);
+      return buffer_at(p + int64_t(r0) * a.K, uint32_t(left < 0x7FFFFFFF ? left : 0x7FFFFFFF));
     };
     wsrc = rows(a.w8, n0, a.N);
     xsrc = rows(a.x8, t0, a.T);
@@ -419,23 +308,18 @@ __global__ __launch_bounds__(KS* WN* WT * 64) void tile_kernel(const LinearArgs 
   };
   auto load = [&]() {
     if (load_id >= last || (KS > 1 && load_kb >= KB)) return;
-    uint8_t* dst = lds + load_buf * BUFFER;
+    const uint32_t dst = lds_at + load_buf * BUFFER;
     const bool whole = load_kb + 1 < KB;
     const int k = load_kb * kBlock;
 #pragma unroll
     for (int i = 0; i < WL; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          wsrc, (__attribute__((address_space(3))) void*)(dst + (wrow0 + i * 8) * kBlock), 16,
-          whole ? off[i & 1] : off_last[i & 1], (wrow0 + i * 8) * a.K + k, 0, NT ? 2 : 0);
+      buffer_to_lds<NT>(wsrc, whole ? off[i & 1] : off_last[i & 1], (wrow0 + i * 8) * a.K + k,
+                        dst + (wrow0 + i * 8) * kBlock);
 #pragma unroll
     for (int i = 0; i < XL; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          xsrc, (__attribute__((address_space(3))) void*)(dst + (BN + xrow0 + i * 8) * kBlock), 16,
-          whole ? off[2] : off_last[2], (xrow0 + i * 8) * a.K + k, 0, 0);
-    if (wave * 64 < BT)
-      __builtin_amdgcn_global_load_lds(
-          (const __attribute__((address_space(1))) void*)(scales + load_kb),
-          (__attribute__((address_space(3))) void*)(dst + S::kRows * kBlock + wave * 256), 4, 0, 0);
+      buffer_to_lds<false>(xsrc, whole ? off[2] : off_last[2], (xrow0 + i * 8) * a.K + k,
+                           dst + (BN + xrow0 + i * 8) * kBlock);
+    if (wave * 64 < BT) global_to_lds4(scales + load_kb, dst + S::kRows * kBlock + wave * 256);
     load_buf = load_buf + 1 == STAGES ? 0 : load_buf + 1;
     ++under_way;
     load_kb += KS;
@@ -450,7 +334,7 @@ __global__ __launch_bounds__(KS* WN* WT * 64) void tile_kernel(const LinearArgs 
   for (int i = 0; i + 1 < STAGES; ++i) load();
 
   // the products' side
-  using Frag = std::conditional_t<OUT == MOE_W_F32, Frag16, Frag8>;
+  using Frag = std::conditional_t<OUT == MOE_W_F32 || BT == 16, Frag16, Frag8>;
   auto frag = [&](const uint8_t* row, int swap) {
     return Frag(load16(row + ((g ^ swap) * 16)), load16(row + (((g + 4) ^ swap) * 16)));
   };
@@ -463,7 +347,9 @@ __global__ __launch_bounds__(KS* WN* WT * 64) void tile_kernel(const LinearArgs 
     int n0, t0;
     place(id, n0, t0);
     const int wave_n = n0 + wn * (BN / WN), wave_t = t0 + wt * (BT / WT);
-    const float* wsc = a.w_scale + int64_t(min(wave_n, a.N - 1) / kBlock) * KB;
+    // (constant address space: scalar loads, which no count of vector loads waits for)
+    const auto wsc = (const __attribute__((address_space(4))) float*)a.w_scale +
+                     int64_t(min(wave_n, a.N - 1) / kBlock) * KB;
     f32x4 acc[NI][TI];
 #pragma unroll
     for (int i = 0; i < NI; ++i)
@@ -570,39 +456,32 @@ __global__ __launch_bounds__(KS* WN* WT * 64) void tile_kernel(const LinearArgs 
 
 // ---- few outputs
 
-// A workgroup owns NI x 16 weight rows and TI x 16 tokens, and its KS waves
-// split the blocks: each loads its own blocks straight into registers, the
-// next while it multiplies one, and waits for nobody until the sums are
-// joined, in a fixed order, through LDS.  Bound by latency (1 x 2048 x 2048:
-// 3.9 us; 17 x 2048 x 2048: 4.8) and by what one CU takes in: 16 waves instead
-// of 8 change nothing, half the rows per workgroup almost halve the time
-// while CUs are free.
-template <int NI, int TI, int KS, int OUT>
+// A workgroup owns NI x 16 weight rows and 16 tokens, and its KS waves split
+// the blocks: each loads its own blocks straight into registers, the next while
+// it multiplies one, and waits for nobody until the sums are joined, in a
+// fixed order, through LDS.  Bound by latency (1 x 2048 x 2048: 3.6 us; 17 x 2048
+// x 2048: 4.5) and by what one CU takes in: 16 waves instead of 8 change
+// nothing, half the rows per workgroup almost halve the time while CUs are free.
+template <int NI, int KS, int OUT>
 __global__ __launch_bounds__(KS * 64) void direct_kernel(const LinearArgs a) {
-  extern __shared__ uint8_t joined[];
-  auto sums = reinterpret_cast<f32x4(*)[NI * TI][64]>(joined);      // [KS]
+  __shared__ f32x4 sums[KS][NI][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, g = lane >> 4;
   const int KB = (a.K + kBlock - 1) / kBlock;
   const int tiles_n = (a.N + NI * 16 - 1) / (NI * 16);
-  const int n0 = int(blockIdx.x) % tiles_n * (NI * 16), t0 = int(blockIdx.x) / tiles_n * (TI * 16);
+  const int n0 = int(blockIdx.x) % tiles_n * (NI * 16), t0 = int(blockIdx.x) / tiles_n * 16;
   const uint8_t* wbase = a.w8 + int64_t(n0) * a.K;
-  const uint8_t* xbase = a.x8 + int64_t(t0) * a.K;
-  const float* sbase = a.x_scale + int64_t(t0) * KB;
   const float* wsc = a.w_scale + int64_t(n0 / kBlock) * KB;
-  uint32_t woff[NI], xoff[TI], soff[TI];     // rows past the ends repeat the last one
+  uint32_t woff[NI];     // rows past the ends repeat the last one
 #pragma unroll
   for (int i = 0; i < NI; ++i)
     woff[i] = uint32_t(min(i * 16 + col, a.N - 1 - n0)) * a.K + g * 16;
-#pragma unroll
-  for (int j = 0; j < TI; ++j) {
-    const int r = min(j * 16 + col, a.T - 1 - t0);
-    xoff[j] = uint32_t(r) * a.K + g * 16;
-    soff[j] = uint32_t(r) * KB;
-  }
+  const int t = min(t0 + col, a.T - 1);
+  const uint8_t* x = a.x8 + int64_t(t) * a.K + g * 16;
+  const float* xsc = a.x_scale + int64_t(t) * KB;
   struct Raw {
-    u32x4 w[NI][2], x[TI][2];
-    float xs[TI], ws;
+    u32x4 w[NI][2], x[2];
+    float scale;
   };
   auto load = [&](Raw& q, int kb) {
     const int k = kb * kBlock;
@@ -610,9 +489,7 @@ __global__ __launch_bounds__(KS * 64) void direct_kernel(const LinearArgs a) {
 #pragma unroll
       for (int i = 0; i < NI; ++i)
         q.w[i][0] = load16(wbase + k + woff[i]), q.w[i][1] = load16(wbase + k + 64 + woff[i]);
-#pragma unroll
-      for (int j = 0; j < TI; ++j)
-        q.x[j][0] = load16(xbase + k + xoff[j]), q.x[j][1] = load16(xbase + k + 64 + xoff[j]);
+      q.x[0] = load16(x + k), q.x[1] = load16(x + k + 64);
     } else {
       // the last, shorter block: zeros past the row's end
       const u32x4 zero = {0u, 0u, 0u, 0u};
@@ -623,38 +500,22 @@ __global__ __launch_bounds__(KS * 64) void direct_kernel(const LinearArgs a) {
         if (lo) q.w[i][0] = load16(wbase + k + woff[i]);
         if (hi) q.w[i][1] = load16(wbase + k + 64 + woff[i]);
       }
-#pragma unroll
-      for (int j = 0; j < TI; ++j) {
-        q.x[j][0] = q.x[j][1] = zero;
-        if (lo) q.x[j][0] = load16(xbase + k + xoff[j]);
-        if (hi) q.x[j][1] = load16(xbase + k + 64 + xoff[j]);
-      }
+      q.x[0] = q.x[1] = zero;
+      if (lo) q.x[0] = load16(x + k);
+      if (hi) q.x[1] = load16(x + k + 64);
     }
-#pragma unroll
-    for (int j = 0; j < TI; ++j) q.xs[j] = sbase[soff[j] + kb];
-    q.ws = wsc[kb];
+    q.scale = xsc[kb] * wsc[kb];
   };
-  f32x4 acc[NI][TI];
+  f32x4 acc[NI];
 #pragma unroll
-  for (int i = 0; i < NI; ++i)
-#pragma unroll
-    for (int j = 0; j < TI; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  using Frag = std::conditional_t<OUT == MOE_W_F32 || TI == 1, Frag16, Frag8>;
+  for (int i = 0; i < NI; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   auto add = [&](const Raw& q) {
-    Frag x[TI];
-    float sc[TI];
-#pragma unroll
-    for (int j = 0; j < TI; ++j) x[j] = Frag(q.x[j][0], q.x[j][1]), sc[j] = q.xs[j] * q.ws;
+    const Frag16 xf(q.x[0], q.x[1]);
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      const Frag w(q.w[i][0], q.w[i][1]);
-      f32x4 d[TI];
+      const f32x4 d = product(Frag16(q.w[i][0], q.w[i][1]), xf);
 #pragma unroll
-      for (int j = 0; j < TI; ++j) d[j] = product(w, x[j]);
-#pragma unroll
-      for (int j = 0; j < TI; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(d[j][e], sc[j], acc[i][j][e]);
+      for (int e = 0; e < 4; ++e) acc[i][e] = fmaf(d[e], q.scale, acc[i][e]);
     }
   };
   Raw q[2];
@@ -667,18 +528,15 @@ __global__ __launch_bounds__(KS * 64) void direct_kernel(const LinearArgs a) {
     if (kb + 2 * KS < KB) load(q[0], kb + 2 * KS);
     add(q[1]);
   }
-  // every wave adds up its share of the groups of 16 x 16, waves in order
+  // wave i adds up the i-th 16 rows' sums, waves in order
 #pragma unroll
-  for (int i = 0; i < NI; ++i)
-#pragma unroll
-    for (int j = 0; j < TI; ++j) sums[wave][i * TI + j][lane] = acc[i][j];
+  for (int i = 0; i < NI; ++i) sums[wave][i][lane] = acc[i];
   __syncthreads();
+  if (wave < NI) {
+    f32x4 v = sums[0][wave][lane];
 #pragma unroll
-  for (int m = wave; m < NI * TI; m += KS) {
-    f32x4 v = sums[0][m][lane];
-#pragma unroll
-    for (int k = 1; k < KS; ++k) v += sums[k][m][lane];
-    store4<OUT>(a, t0 + m % TI * 16 + col, n0 + m / TI * 16 + g * 4, v);
+    for (int k = 1; k < KS; ++k) v += sums[k][wave][lane];
+    store4<OUT>(a, t0 + col, n0 + wave * 16 + g * 4, v);
   }
 }
 
@@ -688,16 +546,6 @@ hipError_t allow_lds(Kernel kernel, int64_t bytes) {
   if (bytes <= 64 * 1024) return hipSuccess;
   return hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                              hipFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
-}
-
-template <int OUT>
-hipError_t launch_ring(const LinearArgs& a, hipStream_t st) {
-  const int64_t lds = ring_lds(a.T, (a.K + kBlock - 1) / kBlock);
-  const hipError_t e = allow_lds(ring_kernel<OUT>, lds);
-  if (e != hipSuccess) return e;
-  const int groups = ((a.N + 15) / 16 + kRingWaves - 1) / kRingWaves;
-  ring_kernel<OUT><<<groups < 256 ? groups : 256, kRingWaves * 64, lds, st>>>(a);
-  return hipGetLastError();
 }
 
 template <int BN, int BT, int WN, int WT, int STAGES, int KS, int OUT, bool NT = false>
@@ -718,13 +566,11 @@ hipError_t launch_tile(const LinearArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
-template <int NI, int TI, int KS, int OUT>
+template <int NI, int OUT>
 hipError_t launch_direct(const LinearArgs& a, hipStream_t st) {
-  const int tiles = ((a.N + NI * 16 - 1) / (NI * 16)) * ((a.T + TI * 16 - 1) / (TI * 16));
-  const int lds = KS * NI * TI * 1024;
-  const hipError_t e = allow_lds(direct_kernel<NI, TI, KS, OUT>, lds);
-  if (e != hipSuccess) return e;
-  direct_kernel<NI, TI, KS, OUT><<<tiles, KS * 64, lds, st>>>(a);
+  constexpr int KS = 8;
+  const int tiles = ((a.N + NI * 16 - 1) / (NI * 16)) * ((a.T + 15) / 16);
+  direct_kernel<NI, KS, OUT><<<tiles, KS * 64, 0, st>>>(a);
   return hipGetLastError();
 }
 
@@ -735,61 +581,61 @@ hipError_t launch(const LinearArgs& a, hipStream_t st) {
     return int64_t((a.N + bn - 1) / bn) * ((a.T + bt - 1) / bt);
   };
   auto rounds = [](int64_t n, int slots) { return (n + slots - 1) / slots; };
-  // The ring needs tiles of 16 rows for more than half of its 2048 waves, and
-  // tokens that fit LDS: 16 x 25,000 x 2048 takes 11.8 (16.6 direct), 1 x
-  // 20,000 x 8192 37 (39), 1 x 16,384 x 4096 20 (16).
-  if (a.T <= 16 && a.N >= 1250 * 16 && ring_lds(a.T, (a.K + kBlock - 1) / kBlock) <= kMaxLds)
-    return launch_ring<OUT>(a, st);
+  const int KB = (a.K + kBlock - 1) / kBlock;
+  // Few tokens, many rows: every byte of the weights once, two workgroups of
+  // two groups of waves per CU.
+  if (a.T <= 16 && a.N >= 20000) return launch_tile<64, 16, 2, 1, 3, 2, OUT, true>(a, st);
   // A CU takes in no more than about 30 GB/s of what comes from HBM, however
   // many of its waves ask: the finest workgroups of which each CU gets at most
-  // one.  32 x 1024 x 4096: 7.0 with 16 x 16, 11.5 with 32 x 32; 200 x 1000 x
-  // 8000: 15 with 32 x 32 (27 as tiles of 64 x 64 through LDS); 500 x 1000 x
-  // 2000: 7.3 with 64 x 32 (9.7); 777 x 1000 x 2000, 400 of them: 12.6 (10.1).
-  if (tiles(16, 16) <= 256) return launch_direct<1, 1, 8, OUT>(a, st);
-  if (tiles(32, 16) <= 256) return launch_direct<2, 1, 8, OUT>(a, st);
-  if (a.T <= 16) {
-    // 16 x 16,384 x 4096: 16.8 with 64 rows, 17.8 with 32; 1 x 20,000 x 8192
-    // (the ring's without room): 46 with 64, 38 with 32
-    if (tiles(64, 16) <= 256) return launch_direct<4, 1, 8, OUT>(a, st);
-    return launch_direct<2, 1, 8, OUT>(a, st);
+  // one.  32 x 1024 x 4096: 7.0 with 16 x 16, 11.5 with 32 x 32; 240 x 1000 x
+  // 4096: 7.4-8.7 with 32 x 32 (12-14 with 64 x 64).  Short rows go straight
+  // into registers (100 x 1000 x 2000: 4.7, through LDS 5.8), for long ones deeper
+  // rings pay (16 x 8192 x 8192: 14, into registers 19).
+  if (tiles(16, 16) <= 256) return launch_direct<1, OUT>(a, st);
+  if (tiles(32, 16) <= 256) {
+    if (KB >= 32) return launch_tile<32, 16, 1, 1, 4, 4, OUT, true>(a, st);
+    return launch_direct<2, OUT>(a, st);
   }
-  if (tiles(32, 32) <= 256) return launch_direct<2, 2, 8, OUT>(a, st);
-  if (tiles(64, 32) <= 256) return launch_direct<4, 2, 8, OUT>(a, st);
-  // Tiles through LDS.  One tile of tokens: narrow ones, three stages, several
-  // workgroups per CU (32 x 151,936 x 2048: 61-66, as 64 x 64 88-95; 64 x
-  // 151,936 x 2048: 76-79 with 128 rows, 83-88 with 64).  More rows per tile
-  // only where that leaves no CU with more of them to do (64 x 40,000 x 4096:
-  // 47-50 with 64 rows, 47-51 with 128).
+  // 16 x 12,000 x 4096: 12 (15 into registers)
+  if (a.T <= 16) return launch_tile<64, 16, 2, 1, 4, 2, OUT, true>(a, st);
+  if (tiles(32, 32) <= 256) return launch_tile<32, 32, 1, 1, 4, 4, OUT>(a, st);
+  // 64 x 8192 x 8192: 21-22 (34 with 64 x 64), 500 x 1000 x 2000: 6.9-7.9 (9.5-10)
+  if (tiles(64, 32) <= 256) return launch_tile<64, 32, 2, 1, 3, 4, OUT>(a, st);
+  // One tile of tokens: narrow tiles, several workgroups per CU.
   if (a.T <= 32) {
-    // up to two per CU: two groups of waves each (25,000 rows, K 4096: 26 and 34)
+    // up to two per CU: two groups of waves each (20 x 25,000 x 4096: 23, 27-29
+    // with one); 32 x 60,000 x 1024: 13-14 with 64 rows, 13-15 with 128, 32 x
+    // 151,936 x 2048: 58-65 and 54-62
     if (tiles(64, 32) <= 512) return launch_tile<64, 32, 2, 1, 3, 2, OUT, true>(a, st);
-    return launch_tile<64, 32, 2, 1, 3, 1, OUT, true>(a, st);
+    if (tiles(128, 64) <= 512) return launch_tile<64, 32, 2, 1, 3, 1, OUT, true>(a, st);
+    return launch_tile<128, 64, 2, 2, 2, 1, OUT, true>(a, st);
   }
   if (a.T <= 64) {
-    if (tiles(64, 64) > 512) {
-      if (2 * rounds(tiles(128, 64), 256) <= rounds(tiles(64, 64), 256))
-        return launch_tile<128, 64, 2, 2, 3, 1, OUT, true>(a, st);
-      return launch_tile<64, 64, 2, 2, 3, 1, OUT, true>(a, st);
-    }
+    // 64 x 151,936 x 2048: 63-71 (75-81 with 64 rows), 64 x 40,000 x 4096: 46-49 (47-50)
+    if (tiles(64, 64) > 512) return launch_tile<128, 64, 2, 2, 2, 1, OUT, true>(a, st);
   } else {
     if constexpr (OUT == MOE_W_BF16) {
       // a round of 256 tiles of 256 x 256 costs 1.6 of 512 of 128 x 128 (32,768
-      // x 4096 x 2048: 330 and 413; 3000 x 4096 x 4096: 81 and 89, 500 x 40,000 x
-      // 4096: 179 and 161)
+      // x 4096 x 2048: 293 and 379; 3000 x 4096 x 4096: 63 and 71, 300 x 40,000 x
+      // 2048: 61 and 49)
       if (8 * rounds(tiles(256, 256), 256) <= 5 * rounds(tiles(128, 128), 512))
         return launch_tile<256, 256, 2, 4, 2, 1, OUT>(a, st);
-    } else {
-      // 4096 x 4096 x 4096: 146 and 157; 3000 x 4096 x 4096: 133 and 116
-      if (2 * rounds(tiles(256, 128), 256) <= rounds(tiles(128, 128), 256))
-        return launch_tile<256, 128, 4, 2, 3, 1, OUT>(a, st);
     }
+    // fp32 32,768 x 4096 x 2048: 566 and 603; bf16 300 x 40,000 x 2048: 44 and 49;
+    // fp32 3000 x 4096 x 4096 (more to do for some CUs): 122 and 103
+    if (2 * rounds(tiles(256, 128), 256) <= rounds(tiles(128, 128), 256))
+      return launch_tile<256, 128, 4, 2, OUT == MOE_W_F32 ? 2 : 3, 1, OUT>(a, st);
     if (tiles(128, 128) > 256) return launch_tile<128, 128, 2, 2, 2, 1, OUT>(a, st);
     if (tiles(128, 128) > 128) return launch_tile<128, 128, 2, 2, 2, 2, OUT>(a, st);
   }
-  // few tiles: groups of waves that share the blocks (100 x 4096 x 4096: 14 with
-  // four, 17 with two; 300 x 4096 x 4096, 320 tiles: 22 with two)
+  // few tiles: groups of waves that share the blocks (777 x 1000 x 2000: fp32
+  // 10.6 with four, 11.0 with two and deeper rings; bf16 10.0 and 8.8; 300 x 4096 x
+  // 4096, 320 tiles: 18-25 with two, two workgroups per CU, 22-31 with one)
   if (tiles(64, 64) > 256) return launch_tile<64, 64, 2, 2, 2, 2, OUT>(a, st);
-  return launch_tile<64, 64, 2, 2, 2, 4, OUT>(a, st);
+  if constexpr (OUT == MOE_W_F32)
+    return launch_tile<64, 64, 2, 2, 2, 4, OUT>(a, st);
+  else
+    return launch_tile<64, 64, 2, 2, 4, 2, OUT>(a, st);
 }
 
 }  // namespace
