@@ -98,14 +98,22 @@ def test_large(T, N):
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("T,N", [
-    (20, 500), (40, 1500), (9, 9001), (13, 16400), (1, 20004), (200, 1004), (400, 1001),     # operands in registers
-    (17, 17003), (32, 33004), (33, 33001), (50, 60004),                                      # one tile of tokens
-    (777, 1000), (310, 4100), (129, 10001), (300, 14004), (1201, 4100), (3900, 4001),        # more
+    (20, 500), (40, 1500), (9, 9001), (13, 16400), (1, 20004), (200, 1004), (400, 1001),
+    (17, 17003), (32, 33004), (21, 66001), (33, 33001), (50, 60004),
+    (777, 1000), (310, 4100), (129, 10001), (300, 14004), (1201, 4100), (1190, 16300), (3900, 4001),
 ])
 def test_every_shape_of_workgroup(T, N, dtype):
     """Sizes that end inside every kernel's tiles, one to three blocks."""
     for K in (48, 272):
         _check(*_inputs(T, N, K, T + N + K), dtype=dtype, pad=4 if N % 4 == 0 else 3)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,N,K", [(40, 1500, 4112), (16, 8000, 4096), (5, 4500, 8192), (16, 9000, 4112),
+                                   (16, 20100, 1936), (250, 1000, 4112), (100, 4000, 4000), (30, 17003, 2064)])
+def test_long_rows(T, N, K, dtype):
+    """Many blocks through every ring of LDS buffers."""
+    _check(*_inputs(T, N, K, T + N + K, spread=False), dtype=dtype, pad=4)
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
