@@ -51,7 +51,7 @@ constexpr double kCutoff = 42.0;        // units below the largest logit from wh
 constexpr int kMaxParts = 256;
 constexpr int kSlice = 4096;            // logits of a row per workgroup
 constexpr int kListCap = 16384;         // listed candidates of a row
-constexpr int kLdsList = 3072;          // of which this many are searched in LDS
+constexpr int kLdsList = 3200;          // of which this many are searched in LDS
 constexpr int kRowList = 12288;         // listed candidates in LDS with a workgroup per row
 
 struct RowCtl {
