@@ -66,7 +66,8 @@ __device__ __forceinline__ float round_bf16(float a) {
 // 409; 2048 columns: 129).
 typedef f32x4 __attribute__((aligned(4))) f32x4_any;
 typedef u32x4 __attribute__((aligned(2))) u32x4_any;
-typedef uint2 __attribute__((aligned(1))) uint2_any;
+typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
+typedef u32x2 __attribute__((aligned(1))) u32x2_any;
 
 // 8 consecutive elements from p + i, of which n exist (1 .. 8; WHOLE: 8).
 template <bool WHOLE>
@@ -197,7 +198,7 @@ __global__ __launch_bounds__(LPR* ROWS) void norm_kernel(const NormArgs a) {
         }
         uint8_t* dst = a.x8 + t * a.H + col;
         if (WHOLE || n == 8) {
-          *reinterpret_cast<uint2_any*>(dst) = make_uint2(q[0], q[1]);
+          *reinterpret_cast<u32x2_any*>(dst) = u32x2{q[0], q[1]};
         } else {
 #pragma unroll
           for (int j = 0; j < 8; ++j)

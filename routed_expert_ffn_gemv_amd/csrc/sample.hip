@@ -202,6 +202,13 @@ __device__ __forceinline__ uint64_t shfl_u64(uint64_t v, int lane) {
   return (uint64_t(hi) << 32) | lo;
 }
 
+// The value of one lane, the same in all.
+__device__ __forceinline__ uint64_t lane_u64(uint64_t v, int lane) {
+  const uint32_t lo = __builtin_amdgcn_readlane(uint32_t(v), lane);
+  const uint32_t hi = __builtin_amdgcn_readlane(uint32_t(v >> 32), lane);
+  return (uint64_t(hi) << 32) | lo;
+}
+
 template <int CTRL, int ROWS>
 __device__ __forceinline__ uint32_t dpp_or_zero(uint32_t v) {
   return uint32_t(__builtin_amdgcn_update_dpp(0, int(v), CTRL, ROWS, 0xF, false));
@@ -229,10 +236,8 @@ __device__ __forceinline__ uint64_t block_max(uint64_t v, uint64_t* red) {
   __syncthreads();
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
   __syncthreads();
-  uint64_t m = 0;
-#pragma unroll 4
-  for (int w = 0; w < int(blockDim.x) / kWave; ++w) m = max_u64(m, red[w]);
-  return m;
+  const int lane = threadIdx.x & 63;
+  return wave_max_u64(lane < int(blockDim.x) / kWave ? red[lane] : 0);
 }
 
 // Inclusive prefixes of a and b over the workgroup; red: two words per wave.
@@ -243,12 +248,12 @@ __device__ __forceinline__ void block_scan(uint64_t& a, uint64_t& b, uint64_t* r
   __syncthreads();
   if (lane == 63) red[2 * wave] = a, red[2 * wave + 1] = b;
   __syncthreads();
-  uint64_t xa = 0, xb = 0;
-#pragma unroll 4
-  for (int w = 0; w < int(blockDim.x) / kWave; ++w) {
-    xa += w < wave ? red[2 * w] : 0;
-    xb += w < wave ? red[2 * w + 1] : 0;
-  }
+  // every wave scans the waves' sums
+  const bool in = lane < int(blockDim.x) / kWave;
+  uint64_t xa = wave_scan(in ? red[2 * lane] : 0), xb = wave_scan(in ? red[2 * lane + 1] : 0);
+  const int before = __builtin_amdgcn_readfirstlane(wave) - 1;
+  xa = before < 0 ? 0 : lane_u64(xa, before);
+  xb = before < 0 ? 0 : lane_u64(xb, before);
   a += xa;
   b += xb;
 }
@@ -475,7 +480,7 @@ __device__ __forceinline__ void fill_bins(const Row& r, const RowView<FMT>& v, i
 }
 
 // First bin whose inclusive prefix reaches target (the last one if none does), found
-// by every wave for itself: 64 ends of 64 bins each, then those 64 bins.
+// by one wave: 64 ends of 64 bins each, then those 64 bins.
 template <class Tp>
 __device__ __forceinline__ int first_reaching(const Tp* prefix, Tp target) {
   static_assert(kBins == 64 * 64, "two steps");
@@ -483,6 +488,29 @@ __device__ __forceinline__ int first_reaching(const Tp* prefix, Tp target) {
   const int run = __popcll(__ballot(prefix[lane * 64 + 63] < target));
   if (run == 64) return kBins - 1;
   return run * 64 + __popcll(__ballot(prefix[run * 64 + lane] < target));
+}
+
+// The bins [lo, hi] in which each target can fall, from the inclusive prefixes
+// of masses and counts; one wave.
+__device__ __forceinline__ void find_targets(const Row& r, const uint64_t* mass, const uint32_t* count,
+                                             int* lo, int* hi) {
+  uint64_t z0 = mass[kBins - 1], z1 = z0;      // bounds of the sum kept so far
+#pragma unroll
+  for (int q = 0; q < 3; ++q) lo[q] = 0, hi[q] = -1;
+  if (r.top_k > 0 && uint32_t(r.top_k) < count[kBins - 1]) {
+    const int b = first_reaching(count, uint32_t(r.top_k));
+    lo[0] = hi[0] = b;
+    z0 = max_u64(b ? mass[b - 1] : 0, 1);
+    z1 = max_u64(mass[b], 1);
+  }
+  if (r.top_p < 1.0) {
+    lo[1] = first_reaching(mass, top_p_target(r.top_p, z0));
+    hi[1] = first_reaching(mass, top_p_target(r.top_p, z1));
+    z0 = max_u64(lo[1] ? mass[lo[1] - 1] : 0, 1);
+    z1 = mass[hi[1]];
+  }
+  lo[2] = first_reaching(mass, draw_target(r.u, z0));
+  hi[2] = first_reaching(mass, draw_target(r.u, z1));
 }
 
 // From the bins' packed sums (PER per thread, from bin threadIdx.x * PER) the
@@ -510,23 +538,21 @@ __device__ __forceinline__ void bound_targets(const Row& r, const uint64_t* pack
     cp -= packed[j] >> r.q_bits;
   }
   __syncthreads();
-  uint64_t z0 = mass[kBins - 1], z1 = z0;      // bounds of the sum kept so far
+  // one wave finds the bins for all (issue slots that the others leave to it)
+  int* found = reinterpret_cast<int*>(red);
+  if (threadIdx.x < kWave) {
+    find_targets(r, mass, count, lo, hi);
+    if (threadIdx.x == 0) {
 #pragma unroll
-  for (int q = 0; q < 3; ++q) lo[q] = 0, hi[q] = -1;
-  if (r.top_k > 0 && uint32_t(r.top_k) < count[kBins - 1]) {
-    const int b = first_reaching(count, uint32_t(r.top_k));
-    lo[0] = hi[0] = b;
-    z0 = max_u64(b ? mass[b - 1] : 0, 1);
-    z1 = max_u64(mass[b], 1);
+      for (int q = 0; q < 3; ++q) found[2 * q] = lo[q], found[2 * q + 1] = hi[q];
+    }
   }
-  if (r.top_p < 1.0) {
-    lo[1] = first_reaching(mass, top_p_target(r.top_p, z0));
-    hi[1] = first_reaching(mass, top_p_target(r.top_p, z1));
-    z0 = max_u64(lo[1] ? mass[lo[1] - 1] : 0, 1);
-    z1 = mass[hi[1]];
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < 3; ++q) {
+    lo[q] = __builtin_amdgcn_readfirstlane(found[2 * q]);
+    hi[q] = __builtin_amdgcn_readfirstlane(found[2 * q + 1]);
   }
-  lo[2] = first_reaching(mass, draw_target(r.u, z0));
-  hi[2] = first_reaching(mass, draw_target(r.u, z1));
 }
 
 // Which tokens matter: those of the bins [lo, hi], and few others.
