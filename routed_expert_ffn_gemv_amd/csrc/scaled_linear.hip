@@ -219,7 +219,7 @@ __device__ __forceinline__ void store8(const LinearArgs& a, int t, int n, f32x4 
 // fp16 on their way from LDS.  Few tokens stream the weights (1 x 151,936 x 2048:
 // 48 us, 6.5 TB/s; a bare read of the same bytes takes 45), many are bound by LDS,
 // matrix instructions and the fma of the scales together (32,768 x 4096 x 2048:
-// 283-297 us on two cards, 1.85-1.94 PFLOP/s).
+// 283-300 us from card to card, 1.83-1.94 PFLOP/s).
 //
 // KS > 1, for few tiles: KS groups of WN x WT waves take every KS-th block each,
 // with rings of their own, and their sums are joined in a fixed order at the
