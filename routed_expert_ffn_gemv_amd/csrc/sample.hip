@@ -573,7 +573,9 @@ struct Wanted {
       if (q < 2) asked[q] = hi[q] >= lo[q];
       scale[q] = middle[q] = 0.0f;
       if (hi[q] < lo[q]) continue;
-      const float from = logit_bound(r, double(hi[q] + 1), -1.0), to = logit_bound(r, double(lo[q]), 1.0);
+      // (the largest logit is an end too: a bound past fp32's range would leave no middle)
+      const float from = logit_bound(r, double(hi[q] + 1), -1.0);
+      const float to = fminf(logit_bound(r, double(lo[q]), 1.0), r.top);
       const float c = 0.5f * from + 0.5f * to;
       const float half = fmaxf(0.5f * to - 0.5f * from, fmaxf(fabsf(c) * 0x1p-18f, 0x1p-100f));
       scale[q] = 1.0f / half;
