@@ -440,11 +440,17 @@ moe_status moe_scaled_linear(const uint8_t* x8, const float* x_scale, int32_t T,
  * temperature, top_k, top_p, min_p: device arrays [T], each may be NULL: 1, 0,
  * 1, 0.  top_k <= 0, top_p >= 1 (or NaN) and min_p <= 0 (or NaN) filter
  * nothing; infinite temperatures make every token that is left equal; equal
- * +infinity logits share the draw.  w is held to 2^-(6 + f) of itself, f =
- * min(28, 63 - 2 ceil(log2 V)) (2^-33 for 151,936 tokens); tokens more than 42
- * temperatures below the largest logit (w < 6e-19) are not drawn.  Sums are
- * exact from there on: results do not depend on T, on the other rows or on
- * the run.  tokens [T] int32.  Limits: 1 <= V <= 2^26, T <= 16384.  ws:
+ * +infinity logits share the draw.
+ * Precision: tokens more than 42 temperatures below the largest logit (w <
+ * 6e-19) are left out.  w is held to 2^-(6 + f) of itself, f = min(28, 63 - 2
+ * ceil(log2 V)) (2^-33 for 151,936 tokens).  A running sum is one of whole
+ * numbers: the tokens of each 1/96 of a temperature together are rounded to
+ * 2^-s of the largest w, s = min(52, 61 - ceil(log2 V)) (2^-43; 2^-35 for 2^26
+ * tokens), so it is off by 2017 * 2^-s of the largest w at most besides, and a
+ * token alone in its 1/96 with w < 2^-(s + 1) is drawn by u >= 1 only.  Whole
+ * numbers have no order of addition: results do not depend on T, on the other
+ * rows or on the run.
+ * tokens [T] int32.  Limits: 1 <= V <= 2^26, T <= 16384.  ws:
  * moe_sample_workspace_size bytes, 256-byte aligned, in use by one call at a
  * time. */
 typedef struct {

@@ -29,7 +29,9 @@
 // was split nor on which atomic came first, and the steps agree on every sum
 // to the last bit.  (A draw next to the border between two tokens of a flat
 // row needs such sums: with fp32 ones about one in 10,000 would differ.)
-// Tokens more than 42 units below the largest (w < 6e-19) are never drawn.
+// A lone token below 2^-(s + 1) of the largest has mass 0, so the last kept
+// token (u >= 1) is found by count.  Tokens more than 42 units below the
+// largest (w < 6e-19) are never drawn.
 //
 // Many rows, or short ones: sample_row_kernel, one workgroup per row and one
 // launch.  Few long rows: three launches with a slice of a row per workgroup;
@@ -435,6 +437,13 @@ __device__ __forceinline__ uint64_t draw_target(double u, uint64_t zn) {
   const uint64_t t = uint64_t(floor(u * double(zn))) + 1;   // the sum exceeds u * zn
   return t > zn ? zn : t;
 }
+// u >= 1 takes the last kept token.  Behind top-p that is the one that reaches
+// the whole kept sum; without, a token whose mass rounds to 0 may be the last,
+// and the draw goes by the count of the kept ones.
+__device__ __forceinline__ bool draws_last(const Row& r) { return r.u >= 1.0 && r.top_p >= 1.0; }
+__device__ __forceinline__ uint32_t kept_count(const Row& r, uint32_t all) {
+  return r.top_k > 0 && uint32_t(r.top_k) < all ? uint32_t(r.top_k) : all;
+}
 
 // ---- the steps
 
@@ -509,8 +518,12 @@ __device__ __forceinline__ void find_targets(const Row& r, const uint64_t* mass,
     z0 = max_u64(lo[1] ? mass[lo[1] - 1] : 0, 1);
     z1 = mass[hi[1]];
   }
-  lo[2] = first_reaching(mass, draw_target(r.u, z0));
-  hi[2] = first_reaching(mass, draw_target(r.u, z1));
+  if (draws_last(r)) {
+    lo[2] = hi[2] = first_reaching(count, kept_count(r, count[kBins - 1]));
+  } else {
+    lo[2] = first_reaching(mass, draw_target(r.u, z0));
+    hi[2] = first_reaching(mass, draw_target(r.u, z1));
+  }
 }
 
 // From the bins' packed sums (PER per thread, from bin threadIdx.x * PER) the
@@ -662,10 +675,11 @@ __device__ __forceinline__ uint64_t draw_token(const Row& r, const int* lo, cons
   uint64_t z = total;
 #pragma unroll 1
   for (int q = 0; q < 3; ++q) {
-    const bool by_count = q == 0;
+    const bool by_count = q == 0 || (q == 2 && draws_last(r));
     if (hi[q] < lo[q]) continue;
-    const uint64_t target = by_count ? uint64_t(r.top_k) : q == 1 ? top_p_target(r.top_p, z)
-                                                                 : draw_target(r.u, z);
+    const uint64_t target = by_count ? uint64_t(kept_count(r, count_before(kBins)))
+                            : q == 1 ? top_p_target(r.top_p, z)
+                                     : draw_target(r.u, z);
     __syncthreads();
     if (threadIdx.x == 0) s.all_or = 0, s.all_and = ~0ull, s.n = 0, s.bin = lo[q], s.base = 0;
     if (threadIdx.x < 256) s.hsum[threadIdx.x] = 0;
@@ -825,8 +839,9 @@ __device__ __forceinline__ uint64_t draw_token_wave(const Row& r, const int* lo,
     const uint64_t hit = __ballot(key && mass_to < target && mass_thru >= target);
     z = max_u64(shfl_u64(mass_thru, __ffsll((long long)hit) - 1), 1);
   }
-  const uint64_t target = draw_target(r.u, z);
-  const uint64_t hit = __ballot(key && mass_to < target && mass_thru >= target);
+  const bool last = draws_last(r);
+  const uint64_t target = last ? uint64_t(kept_count(r, count_before(kBins))) : draw_target(r.u, z);
+  const uint64_t hit = __ballot(key && (last ? count_to + 1 == target : mass_to < target && mass_thru >= target));
   *kept = z;
   return shfl_u64(key, __ffsll((long long)hit) - 1);
 }

@@ -7,7 +7,8 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_sample import _check, _logits, _params
+from oracle import around
+from test_gpu_sample import _call, _check, _logits, _params
 
 pytestmark = pytest.mark.gpu
 
@@ -39,3 +40,34 @@ def test_logits_near_the_end_of_the_type(V):
                 top_p=[1, 0.9, 1, 0.9, 0.8, 1, 0.95, 0.5, 1, 0.9, 1, 0.9])
     _check(x, p)
     _check(torch.as_tensor(np.clip(x, -3.3e38, 3.3e38)).to(torch.bfloat16), p)
+
+
+@pytest.mark.parametrize("V", [9001, 50257])
+def test_the_last_kept_token(V):
+    """u >= 1 takes the last kept token, however little it weighs: alone, in
+    runs of equal logits (more than a wave searches, more than the list
+    holds), behind top-k, top-p and min-p."""
+    x = np.full((10, V), -np.inf, np.float32)
+    x[:, 3] = 0.0
+    x[0, 900] = -40.0
+    x[1, [900, 77, 8000]] = [-38.0, -40.5, -41.9]
+    x[2, 100:200] = -40.0
+    x[3, 100:] = -39.0
+    x[4, 100:] = -39.0
+    x[5, 100:200] = -39.0
+    x[6, 100:200] = -2.0
+    x[7] = _logits(1, V, 60)[0]
+    x[8, 100:110] = -41.5
+    x[9, 100:300] = np.linspace(-41, -30, 200)
+    p = _params(10, temperature=1.0, min_p=[0, 0, 0, 0, 0, 0, 0.1, 0, 0, 0],
+                top_k=[0, 0, 0, 0, V // 2, 58, 30, 100, 5, 100],
+                top_p=[1, 1, 1, 1, 1, 1, 0.9, 1, 1, 1], u=[1, 2, 1, 1, 1, np.inf, 1, 1, 1, 1])
+    t = torch.as_tensor(x)
+    tok, prob = _call(t.cuda(), p)
+    order = [np.argsort(-r.astype(np.float64), kind="stable") for r in x]
+    want = [900, 8000, 199, V - 1, 100 + V // 2 - 2, 156, None, order[7][99], 103, order[9][99]]
+    want[6] = around.sample_row(x[6], 1.0, 1.0, 30, float(np.float32(0.9)), float(np.float32(0.1)))[0]
+    np.testing.assert_array_equal(tok, want)
+    probs = np.array([around.sample_row(x[t], 1.0, 1.0, int(p["top_k"][t]), float(p["top_p"][t]),
+                                        float(p["min_p"][t]))[1] for t in range(10)])
+    assert (np.abs(prob - probs) <= 2.0 ** -23 * probs + 1e-30).all()
