@@ -412,6 +412,20 @@ def _flat(t, n, what, dtypes):
                          f"got {list(t.shape)} of {t.dtype}")
 
 
+def _matrix(t, rows, cols, what, dtypes):
+    """A contiguous tensor whose rows are `cols` long: [>= rows][cols], or flat."""
+    if t.shape == (rows, cols) and t.dtype in dtypes and t.is_contiguous():
+        return
+    _flat(t, rows * cols, what, dtypes)
+    if rows > 1 and t.ndim > 1 and t.shape[-1] != cols:
+        n = 1
+        for size in reversed(t.shape):     # (or in several dimensions, as blocks of columns)
+            n *= size
+            if n == cols:
+                return
+        raise ValueError(f"{what}: [{rows}][{cols}] wanted, got {list(t.shape)}")
+
+
 def _gpu_of(what, first, *others):
     """The one GPU that holds the tensors (None: left out)."""
     dev = first.get_device()
@@ -465,10 +479,10 @@ def moe_add_rmsnorm(T, H, y, resid, weight, eps, resid_out=None, x=None, x8=None
             raise ValueError(f"x: bf16 wanted, got {x.dtype}")
         xp, x_row = x.data_ptr(), _rows(x, T, H, "x")
     if x8 is not None:
-        _flat(x8, T * H, "x8", _CODES)
+        _matrix(x8, T, H, "x8", _CODES)
         qp = x8.data_ptr()
     if x8_scale is not None:
-        _flat(x8_scale, T * ((H + 127) // 128), "x8_scale", _F32)
+        _matrix(x8_scale, T, (H + 127) // 128, "x8_scale", _F32)
         sp = x8_scale.data_ptr()
     _flat(weight, H, "weight", _FMT_OF)
     dev = _gpu_of("moe_add_rmsnorm", resid, y, weight, resid_out, x, x8, x8_scale)
@@ -492,10 +506,10 @@ def moe_scaled_linear(x8, x_scale, T, w8, w_scale, N, K, out, ws=None, stream=No
     N, K) bytes (None when that is 0)."""
     T, N, K = int(T), int(N), int(K)
     kb = (K + 127) // 128
-    _flat(x8, T * K, "x8", _CODES)
-    _flat(x_scale, T * kb, "x_scale", _F32)
-    _flat(w8, N * K, "w8", _CODES)
-    _flat(w_scale, (N + 127) // 128 * kb, "w_scale", _F32)
+    _matrix(x8, T, K, "x8", _CODES)
+    _matrix(x_scale, T, kb, "x_scale", _F32)
+    _matrix(w8, N, K, "w8", _CODES)
+    _matrix(w_scale, (N + 127) // 128, kb, "w_scale", _F32)
     if ws is not None:
         _flat(ws, 0, "ws", _U8)
     fmt, row = _fmt_of(out, "out"), _rows(out, T, N, "out")
