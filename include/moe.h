@@ -451,7 +451,8 @@ moe_status moe_scaled_linear(const uint8_t* x8, const float* x_scale, int32_t T,
  * numbers have no order of addition: results do not depend on T, on the other
  * rows or on the run.
  * tokens [T] int32.  Limits: 1 <= V <= 2^26, T <= 16384.  ws:
- * moe_sample_workspace_size bytes, 256-byte aligned, in use by one call at a
+ * moe_sample_workspace_size bytes (no less for larger T or V, so that the
+ * largest call's serves the others), 256-byte aligned, in use by one call at a
  * time. */
 typedef struct {
   const float* temperature;

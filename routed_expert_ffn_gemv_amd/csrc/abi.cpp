@@ -797,7 +797,7 @@ moe_status moe_scaled_linear(const uint8_t* x8, const float* x_scale, int32_t T,
 moe_status moe_sample_workspace_size(int32_t T, int32_t V, size_t* bytes) {
   if (!bytes || T < 0 || V < 1) return MOE_ERR_INVALID;
   if (T > kMaxSampleT || V > kMaxVocab) return MOE_ERR_UNSUPPORTED;
-  *bytes = up(sample_ws(T));
+  *bytes = up(sample_ws(T, V));
   return MOE_OK;
 }
 

@@ -138,7 +138,7 @@ struct SampleArgs {
   void* ws;
   int parts, shift, frac_bits, q_bits;   // set by launch_sample
 };
-size_t sample_ws(int T);
+size_t sample_ws(int T, int V);
 hipError_t launch_sample(SampleArgs a, hipStream_t st);
 
 // product of e4m3 activations and weights with block scales

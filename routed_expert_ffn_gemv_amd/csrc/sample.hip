@@ -1089,13 +1089,15 @@ __global__ __launch_bounds__(kThreads) void sample_pick_kernel(const SampleArgs 
   finish_row(a, w, row, index_of(key), prob_of(r, key, kept), &flag);
 }
 
+// Up to how many rows of V logits go in slices.  A workgroup per row has one
+// launch but one CU's speed: 16 x 32,000 takes 24 us (25 us in slices), 16 x
+// 151,936 61 us (29 us), 64 x 48,000 34 us (34 us), 128 x 64,000 44 us (46 us), 128
+// and 256 x 151,936 75 and 94 us (64 and 108 us).
+int sliced_rows(int V) { return V <= 36000 ? 0 : V / 650 - 1; }
+
 template <int FMT>
 hipError_t launch(SampleArgs a, hipStream_t st) {
-  // A workgroup per row has one launch but one CU's speed: 16 x 32,000 takes
-  // 24 us (25 us in slices), 16 x 151,936 61 us (29 us), 64 x 48,000 34 us (34
-  // us), 128 x 64,000 44 us (46 us), 128 and 256 x 151,936 75 and 94 us (64 and
-  // 108 us).
-  if (a.V <= 36000 || a.T >= a.V / 650) {
+  if (a.T > sliced_rows(a.V)) {
     sample_row_kernel<FMT><<<a.T, kRowThreads, 0, st>>>(a);
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && a.n_out) {
@@ -1118,9 +1120,12 @@ hipError_t launch(SampleArgs a, hipStream_t st) {
 
 }  // namespace
 
-size_t sample_ws(int T) {
+// What the slices use; more rows, which use none, ask for no more than the
+// most rows in slices, so that a workspace serves smaller calls too.  One row's
+// at least.
+size_t sample_ws(int T, int V) {
   Ws w;
-  return ws_layout(T, nullptr, &w);
+  return ws_layout(min(T, max(1, sliced_rows(V))), nullptr, &w);
 }
 
 hipError_t launch_sample(SampleArgs a, hipStream_t st) {

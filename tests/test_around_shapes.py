@@ -50,3 +50,22 @@ def test_one_row_may_lie_in_a_longer_one():
     with pytest.raises(ValueError, match="must be on one GPU"):
         moe.moe_scaled_linear(_codes(1, K + 16), torch.zeros((1, 3)), 1, _codes(N, K), torch.zeros((3, 2)),
                               N, K, torch.zeros((1, N)))
+
+
+def test_sample_workspace_is_what_the_slices_need():
+    """Rows that take a workgroup each use none; sizes grow with T and V, so
+    that one workspace serves every smaller call."""
+    size = moe.moe_sample_workspace_size
+    row = size(1, 1000)
+    assert 0 < row <= 256 * 1024
+    assert size(256, 32000) == size(16384, 36000) == row
+    assert size(16384, 151936) == size(256, 151936) < 256 * row
+    assert size(4, 151936) <= 4 * row
+    Ts = (0, 1, 2, 4, 53, 54, 55, 64, 76, 77, 78, 232, 233, 234, 300, 16384)
+    Vs = (1, 4096, 36000, 36001, 50257, 50700, 151936, 1 << 26)
+    for V in Vs:
+        for a, b in zip(Ts, Ts[1:]):
+            assert size(a, V) <= size(b, V)
+    for T in Ts:
+        for a, b in zip(Vs, Vs[1:]):
+            assert size(T, a) <= size(T, b)

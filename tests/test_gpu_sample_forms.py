@@ -8,7 +8,7 @@ import pytest
 import torch
 
 from oracle import around
-from test_gpu_sample import _call, _check, _logits, _params
+from test_gpu_sample import _call, _check, _expect, _logits, _params
 
 pytestmark = pytest.mark.gpu
 
@@ -71,3 +71,32 @@ def test_the_last_kept_token(V):
     probs = np.array([around.sample_row(x[t], 1.0, 1.0, int(p["top_k"][t]), float(p["top_p"][t]),
                                         float(p["min_p"][t]))[1] for t in range(10)])
     assert (np.abs(prob - probs) <= 2.0 ** -23 * probs + 1e-30).all()
+
+
+@pytest.mark.parametrize("V,T", [(36001, 54), (36001, 55), (36000, 60), (50257, 76), (50257, 77)])
+def test_either_side_of_the_rule_in_the_workspace_asked_for(V, T):
+    """The last batch in slices and the first with a workgroup per row: equal
+    to each row by itself, and nothing behind the workspace is written."""
+    import routed_expert_ffn_gemv_amd as moe
+    x = _logits(T, V, T)
+    p = _params(T, seed=T)
+    d = {k: torch.as_tensor(v, device="cuda") for k, v in p.items()}
+    u = d.pop("u")
+    xs = torch.as_tensor(x, device="cuda")
+    size = moe.moe_sample_workspace_size(T, V)
+    ws = torch.full((size + 65536,), 0x5A, dtype=torch.uint8, device="cuda")
+    tok = torch.full((T,), -5, dtype=torch.int32, device="cuda")
+    prob = torch.zeros(T, device="cuda")
+    moe.moe_sample(xs, T, V, u, tok, ws[:size], prob=prob, **d)
+    torch.cuda.synchronize()
+    want, want_p = _expect(x.astype(np.float64), p)
+    np.testing.assert_array_equal(tok.cpu().numpy(), want)
+    assert (np.abs(prob.cpu().numpy() - want_p) <= 2.0 ** -23 * want_p + 1e-30).all()
+    assert bool((ws[size:] == 0x5A).all())
+    one = torch.zeros(1, dtype=torch.int32, device="cuda")
+    one_p = torch.zeros(1, device="cuda")
+    for t in (0, T // 2, T - 1):
+        moe.moe_sample(xs[t:t + 1], 1, V, u[t:t + 1], one, ws[:size], prob=one_p,
+                       **{k: v[t:t + 1] for k, v in d.items()})
+        torch.cuda.synchronize()
+        assert int(one) == int(tok[t]) and float(one_p) == float(prob[t])
