@@ -450,10 +450,10 @@ moe_status moe_scaled_linear(const uint8_t* x8, const float* x_scale, int32_t T,
  * token alone in its 1/96 with w < 2^-(s + 1) is drawn by u >= 1 only.  Whole
  * numbers have no order of addition: results do not depend on T, on the other
  * rows or on the run.
- * tokens [T] int32.  Limits: 1 <= V <= 2^26, T <= 16384.  ws:
- * moe_sample_workspace_size bytes (no less for larger T or V, so that the
- * largest call's serves the others), 256-byte aligned, in use by one call at a
- * time. */
+ * tokens [T] int32.  No output overlaps an input.  Limits: 1 <= V <= 2^26, T <=
+ * 16384.  ws: moe_sample_workspace_size bytes (no less for larger T or V, so
+ * that the largest call's serves the others), 256-byte aligned, in use by one
+ * call at a time. */
 typedef struct {
   const float* temperature;
   const int32_t* top_k;
@@ -471,7 +471,8 @@ moe_status moe_sample(const void* logits, int32_t fmt, int32_t T, int32_t V, int
  * g_i's place.  The drafts are fixed before the pass, so keeping a draft
  * exactly when the row draws it leaves the distribution of the output that
  * of sampling token after token.  out_tokens [T]: every row's token; *n_out =
- * kept drafts + 1.  1 <= T <= 64; draft [T-1] may be NULL when T = 1. */
+ * kept drafts + 1.  1 <= T <= 64; draft [T-1] may be NULL when T = 1, and does
+ * not overlap out_tokens (MOE_ERR_INVALID). */
 moe_status moe_verify_sample(const void* logits, int32_t fmt, int32_t T, int32_t V, int64_t stride,
                              const moe_sample_params* params, const float* u,
                              const int32_t* draft, int32_t* out_tokens, float* prob,

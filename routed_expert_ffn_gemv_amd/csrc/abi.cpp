@@ -325,6 +325,11 @@ moe_status run_sample(const void* logits, int32_t fmt, int32_t T, int32_t V, int
   }
   if (!ws || !aligned(ws, kAlign)) return MOE_ERR_INVALID;
   if (ws_bytes < need) return MOE_ERR_WORKSPACE;
+  // drafts are compared with the tokens once these are written
+  if (n_out && T > 1) {
+    const uintptr_t d = reinterpret_cast<uintptr_t>(draft), o = reinterpret_cast<uintptr_t>(tokens);
+    if (d < o + size_t(T) * 4 && o < d + size_t(T - 1) * 4) return MOE_ERR_INVALID;
+  }
   a.logits = logits;
   a.fmt = fmt;
   a.T = T;

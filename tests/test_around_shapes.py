@@ -69,3 +69,12 @@ def test_sample_workspace_is_what_the_slices_need():
     for T in Ts:
         for a, b in zip(Vs, Vs[1:]):
             assert size(T, a) <= size(T, b)
+
+
+@pytest.mark.parametrize("off", [0, 4, -8, 12, -4])
+def test_drafts_within_the_tokens_are_refused(off):
+    """They are compared once the tokens are written.  (Addresses are never
+    dereferenced: the call is refused before any launch.)"""
+    at = 1 << 20
+    assert moe.lib.moe_verify_sample(at, moe.MOE_W_F32, 4, 1000, 1000, None, at, at + 4096 + off, at + 4096,
+                                     at, at, at, 1 << 30, None) == moe.MOE_ERR_INVALID

@@ -100,3 +100,24 @@ def test_either_side_of_the_rule_in_the_workspace_asked_for(V, T):
                        **{k: v[t:t + 1] for k, v in d.items()})
         torch.cuda.synchronize()
         assert int(one) == int(tok[t]) and float(one_p) == float(prob[t])
+
+
+@pytest.mark.parametrize("V", [9001, 50257])
+def test_drafts_right_behind_the_tokens(V):
+    """Drafts that touch the tokens' ends are drafts like others."""
+    import routed_expert_ffn_gemv_amd as moe
+    T = 4
+    x = _logits(T, V, 70)
+    p = _params(T, seed=70)
+    want, _ = _expect(x.astype(np.float64), p)
+    d = {k: torch.as_tensor(v, device="cuda") for k, v in p.items()}
+    u = d.pop("u")
+    ws = torch.empty(moe.moe_sample_workspace_size(T, V), dtype=torch.uint8, device="cuda")
+    for drafts, tokens in ((slice(0, 3), slice(3, 7)), (slice(4, 7), slice(0, 4))):
+        buf = torch.full((7,), -5, dtype=torch.int32, device="cuda")
+        buf[drafts] = torch.as_tensor([want[0], want[1], (want[2] + 1) % V], dtype=torch.int32)
+        n = torch.zeros(1, dtype=torch.int32, device="cuda")
+        moe.moe_verify_sample(torch.as_tensor(x, device="cuda"), T, V, buf[drafts], u, buf[tokens], n, ws, **d)
+        torch.cuda.synchronize()
+        np.testing.assert_array_equal(buf[tokens].cpu().numpy(), want)
+        assert int(n) == 3
