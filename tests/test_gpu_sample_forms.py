@@ -121,3 +121,179 @@ def test_drafts_right_behind_the_tokens(V):
         torch.cuda.synchronize()
         np.testing.assert_array_equal(buf[tokens].cpu().numpy(), want)
         assert int(n) == 3
+
+
+VS = (9001, 50257)
+
+
+@pytest.mark.parametrize("V", VS)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_masks_infinities_and_nan(V, dtype):
+    x = _logits(12, V, 80)
+    low = float(torch.finfo(dtype).min)
+    x[0, :] = -np.inf                        # nothing left
+    x[1, :] = -np.inf
+    x[1, 777] = -3.0                         # one left
+    x[2, ::2] = -np.inf
+    x[3, 5:] = low                           # the type's lowest value is a logit like another
+    x[4, :] = low
+    x[5, ::3] = np.nan
+    x[6, :] = np.nan
+    x[7, [8, 100, 4000]] = np.inf            # equal infinities share the draw
+    x[8, :] = -np.inf
+    x[8, V - 1] = low
+    x[9, ::5] = np.inf
+    x[10, [0, V - 1]] = np.inf
+    x[10, 1:V - 1:2] = np.nan
+    x[11, :V - 2] = -np.inf                  # the last two, of one value
+    x[11, V - 2:] = -7.5
+    p = _params(12, temperature=[0.9] * 9 + [np.inf, 1e-40, 0.3], top_k=[0] * 9 + [1000, 0, 0],
+                top_p=[0.97] * 9 + [0.4567, 1, 1], min_p=0.0, seed=80)
+    t = torch.as_tensor(x).to(dtype)
+    _check(t, p)
+    tok, prob = _call(t.cuda(), p)
+    assert tok[0] == tok[6] == -1 and prob[0] == prob[6] == 0
+
+
+@pytest.mark.parametrize("V", VS)
+def test_every_extreme_parameter(V):
+    T = 16
+    p = _params(T, seed=81,
+                temperature=[0, -1, np.nan, 1e-30, 1e-45, 1e30, np.inf, 1, 1, 1, 1, 1, 1, 1, 1, 100],
+                top_k=[0, 0, 0, 0, 0, 0, 0, -4, 2 ** 31 - 1, V, V + 1, 1, 0, 0, 0, V - 1],
+                top_p=[1, 1, 1, 1, 1, 1, 1, 1, 1, 1, 1, 1, np.nan, 1.5, -2, 0.9],
+                min_p=[0, 0, 0, 0, 0, 0, 0, np.nan, -1, 0, 0, 0, 1, 2, 0, 0],
+                u=[0.5, 0.5, 0.5, 0.5, 0.5, 0.31, 0.77, 0.2, 0.4, 0.6, 0.8, 0.9, 0.3, 0.9, 0.9, 0.77])
+    _check(_logits(T, V, 81), p)
+
+
+@pytest.mark.parametrize("V", VS)
+def test_draws_outside_the_unit_interval(V):
+    x = np.repeat(_logits(1, V, 82), 6, axis=0)
+    u = np.array([0.0, 1.0, 5.0, -1.0, np.nan, 1 - 2.0 ** -24], np.float32)
+    order = np.argsort(-x[0].astype(np.float64), kind="stable")
+    for k, top_p, last in ((40, 1.0, order[39]), (3000, 1.0, order[2999]), (0, 1e-9, order[0])):
+        tok, _ = _call(torch.as_tensor(x).cuda(), _params(6, temperature=1.0, top_k=k, top_p=top_p, min_p=0.0, u=u))
+        assert tok[0] == tok[3] == tok[4] == order[0]
+        assert tok[1] == tok[2] == tok[5] == last
+
+
+@pytest.mark.parametrize("off", ["temperature", "top_k", "top_p", "min_p", None])
+@pytest.mark.parametrize("V", VS)
+def test_parameters_one_by_one_left_out(V, off):
+    off = {off: None} if off else dict.fromkeys(("temperature", "top_k", "top_p", "min_p"))
+    _check(_logits(8, V, 83), _params(8, seed=83, **off))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("pad,off", [(1, 0), (3, 1), (0, 2), (5, 3), (7, 7)])
+def test_rows_that_start_anywhere(dtype, pad, off):
+    """Slices of rows that start and end inside 16 bytes, between large logits."""
+    T, V = 7, 50257
+    x = torch.as_tensor(_logits(T, V, 84)).to(dtype)
+    buf = torch.full((T * (V + pad) + off + 8,), 1e30, dtype=dtype, device="cuda")
+    view = buf[off:off + T * (V + pad)].view(T, V + pad)[:, :V]
+    view.copy_(x)
+    p = _params(T, seed=84)
+    tok, prob = _call(view, p)
+    want, want_p = _expect(x.double().numpy(), p)
+    np.testing.assert_array_equal(tok, want)
+    assert (np.abs(prob - want_p) <= 2.0 ** -23 * want_p + 1e-30).all()
+
+
+@pytest.mark.parametrize("T,V", [(1, 50257), (2, 50257), (4, 50257), (17, 50257), (64, 50257), (4, 151936),
+                                 (1, 9001), (17, 9001), (64, 41000)])
+def test_verify_in_both_forms(T, V):
+    """Every number of kept drafts at the ends and in the middle; greedy rows,
+    and rows with nothing to draw (token -1, which no draft is)."""
+    x = _logits(T, V, 85 + T)
+    if T > 2:
+        x[T - 2] = -np.inf
+    p = _params(T, seed=85)
+    p["temperature"][::3] = 0.0
+    want, want_p = _expect(x.astype(np.float64), p)
+    xs = torch.as_tensor(x).cuda()
+    for kept in sorted({0, 1, T // 2, T - 2, T - 1} & set(range(T))):
+        draft = np.maximum(want[:T - 1], 0)
+        if kept < T - 1:
+            draft[kept] = (want[kept] + 1) % V
+        n_want = next((i for i in range(T - 1) if draft[i] != want[i]), T - 1) + 1
+        tok, prob, n = _call(xs, p, draft=draft, verify=True)
+        np.testing.assert_array_equal(tok, want)
+        assert (np.abs(prob - want_p) <= 2.0 ** -23 * want_p + 1e-30).all()
+        assert n == n_want
+
+
+def test_rows_alone_and_in_batches_of_either_form():
+    """40,009 logits: 64 rows take a workgroup each, 61 and 1 go in slices."""
+    V = 40009
+    x = torch.as_tensor(_logits(64, V, 86)).cuda()
+    p = _params(64, seed=86)
+    tok, prob = _call(x, p)
+    for rows in [slice(0, 60), slice(4, 64)] + [slice(t, t + 1) for t in (0, 13, 40, 63)]:
+        a, b = _call(x[rows], {k: v[rows] for k, v in p.items()})
+        np.testing.assert_array_equal(a, tok[rows])
+        np.testing.assert_array_equal(b, prob[rows])
+
+
+@pytest.mark.parametrize("V", VS)
+def test_replayed_verify_pass(V):
+    """Captured once; new logits, numbers and drafts between the replays."""
+    import routed_expert_ffn_gemv_amd as moe
+    T = 5
+    p = _params(T, seed=87)
+    par = {k: torch.as_tensor(v, device="cuda") for k, v in p.items() if k != "u"}
+    logits, u = torch.zeros((T, V), device="cuda"), torch.zeros(T, device="cuda")
+    draft = torch.zeros(T - 1, dtype=torch.int32, device="cuda")
+    tok = torch.zeros(T, dtype=torch.int32, device="cuda")
+    n = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = torch.empty(moe.moe_sample_workspace_size(T, V), dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    moe.moe_verify_sample(logits, T, V, draft, u, tok, n, ws, stream=side, **par)
+    side.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        moe.moe_verify_sample(logits, T, V, draft, u, tok, n, ws, **par)
+    for kept, seed in ((4, 90), (0, 91), (2, 92), (3, 93)):
+        x = _logits(T, V, seed)
+        p["u"] = np.random.default_rng(seed).random(T, dtype=np.float32)
+        want, _ = _expect(x.astype(np.float64), p)
+        d = want[:T - 1].astype(np.int32)
+        if kept < T - 1:
+            d[kept] = (d[kept] + 1) % V
+        logits.copy_(torch.as_tensor(x))
+        u.copy_(torch.as_tensor(p["u"]))
+        draft.copy_(torch.as_tensor(d))
+        g.replay()
+        torch.cuda.synchronize()
+        np.testing.assert_array_equal(tok.cpu().numpy(), want)
+        assert int(n) == kept + 1
+        _call(logits, p)
+
+
+def test_more_logits_than_31_bits_count():
+    """16,384 rows of 151,936: the far rows' tokens, masked elsewhere."""
+    import routed_expert_ffn_gemv_amd as moe
+    T, V = 16384, 151936
+    if torch.cuda.mem_get_info()[0] < 12 << 30:
+        pytest.skip("12 GB of GPU memory wanted")
+    x = torch.full((T, V), float("-inf"), dtype=torch.bfloat16, device="cuda")
+    row = torch.arange(T, device="cuda")
+    want = (row * 9973 + 5) % V
+    x[row, want] = 1.5
+    full = _logits(4, V, 88)
+    far = [0, 14134, 14135, T - 1]           # element 2^31 lies in row 14,134
+    for i, t in enumerate(far):
+        x[t] = torch.as_tensor(full[i]).to(torch.bfloat16)
+    p = _params(T, seed=88, temperature=0.8, top_k=50, top_p=0.9, min_p=0.0)
+    par = {k: torch.as_tensor(v, device="cuda") for k, v in p.items()}
+    u = par.pop("u")
+    tok = torch.zeros(T, dtype=torch.int32, device="cuda")
+    ws = torch.empty(moe.moe_sample_workspace_size(T, V), dtype=torch.uint8, device="cuda")
+    moe.moe_sample(x, T, V, u, tok, ws, **par)
+    torch.cuda.synchronize()
+    ref, _ = _expect(torch.as_tensor(full).to(torch.bfloat16).double().numpy(), {k: v[far] for k, v in p.items()})
+    want = want.to(torch.int32)
+    want[far] = torch.as_tensor(ref, dtype=torch.int32, device="cuda")
+    assert torch.equal(tok, want)
