@@ -382,7 +382,8 @@ moe_status moe_verify_accept(const float* logits, int32_t T, int32_t V, const in
  *   x8, x8_scale          (may be NULL, both or neither): n in 8 bits for
  *       moe_scaled_linear.  Per row and block b of 128 columns (the last one
  *       may be shorter): x8_scale = max(amax |n|, 448 * 2^-126) / 448 and
- *       x8 = e4m3(n / x8_scale), rounded to the nearest, ties to even.
+ *       x8 = e4m3(n / x8_scale), rounded to the nearest, ties to even.  NaN
+ *       columns are NaN codes and left out of the maximum.
  * At least one of x, x8 and resid_out is not NULL.  y, resid (and resid_out,
  * which has resid's format) and weight are MOE_W_F32 or MOE_W_BF16; y is what
  * moe_layer or moe_prefill_layer wrote, for example.  Strides are in elements
@@ -406,7 +407,8 @@ moe_status moe_add_rmsnorm(int32_t T, int32_t H, const void* y, int32_t y_fmt, i
  * x_scale [T][ceil(K / 128)] are what moe_add_rmsnorm writes; w8 [N][K] and
  * w_scale [ceil(N / 128)][ceil(K / 128)], one scale per 128 x 128 weights.
  * Codes are OCP e4m3 (no infinities; a NaN code makes the sums it enters
- * NaN), scales fp32, all contiguous.  out is MOE_W_F32 or MOE_W_BF16 (rounded
+ * NaN), scales fp32 (a block's two are multiplied first, in fp32: their product
+ * has to be a normal number, or loses what fp32 loses below it), all contiguous.  out is MOE_W_F32 or MOE_W_BF16 (rounded
  * once), out_stride elements from row to row (>= N).  Sums are fp32; for
  * bf16 outputs of more than 16 tokens the hardware's 8-bit products may be
  * used, which add eight neighbouring ones with 13 bits below the largest.

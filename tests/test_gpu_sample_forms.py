@@ -297,3 +297,36 @@ def test_more_logits_than_31_bits_count():
     want = want.to(torch.int32)
     want[far] = torch.as_tensor(ref, dtype=torch.int32, device="cuda")
     assert torch.equal(tok, want)
+
+
+def _largest_vocabulary():
+    """2^26 logits, and of them those that a top-k of 40 can keep."""
+    V = 1 << 26
+    x = np.random.default_rng(95).standard_normal((2, V), dtype=np.float32) * 3
+    x[1, 1 << 25:] = -np.inf
+    few = [np.sort(np.argpartition(-r, 400)[:400]) for r in x]      # in the order of their indexes
+    p = _params(2, temperature=[0.9, 2.0], top_k=40, top_p=[0.9, 1.0], min_p=0.0, u=[0.41, 0.77])
+    want = []
+    for t in range(2):
+        tok, prob, slack = around.sample_row(x[t, few[t]], float(p["u"][t]), float(p["temperature"][t]), 40,
+                                             float(p["top_p"][t]))
+        assert slack > 2.0 ** -14                # w is held to 2^-17 of itself here
+        want.append((few[t][tok], prob))
+    return x, p, want
+
+
+def test_the_largest_vocabulary():
+    x, p, want = _largest_vocabulary()
+    tok, prob = _call(torch.as_tensor(x).cuda(), p)
+    assert tok.tolist() == [w[0] for w in want]
+    assert (np.abs(prob - [w[1] for w in want]) <= 2.0 ** -16 * np.array([w[1] for w in want])).all()
+
+
+def test_one_value_in_a_very_long_row():
+    """2^24 + 3 equal logits: the token is the u-th part of them exactly."""
+    V = (1 << 24) + 3
+    x = torch.full((1, V), -2.5, dtype=torch.bfloat16, device="cuda")
+    p = _params(1, temperature=0.7, top_k=None, top_p=None, min_p=None, u=0.618)
+    tok, prob = _call(x, p)
+    assert tok[0] == int(np.floor(np.float64(p["u"][0]) * V))
+    assert abs(prob[0] * V - 1) <= 2.0 ** -23
