@@ -407,9 +407,9 @@ moe_status moe_add_rmsnorm(int32_t T, int32_t H, const void* y, int32_t y_fmt, i
  * x_scale [T][ceil(K / 128)] are what moe_add_rmsnorm writes; w8 [N][K] and
  * w_scale [ceil(N / 128)][ceil(K / 128)], one scale per 128 x 128 weights.
  * Codes are OCP e4m3 (no infinities; a NaN code makes the sums it enters
- * NaN), scales fp32 (a block's two are multiplied first, in fp32: their product
- * has to be a normal number, or loses what fp32 loses below it), all contiguous.  out is MOE_W_F32 or MOE_W_BF16 (rounded
- * once), out_stride elements from row to row (>= N).  Sums are fp32; for
+ * NaN), scales fp32, all contiguous.  A block's two scales are multiplied first,
+ * in fp32: a product below 2^-126 loses bits.  out is MOE_W_F32 or MOE_W_BF16
+ * (rounded once), out_stride elements from row to row (>= N).  Sums are fp32; for
  * bf16 outputs of more than 16 tokens the hardware's 8-bit products may be
  * used, which add eight neighbouring ones with 13 bits below the largest.
  * x8 and w8 16-byte aligned, K a multiple of 16, else MOE_ERR_INVALID; N and

@@ -219,7 +219,7 @@ __device__ __forceinline__ void store8(const LinearArgs& a, int t, int n, f32x4 
 // fp16 on their way from LDS.  Few tokens stream the weights (1 x 151,936 x 2048:
 // 48 us, 6.5 TB/s; a bare read of the same bytes takes 45), many are bound by LDS,
 // matrix instructions and the fma of the scales together (32,768 x 4096 x 2048:
-// 283-300 us from card to card, 1.83-1.94 PFLOP/s).
+// 281-300 us from card to card, 1.83-1.96 PFLOP/s).
 //
 // KS > 1, for few tiles: KS groups of WN x WT waves take every KS-th block each,
 // with rings of their own, and their sums are joined in a fixed order at the
@@ -460,7 +460,7 @@ __global__ __launch_bounds__(KS* WN* WT * 64) void tile_kernel(const LinearArgs 
 // the blocks: each loads its own blocks straight into registers, the next while
 // it multiplies one, and waits for nobody until the sums are joined, in a
 // fixed order, through LDS.  Bound by latency (1 x 2048 x 2048: 3.6 us; 17 x 2048
-// x 2048: 4.5) and by what one CU takes in: 16 waves instead of 8 change
+// x 2048: 4.6) and by what one CU takes in: 16 waves instead of 8 change
 // nothing, half the rows per workgroup almost halve the time while CUs are free.
 template <int NI, int KS, int OUT>
 __global__ __launch_bounds__(KS * 64) void direct_kernel(const LinearArgs a) {
