@@ -60,7 +60,8 @@ typedef enum {
   MOE_W_F32 = 0,   /* fp32, [rows][cols] */
   MOE_W_BF16 = 1,  /* bf16 bits, [rows][cols] (router, activations, logits) */
   MOE_W_Q2B32 = 2, /* 2-bit codes, 3.0 bits per weight with scale and min */
-  MOE_W_Q4B32 = 3  /* 4-bit codes, 5.0 bits per weight with scale and min */
+  MOE_W_Q4B32 = 3, /* 4-bit codes, 5.0 bits per weight with scale and min */
+  MOE_W_E4M3 = 4   /* OCP e4m3 codes with fp32 scales (moe_kv_cache only) */
 } moe_wfmt;
 
 /* One matrix pool: `n` matrices of [rows][cols] stacked by slot.
@@ -422,6 +423,103 @@ moe_status moe_scaled_linear(const uint8_t* x8, const float* x_scale, int32_t T,
                              const uint8_t* w8, const float* w_scale, int32_t N, int32_t K,
                              void* out, int32_t out_fmt, int64_t out_stride, void* ws,
                              size_t ws_bytes, void* stream);
+
+/* ---- The attention half of a decoder layer, between moe_add_rmsnorm's x and
+ * the next moe_layer ([MD] "問題": 48 layers, of which the pages describe the
+ * experts; "予測してから検証する": a verify pass of 1 + up to 3 drafts; "長い
+ * プロンプトを読む": prompts read in chunks.  They name no attention: the
+ * formulas below are the usual ones):
+ *   x8 -> moe_scaled_linear -> qkv -> moe_rope_append -> q and the cache
+ *      -> moe_paged_attention -> x8 -> moe_scaled_linear -> y
+ *
+ * Keys and values of one layer, in pages of page_size positions (a power of
+ * two).  Element (page, slot, head, d) of k sits at page * page_stride + slot *
+ * slot_stride + head * head_stride + d elements, and that of v likewise: pages
+ * of slots or of heads, keys and values in one allocation or in two.  No two
+ * elements share a place.  fmt MOE_W_BF16: bf16 bits, strides multiples of 8;
+ * MOE_W_E4M3: codes, strides multiples of 16, with one scale per (page, slot,
+ * head) in k_scale and v_scale [num_pages][page_size][Hkv], contiguous (value
+ * = code * scale).  k and v 16-byte aligned.  D: 64, 128 or 256, Hkv <= 256. */
+typedef struct {
+  int32_t num_pages, page_size, Hkv, D;
+  int32_t fmt;
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int64_t page_stride, slot_stride, head_stride;
+} moe_kv_cache;
+
+/* The sequences of one step.  Sequence b's new tokens are rows q_off[b] ..
+ * q_off[b + 1] - 1 of the step's rows (q_off [B + 1] ascending), its last
+ * one is at position kv_len[b] - 1 of the sequence, and position p lies in
+ * slot p % page_size of page page_table[b * table_stride + p / page_size].
+ * All three are device arrays, read when the kernels run (a captured graph
+ * serves every step of its B, T and table).  Entries outside [0, num_pages)
+ * are pages that are not there (never touched); positions from max_pages *
+ * page_size on and negative ones (more new tokens than kv_len) are not there
+ * either.  Rows before q_off[0] and from q_off[B] on belong to no sequence.
+ * Values that contradict each other give unspecified results, never accesses
+ * out of bounds.  Limits: 1 <= B <= 4096, max_pages * page_size <= 2^30. */
+typedef struct {
+  int32_t B;
+  int32_t max_pages;
+  const int32_t* q_off;
+  const int32_t* kv_len;
+  const int32_t* page_table;
+  int64_t table_stride;
+} moe_kv_batch;
+
+/* Frequencies of the position rotation, on the host (freq: a HOST array of
+ * R / 2 doubles; rot_scale may be NULL).  With f_j = theta^(-2 j / R):
+ *  MOE_ROPE_PLAIN   freq_j = f_j
+ *  MOE_ROPE_LINEAR  freq_j = f_j / factor
+ *  MOE_ROPE_BASE    theta * factor^(R / (R - 2)) in theta's place (R > 2)
+ *  MOE_ROPE_BANDS   f_j for pairs that turn at least `fast` times within
+ *      `context` positions, f_j / factor for those that turn at most `slow`
+ *      times, a linear mixture between the two: with d(n) = R ln(context /
+ *      (2 pi n)) / (2 ln theta), lo = max(floor(d(fast)), 0), hi =
+ *      min(ceil(d(slow)), R - 1) and w_j = clamp((j - lo) / max(hi - lo,
+ *      0.001), 0, 1): freq_j = f_j (1 - w_j) + f_j / factor w_j
+ * *rot_scale, which multiplies cosines and sines: 1, for BANDS 0.1 ln(factor)
+ * + 1.  R even, 2 <= R <= 256, theta > 1, factor >= 1 (not read by PLAIN);
+ * context >= 1 and fast > slow > 0 are read by BANDS only. */
+typedef enum {
+  MOE_ROPE_PLAIN = 0,
+  MOE_ROPE_LINEAR = 1,
+  MOE_ROPE_BASE = 2,
+  MOE_ROPE_BANDS = 3
+} moe_rope_scaling;
+
+moe_status moe_rope_frequencies(int32_t R, double theta, int32_t scaling, double factor,
+                                int32_t context, double fast, double slow, double* freq,
+                                float* rot_scale);
+
+/* Norm and rotation of the new tokens' queries and keys, keys and values into
+ * the cache.  qkv: T rows of (Hq + 2 Hkv) heads of D columns, queries, keys,
+ * values in turn, MOE_W_F32 or MOE_W_BF16, stride elements from row to row.
+ * Per query and key head a:
+ *   a = a / sqrt(mean(a^2) + eps) * weight   (q_weight, k_weight [D]; NULL: a
+ *       as it is)
+ *   the first R columns rotated by angle_j = position * freq[j] (freq: device
+ *       array of R / 2 doubles, angles in 64 bits): with c = rot_scale *
+ *       cos(angle_j), s = rot_scale * sin(angle_j) the pair (a1, a2) becomes
+ *       (a1 c - a2 s, a2 c + a1 s).  Pair j is columns j and j + R / 2, or 2 j
+ *       and 2 j + 1 (interleaved != 0).  R = 0: no rotation (freq not read).
+ * in fp32, rounded once.  Queries go to q (bf16, T rows of Hq * D, q_stride
+ * from row to row; q equal to a bf16 qkv with its stride: in place), keys
+ * and (as they are) values to their position's place in the cache; in
+ * MOE_W_E4M3 with scale = max(amax, 448 * 2^-126) / 448 per row of D, code =
+ * e4m3(value / scale).  Keys and values of positions that are not there are
+ * dropped, their queries written.  Rows of no sequence are left as they were,
+ * and so is all of the cache but the new positions.  No other output overlaps
+ * an input; two tokens that share a place leave one of theirs.  Limits: T <=
+ * 2^22, Hq <= 1024.  Results do not depend on T or on the run. */
+moe_status moe_rope_append(const moe_kv_cache* cache, const moe_kv_batch* batch, const void* qkv,
+                           int32_t qkv_fmt, int64_t stride, int32_t T, int32_t Hq,
+                           const double* freq, int32_t R, int32_t interleaved, float rot_scale,
+                           const void* q_weight, const void* k_weight, int32_t weight_fmt,
+                           float eps, uint16_t* q, int64_t q_stride, void* stream);
 
 /* Sampling: one token per row of logits ([MD] "予測してから検証する" describes
  * greedy drafts and acceptance; the pages name no sampler: the rule below is

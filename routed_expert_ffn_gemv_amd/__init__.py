@@ -17,7 +17,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libmoe.so")
 
 MOE_OK, MOE_ERR_INVALID, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_DEVICE = range(5)
-MOE_W_F32, MOE_W_BF16, MOE_W_Q2B32, MOE_W_Q4B32 = range(4)
+MOE_W_F32, MOE_W_BF16, MOE_W_Q2B32, MOE_W_Q4B32, MOE_W_E4M3 = range(5)
+MOE_ROPE_PLAIN, MOE_ROPE_LINEAR, MOE_ROPE_BASE, MOE_ROPE_BANDS = range(4)
 MOE_LAYER_MAX_T = 16
 FORMATS = {"f32": MOE_W_F32, "bf16": MOE_W_BF16, "q2": MOE_W_Q2B32, "q4": MOE_W_Q4B32}
 
@@ -30,7 +31,7 @@ EXPORTS = ("moe_status_string", "moe_version", "moe_workspace_size", "moe_route"
            "moe_set_wait_budget", "moe_set_trace", "moe_layer_noalloc",
            "moe_expert_ffn_accum", "moe_set_deterministic", "moe_add_rmsnorm",
            "moe_scaled_linear_workspace_size", "moe_scaled_linear", "moe_sample_workspace_size",
-           "moe_sample", "moe_verify_sample")
+           "moe_sample", "moe_verify_sample", "moe_rope_frequencies", "moe_rope_append")
 MOE_REFRESH_MAX_SWAPS = 1024
 
 
@@ -71,6 +72,20 @@ class moe_miss(ctypes.Structure):
 class moe_sample_params(ctypes.Structure):
     _fields_ = [("temperature", ctypes.c_void_p), ("top_k", ctypes.c_void_p),
                 ("top_p", ctypes.c_void_p), ("min_p", ctypes.c_void_p)]
+
+
+class moe_kv_cache(ctypes.Structure):
+    _fields_ = [("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("Hkv", ctypes.c_int32),
+                ("D", ctypes.c_int32), ("fmt", ctypes.c_int32), ("k", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("page_stride", ctypes.c_int64), ("slot_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class moe_kv_batch(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("q_off", ctypes.c_void_p),
+                ("kv_len", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64)]
 
 
 def _load():
@@ -139,6 +154,12 @@ def _load():
     lib.moe_sample.argtypes = [P, I32, I32, I32, I64, SA, P, P, P, P, SZ, P]
     lib.moe_verify_sample.restype = I32
     lib.moe_verify_sample.argtypes = [P, I32, I32, I32, I64, SA, P, P, P, P, P, P, SZ, P]
+    F64 = ctypes.c_double
+    lib.moe_rope_frequencies.restype = I32
+    lib.moe_rope_frequencies.argtypes = [I32, F64, I32, F64, I32, F64, F64, P, P]
+    KC, KB = ctypes.POINTER(moe_kv_cache), ctypes.POINTER(moe_kv_batch)
+    lib.moe_rope_append.restype = I32
+    lib.moe_rope_append.argtypes = [KC, KB, P, I32, I64, I32, I32, P, I32, I32, F32, P, P, I32, F32, P, I64, P]
     lib.moe_host_isa.restype = I32
     lib.moe_host_isa.argtypes = []
     lib.moe_host_miss_ffn.restype = I32
@@ -378,10 +399,10 @@ def _formats():
     import torch
     bf16 = dict.fromkeys((torch.bfloat16, torch.int16, torch.uint16), MOE_W_BF16)
     return {torch.float32: MOE_W_F32, **bf16}, (torch.uint8, torch.float8_e4m3fn), (torch.float32,), (
-        torch.int32,), (torch.uint8,)
+        torch.int32,), (torch.uint8,), (torch.float64,)
 
 
-_FMT_OF, _CODES, _F32, _I32, _U8 = _formats()
+_FMT_OF, _CODES, _F32, _I32, _U8, _F64 = _formats()
 _BF16 = tuple(t for t, f in _FMT_OF.items() if f == MOE_W_BF16)
 
 
@@ -573,6 +594,120 @@ def moe_verify_sample(logits, T, V, draft, u, out_tokens, n_out, ws, temperature
     _launch(lib.moe_verify_sample, "moe_verify_sample", dev, stream, logits.data_ptr(), fmt, T, V, row,
             par, u.data_ptr(), _ptr(draft), out_tokens.data_ptr(), _ptr(prob), n_out.data_ptr(),
             ws.data_ptr(), ws.numel())
+
+
+class KVCache:
+    """A moe_kv_cache built from torch tensors (kept alive here).  k and v:
+    [num_pages][page_size][Hkv][D], bf16 (or its bits) or e4m3 (uint8 or
+    float8_e4m3fn), alike in shape and strides; any order of the first three
+    dimensions in memory (a permuted view of head-major pages, one half of
+    an allocation of both).  e4m3: k_scale and v_scale fp32 [num_pages]
+    [page_size][Hkv], contiguous."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        if k.ndim != 4 or v.shape != k.shape or v.stride() != k.stride() or v.dtype != k.dtype:
+            raise ValueError("k, v: [num_pages][page_size][Hkv][D], alike in shape, strides and format, wanted, got "
+                             f"{list(k.shape)} and {list(v.shape)} with strides {k.stride()} and {v.stride()}")
+        if k.dtype not in _BF16 and k.dtype not in _CODES:
+            raise ValueError(f"k, v: bf16 or e4m3 codes wanted, got {k.dtype}")
+        pages, page_size, heads, D = k.shape
+        if D > 1 and k.stride(3) != 1:
+            raise ValueError("k, v: the columns of a row next to each other wanted")
+        f8 = k.dtype in _CODES
+        if f8 != (k_scale is not None) or f8 != (v_scale is not None):
+            raise ValueError("k_scale, v_scale: wanted with e4m3 codes, and only with these")
+        if f8:
+            for t, what in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+                if t.shape != k.shape[:3] or t.dtype not in _F32 or not t.is_contiguous():
+                    raise ValueError(f"{what}: contiguous fp32 {list(k.shape[:3])} wanted, got "
+                                     f"{list(t.shape)} of {t.dtype}")
+        self._keep = [k, v, k_scale, v_scale]
+        self.device = _gpu_of("KVCache", k, v, k_scale, v_scale)
+        c = moe_kv_cache()
+        c.num_pages, c.page_size, c.Hkv, c.D = pages, page_size, heads, D
+        c.fmt = MOE_W_E4M3 if f8 else MOE_W_BF16
+        c.k, c.v, c.k_scale, c.v_scale = _ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale)
+        # (the stride of a dimension of one element says nothing)
+        c.page_stride, c.slot_stride, c.head_stride = (
+            k.stride(i) if k.shape[i] > 1 else max(D, 16) for i in range(3))
+        self.cache, self.Hkv, self.D = c, heads, D
+        self.ref = ctypes.byref(c)
+
+
+class KVBatch:
+    """A moe_kv_batch built from torch tensors (kept alive here): q_off int32
+    [B + 1], kv_len int32 [B], page_table int32 [B][max_pages], whose rows may
+    be strided.  Their contents are read when a call's kernels run: a step
+    writes its numbers into the same tensors and keeps the KVBatch."""
+
+    def __init__(self, q_off, kv_len, page_table):
+        B = kv_len.numel()
+        _flat(kv_len, B, "kv_len", _I32)
+        if q_off.numel() != B + 1:
+            raise ValueError(f"q_off: {B + 1} elements wanted, got {q_off.numel()}")
+        _flat(q_off, B + 1, "q_off", _I32)
+        if page_table.ndim != 2 or page_table.shape[0] != B or page_table.dtype not in _I32:
+            raise ValueError(f"page_table: int32 [{B}][max_pages] wanted, got {list(page_table.shape)} "
+                             f"of {page_table.dtype}")
+        stride = _rows(page_table, B, page_table.shape[1], "page_table")
+        self._keep = [q_off, kv_len, page_table]
+        self.device = _gpu_of("KVBatch", q_off, kv_len, page_table)
+        b = moe_kv_batch()
+        b.B, b.max_pages, b.table_stride = B, page_table.shape[1], stride
+        b.q_off, b.kv_len, b.page_table = _ptr(q_off), _ptr(kv_len), _ptr(page_table)
+        self.batch, self.B = b, B
+        self.ref = ctypes.byref(b)
+
+
+def moe_rope_frequencies(R, theta, scaling="plain", factor=1.0, context=0, fast=32.0, slow=1.0):
+    """(freq, rot_scale) of moe_rope_append: a float64 CPU tensor of R / 2
+    frequencies (to be moved to the GPU once) and the cosines' and sines'
+    factor.  scaling: "plain", "linear", "base" or "bands"."""
+    import torch
+    kinds = {"plain": MOE_ROPE_PLAIN, "linear": MOE_ROPE_LINEAR, "base": MOE_ROPE_BASE, "bands": MOE_ROPE_BANDS}
+    if scaling not in kinds:
+        raise ValueError(f"scaling: one of {', '.join(kinds)} wanted, got {scaling!r}")
+    freq = torch.zeros(max(int(R) // 2, 1), dtype=torch.float64)
+    rot_scale = ctypes.c_float(0.0)
+    _check(lib.moe_rope_frequencies(int(R), theta, kinds[scaling], factor, int(context), fast, slow,
+                                    freq.data_ptr(), ctypes.byref(rot_scale)), "moe_rope_frequencies")
+    return freq, rot_scale.value
+
+
+def _device_of(what, cache, batch, first, *others):
+    dev = _gpu_of(what, first, *others)
+    if cache.device != dev or batch.device != dev:
+        raise ValueError(f"{what}: every tensor must be on one GPU")
+    return dev
+
+
+def moe_rope_append(cache, batch, qkv, T, Hq, q, freq=None, rot_scale=1.0, interleaved=False, q_weight=None,
+                    k_weight=None, eps=1e-6, stream=None):
+    """Query and key heads of qkv [T][(Hq + 2 Hkv) * D] (fp32 or bf16, rows may
+    be strided) normalised (q_weight, k_weight [D], fp32 or bf16 alike; None:
+    not) and rotated (freq: float64 device tensor of R / 2 frequencies, None:
+    not): queries into q (bf16 [T][Hq * D], may be qkv's own), keys and
+    values into the pages of a KVCache, at the positions a KVBatch gives."""
+    T, Hq = int(T), int(Hq)
+    D = cache.D
+    fmt, row = _fmt_of(qkv, "qkv"), _rows(qkv, T, (Hq + 2 * cache.Hkv) * D, "qkv")
+    if q.dtype not in _BF16:
+        raise ValueError(f"q: bf16 wanted, got {q.dtype}")
+    q_row = _rows(q, T, Hq * D, "q")
+    R, fp = 0, None
+    if freq is not None:
+        _flat(freq, 0, "freq", _F64)
+        R, fp = 2 * freq.numel(), freq.data_ptr()
+    w_fmt, wp = MOE_W_F32, [None, None]
+    for i, (w, what) in enumerate(((q_weight, "q_weight"), (k_weight, "k_weight"))):
+        if w is not None:
+            _flat(w, D, what, _FMT_OF)
+            w_fmt, wp[i] = _FMT_OF[w.dtype], w.data_ptr()
+    if q_weight is not None and k_weight is not None and _FMT_OF[q_weight.dtype] != w_fmt:
+        raise ValueError("q_weight, k_weight: one format wanted")
+    dev = _device_of("moe_rope_append", cache, batch, qkv, q, freq, q_weight, k_weight)
+    _launch(lib.moe_rope_append, "moe_rope_append", dev, stream, cache.ref, batch.ref, qkv.data_ptr(), fmt, row,
+            T, Hq, fp, R, 1 if interleaved else 0, rot_scale, wp[0], wp[1], w_fmt, eps, q.data_ptr(), q_row)
 
 
 def _hptr(a, dtype):

@@ -1,6 +1,7 @@
 // C ABI of the routed-MoE layer: host-side validation, workspace layout and
 // kernel dispatch.  No call allocates device memory or synchronises.
 #include <hip/hip_runtime.h>
+#include <math.h>
 #include <stdint.h>
 #include <string.h>
 
@@ -26,6 +27,10 @@ constexpr int kMaxNormH = 32768;
 constexpr int kMaxSampleT = 16384;
 constexpr int kMaxLinearK = 32768;
 constexpr int kMaxLinearN = 1 << 24;
+constexpr int kMaxKvHeads = 256;
+constexpr int kMaxQHeads = 1024;
+constexpr int kMaxBatch = 4096;
+constexpr int64_t kMaxPositions = int64_t(1) << 30;
 constexpr size_t kAlign = 256;
 constexpr int kRouterGemmMinT = 256;       // tokens from which the router runs on MFMA
 constexpr int64_t kFfnGemmMinPairs = 2048; // pairs from which the FFN runs as grouped GEMMs
@@ -297,6 +302,48 @@ PrefillEvents* prefill_events() {
 // Floating formats of the calls around the layer (activations, logits).
 bool act_fmt(int32_t fmt) { return fmt == MOE_W_F32 || fmt == MOE_W_BF16; }
 bool act_aligned(const void* p, int32_t fmt) { return aligned(p, fmt == MOE_W_F32 ? 4 : 2); }
+
+// Checks a cache and a step's sequences and fills in what the kernels take.
+moe_status check_kv(const moe_kv_cache* c, const moe_kv_batch* b, KvArgs* a) {
+  if (!c || !b) return MOE_ERR_INVALID;
+  if (c->num_pages < 1 || c->page_size < 1 || c->Hkv < 1 || c->D < 1) return MOE_ERR_INVALID;
+  if (c->fmt != MOE_W_BF16 && c->fmt != MOE_W_E4M3) return MOE_ERR_UNSUPPORTED;
+  if ((c->D != 64 && c->D != 128 && c->D != 256) || c->Hkv > kMaxKvHeads ||
+      (c->page_size & (c->page_size - 1)))
+    return MOE_ERR_UNSUPPORTED;
+  const bool f8 = c->fmt == MOE_W_E4M3;
+  if (!c->k || !c->v || !aligned(c->k, 16) || !aligned(c->v, 16)) return MOE_ERR_INVALID;
+  if (f8 && (!c->k_scale || !c->v_scale || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4)))
+    return MOE_ERR_INVALID;
+  const int64_t unit = f8 ? 16 : 8;
+  for (int64_t s : {c->page_stride, c->slot_stride, c->head_stride})
+    if (s < c->D || s % unit) return MOE_ERR_INVALID;
+  if (b->B < 1 || b->max_pages < 1 || b->table_stride < b->max_pages) return MOE_ERR_INVALID;
+  if (b->B > kMaxBatch || int64_t(b->max_pages) * c->page_size > kMaxPositions)
+    return MOE_ERR_UNSUPPORTED;
+  if (!b->q_off || !b->kv_len || !b->page_table || !aligned(b->q_off, 4) ||
+      !aligned(b->kv_len, 4) || !aligned(b->page_table, 4))
+    return MOE_ERR_INVALID;
+  a->k = static_cast<uint8_t*>(c->k);
+  a->v = static_cast<uint8_t*>(c->v);
+  a->k_scale = f8 ? c->k_scale : nullptr;
+  a->v_scale = f8 ? c->v_scale : nullptr;
+  a->page_stride = c->page_stride;
+  a->slot_stride = c->slot_stride;
+  a->head_stride = c->head_stride;
+  a->num_pages = c->num_pages;
+  a->page_shift = __builtin_ctz(unsigned(c->page_size));
+  a->Hkv = c->Hkv;
+  a->D = c->D;
+  a->f8 = f8;
+  a->B = b->B;
+  a->max_pages = b->max_pages;
+  a->q_off = b->q_off;
+  a->kv_len = b->kv_len;
+  a->page_table = b->page_table;
+  a->table_stride = b->table_stride;
+  return MOE_OK;
+}
 
 // moe_sample and moe_verify_sample (n_out set).
 moe_status run_sample(const void* logits, int32_t fmt, int32_t T, int32_t V, int64_t stride,
@@ -797,6 +844,79 @@ moe_status moe_scaled_linear(const uint8_t* x8, const float* x_scale, int32_t T,
   a.out_fmt = out_fmt;
   a.out_stride = out_stride;
   return device_status(launch_scaled_linear(a, static_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_rope_frequencies(int32_t R, double theta, int32_t scaling, double factor,
+                                int32_t context, double fast, double slow, double* freq,
+                                float* rot_scale) {
+  if (R < 2 || R % 2 || !(theta > 1.0) || !isfinite(theta) || !freq) return MOE_ERR_INVALID;
+  if (R > 256 || scaling < MOE_ROPE_PLAIN || scaling > MOE_ROPE_BANDS) return MOE_ERR_UNSUPPORTED;
+  if (scaling != MOE_ROPE_PLAIN && !(factor >= 1.0 && isfinite(factor))) return MOE_ERR_INVALID;
+  if (scaling == MOE_ROPE_BASE && R == 2) return MOE_ERR_INVALID;
+  if (scaling == MOE_ROPE_BANDS && (context < 1 || !(slow > 0.0) || !(fast > slow) || !isfinite(fast)))
+    return MOE_ERR_INVALID;
+  const double base = scaling == MOE_ROPE_BASE ? theta * pow(factor, double(R) / (R - 2)) : theta;
+  double lo = 0.0, width = 1.0;
+  if (scaling == MOE_ROPE_BANDS) {
+    // the pair that turns n times within the context
+    auto pair = [&](double n) { return R * log(context / (2.0 * M_PI * n)) / (2.0 * log(theta)); };
+    const double hi = fmin(ceil(pair(slow)), R - 1.0);
+    lo = fmax(floor(pair(fast)), 0.0);
+    width = fmax(hi - lo, 0.001);
+  }
+  for (int j = 0; j < R / 2; ++j) {
+    const double f = pow(base, -2.0 * j / R);
+    if (scaling == MOE_ROPE_LINEAR) {
+      freq[j] = f / factor;
+    } else if (scaling == MOE_ROPE_BANDS) {
+      const double w = fmin(fmax((j - lo) / width, 0.0), 1.0);
+      freq[j] = f * (1.0 - w) + f / factor * w;
+    } else {
+      freq[j] = f;
+    }
+  }
+  if (rot_scale) *rot_scale = scaling == MOE_ROPE_BANDS ? float(0.1 * log(factor) + 1.0) : 1.0f;
+  return MOE_OK;
+}
+
+moe_status moe_rope_append(const moe_kv_cache* cache, const moe_kv_batch* batch, const void* qkv,
+                           int32_t qkv_fmt, int64_t stride, int32_t T, int32_t Hq,
+                           const double* freq, int32_t R, int32_t interleaved, float rot_scale,
+                           const void* q_weight, const void* k_weight, int32_t weight_fmt,
+                           float eps, uint16_t* q, int64_t q_stride, void* stream) {
+  RopeArgs a;
+  memset(&a, 0, sizeof(a));
+  const moe_status s = check_kv(cache, batch, &a.kv);
+  if (s != MOE_OK) return s;
+  const int D = a.kv.D;
+  if (T < 0 || Hq < 1 || R < 0 || R % 2 || R > D) return MOE_ERR_INVALID;
+  if (T > kMaxT || Hq > kMaxQHeads || !act_fmt(qkv_fmt)) return MOE_ERR_UNSUPPORTED;
+  if ((q_weight || k_weight) && !act_fmt(weight_fmt)) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  const int64_t width = int64_t(Hq + 2 * a.kv.Hkv) * D;
+  if (!qkv || !q || (R && !freq) || stride < width || q_stride < int64_t(Hq) * D)
+    return MOE_ERR_INVALID;
+  if (!act_aligned(qkv, qkv_fmt) || !aligned(q, 2) || !aligned(freq, 8) ||
+      !act_aligned(q_weight, weight_fmt) || !act_aligned(k_weight, weight_fmt))
+    return MOE_ERR_INVALID;
+  if (q == qkv && (qkv_fmt != MOE_W_BF16 || q_stride != stride)) return MOE_ERR_INVALID;
+  if (!(eps >= 0.0f) || !isfinite(rot_scale)) return MOE_ERR_INVALID;
+  a.qkv = qkv;
+  a.fmt = qkv_fmt;
+  a.stride = stride;
+  a.T = T;
+  a.Hq = Hq;
+  a.freq = freq;
+  a.R = R;
+  a.interleaved = interleaved != 0;
+  a.rot_scale = rot_scale;
+  a.q_weight = q_weight;
+  a.k_weight = k_weight;
+  a.weight_fmt = weight_fmt;
+  a.eps = eps;
+  a.q = q;
+  a.q_stride = q_stride;
+  return device_status(launch_rope_append(a, static_cast<hipStream_t>(stream)));
 }
 
 moe_status moe_sample_workspace_size(int32_t T, int32_t V, size_t* bytes) {

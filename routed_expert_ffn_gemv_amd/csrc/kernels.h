@@ -120,6 +120,41 @@ struct NormArgs {
 };
 hipError_t launch_add_rmsnorm(const NormArgs& a, hipStream_t st);
 
+// paged keys and values and the sequences of a step
+struct KvArgs {
+  uint8_t* k;
+  uint8_t* v;
+  float* k_scale;              // e4m3: [num_pages][page_size][Hkv]
+  float* v_scale;
+  int64_t page_stride, slot_stride, head_stride;   // elements
+  int num_pages, page_shift, Hkv, D;
+  bool f8;
+  int B, max_pages;
+  const int32_t* q_off;        // [B + 1]
+  const int32_t* kv_len;       // [B]
+  const int32_t* page_table;
+  int64_t table_stride;
+};
+
+// head norms, rotation, append
+struct RopeArgs {
+  KvArgs kv;
+  const void* qkv;
+  int fmt;
+  int64_t stride;
+  int T, Hq;
+  const double* freq;          // [R / 2]
+  int R, interleaved;
+  float rot_scale;
+  const void* q_weight;        // [D] or null
+  const void* k_weight;
+  int weight_fmt;
+  float eps;
+  uint16_t* q;
+  int64_t q_stride;
+};
+hipError_t launch_rope_append(const RopeArgs& a, hipStream_t st);
+
 // sampling: one token per row of logits
 struct SampleArgs {
   const void* logits;
