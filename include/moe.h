@@ -521,6 +521,39 @@ moe_status moe_rope_append(const moe_kv_cache* cache, const moe_kv_batch* batch,
                            const void* q_weight, const void* k_weight, int32_t weight_fmt,
                            float eps, uint16_t* q, int64_t q_stride, void* stream);
 
+/* Attention of the new tokens over their sequences' pages.  q: bf16, T rows
+ * of Hq * D, q_stride from row to row (what moe_rope_append writes); query
+ * head h reads key and value head h / (Hq / Hkv).  The token at position p
+ * sees the positions p - window + 1 .. p (window 0: 0 .. p) that are there:
+ *   s_i = scale * q . k_i     out = sum_i exp(s_i - max s) v_i / sum_i exp(s_i - max s)
+ * A token that sees none gets zeros.  What lies in places of no position
+ * seen (later slots of the last page, other pages) has no effect, NaN and
+ * infinities included, except within a sequence's own kv_len positions, where
+ * a NaN or infinity may reach every row of its step's tokens.  Scores,
+ * maxima, sums and the weighted sums are fp32; the weights are rounded to
+ * bf16 before they multiply the values.
+ *   out: bf16, T rows of Hq * D (may be NULL)
+ *   x8, x8_scale: the unrounded out in 8 bits for moe_scaled_linear, as
+ *     moe_add_rmsnorm writes x8: [T][Hq * D] and [T][Hq * D / 128], contiguous
+ *     (may be NULL, both or neither; D 128 or 256, else MOE_ERR_UNSUPPORTED)
+ * At least one of out and x8 is not NULL; rows of no sequence are left as
+ * they were.  No output overlaps an input.  scale > 0 and finite, window >=
+ * 0, Hq a multiple of Hkv, Hq <= 1024, Hq / Hkv <= 256, T <= 2^22; pointers
+ * need their element's alignment only.  The order of the sums depends on the
+ * lengths of all sequences, T and the shapes: calls of one batch give
+ * identical bits, a sequence in another batch may differ in its last ones.
+ * Fastest where Hq / Hkv * T / B, the rows of a sequence, are near those of
+ * every sequence.  ws: moe_paged_attention_workspace_size bytes (no less for
+ * a larger T; at present the same for every B), 256-byte aligned, in use by
+ * one call at a time; what it holds before a call does not matter. */
+moe_status moe_paged_attention_workspace_size(int32_t T, int32_t B, int32_t Hq, int32_t Hkv,
+                                              int32_t D, size_t* bytes);
+moe_status moe_paged_attention(const moe_kv_cache* cache, const moe_kv_batch* batch,
+                               const uint16_t* q, int64_t q_stride, int32_t T, int32_t Hq,
+                               float scale, int32_t window, uint16_t* out, int64_t out_stride,
+                               uint8_t* x8, float* x8_scale, void* ws, size_t ws_bytes,
+                               void* stream);
+
 /* Sampling: one token per row of logits ([MD] "予測してから検証する" describes
  * greedy drafts and acceptance; the pages name no sampler: the rule below is
  * this library's).  logits: T rows of V entries, MOE_W_F32 or MOE_W_BF16,

@@ -54,12 +54,13 @@ def head_norm(a, weight, eps):
 
 def attend(q, k, v, pos, seen, scale, window=0):
     """One sequence: q [n][Hq][D] at positions pos [n], k and v [L][Hkv][D],
-    seen [L]: positions that are there.  Returns (out [n][Hq][D], spread): the
-    weighted mean of |v - out|, what errors of the weights scale with."""
+    seen [L]: positions that are there.  Returns out [n][Hq][D], and what its
+    errors scale with: the weighted means of |v - out| and |v|, and per row
+    the largest scale * sum |q k| [n][Hq][1]."""
     n, Hq, D = q.shape
     G = Hq // k.shape[1]
     at = np.arange(k.shape[0])
-    out, spread = np.zeros((n, Hq, D)), np.zeros((n, Hq, D))
+    out, spread, level, mag = (np.zeros((n, Hq, w)) for w in (D, D, D, 1))
     for i in range(n):
         keep = seen & (at <= pos[i])
         if window:
@@ -67,10 +68,12 @@ def attend(q, k, v, pos, seen, scale, window=0):
         if not keep.any():
             continue
         for h in range(Hq):
-            s = (k[keep, h // G] @ q[i, h]) * scale
+            kk, vv = k[keep, h // G], v[keep, h // G]
+            s = (kk @ q[i, h]) * scale
             w = np.exp(s - s.max())
             w /= w.sum()
-            vv = v[keep, h // G]
             out[i, h] = w @ vv
             spread[i, h] = w @ np.abs(vv - out[i, h])
-    return out, spread
+            level[i, h] = w @ np.abs(vv)
+            mag[i, h] = (np.abs(kk) @ np.abs(q[i, h])).max() * scale
+    return out, spread, level, mag

@@ -31,7 +31,8 @@ EXPORTS = ("moe_status_string", "moe_version", "moe_workspace_size", "moe_route"
            "moe_set_wait_budget", "moe_set_trace", "moe_layer_noalloc",
            "moe_expert_ffn_accum", "moe_set_deterministic", "moe_add_rmsnorm",
            "moe_scaled_linear_workspace_size", "moe_scaled_linear", "moe_sample_workspace_size",
-           "moe_sample", "moe_verify_sample", "moe_rope_frequencies", "moe_rope_append")
+           "moe_sample", "moe_verify_sample", "moe_rope_frequencies", "moe_rope_append",
+           "moe_paged_attention_workspace_size", "moe_paged_attention")
 MOE_REFRESH_MAX_SWAPS = 1024
 
 
@@ -160,6 +161,10 @@ def _load():
     KC, KB = ctypes.POINTER(moe_kv_cache), ctypes.POINTER(moe_kv_batch)
     lib.moe_rope_append.restype = I32
     lib.moe_rope_append.argtypes = [KC, KB, P, I32, I64, I32, I32, P, I32, I32, F32, P, P, I32, F32, P, I64, P]
+    lib.moe_paged_attention_workspace_size.restype = I32
+    lib.moe_paged_attention_workspace_size.argtypes = [I32, I32, I32, I32, I32, ctypes.POINTER(SZ)]
+    lib.moe_paged_attention.restype = I32
+    lib.moe_paged_attention.argtypes = [KC, KB, P, I64, I32, I32, F32, I32, P, I64, P, P, P, SZ, P]
     lib.moe_host_isa.restype = I32
     lib.moe_host_isa.argtypes = []
     lib.moe_host_miss_ffn.restype = I32
@@ -708,6 +713,44 @@ def moe_rope_append(cache, batch, qkv, T, Hq, q, freq=None, rot_scale=1.0, inter
     dev = _device_of("moe_rope_append", cache, batch, qkv, q, freq, q_weight, k_weight)
     _launch(lib.moe_rope_append, "moe_rope_append", dev, stream, cache.ref, batch.ref, qkv.data_ptr(), fmt, row,
             T, Hq, fp, R, 1 if interleaved else 0, rot_scale, wp[0], wp[1], w_fmt, eps, q.data_ptr(), q_row)
+
+
+def moe_paged_attention_workspace_size(T, B, Hq, Hkv, D):
+    n = ctypes.c_size_t(0)
+    _check(lib.moe_paged_attention_workspace_size(int(T), int(B), int(Hq), int(Hkv), int(D), ctypes.byref(n)),
+           "moe_paged_attention_workspace_size")
+    return n.value
+
+
+def moe_paged_attention(cache, batch, q, T, Hq, scale, ws, out=None, x8=None, x8_scale=None, window=0,
+                        stream=None):
+    """Attention of the new tokens q [T][Hq * D] (bf16, rows may be strided)
+    over the pages of a KVCache, for the sequences of a KVBatch: into out (bf16
+    [T][Hq * D]) and/or x8 (e4m3 codes, uint8 or float8_e4m3fn) with x8_scale
+    (fp32 [T][Hq * D / 128]).  window: positions that a token sees, 0: all up
+    to its own.  ws: uint8 device tensor of at least
+    moe_paged_attention_workspace_size(T, B, Hq, Hkv, D) bytes."""
+    T, Hq = int(T), int(Hq)
+    width = Hq * cache.D
+    if q.dtype not in _BF16:
+        raise ValueError(f"q: bf16 wanted, got {q.dtype}")
+    q_row = _rows(q, T, width, "q")
+    op = xp = sp = None
+    out_row = 0
+    if out is not None:
+        if out.dtype not in _BF16:
+            raise ValueError(f"out: bf16 wanted, got {out.dtype}")
+        op, out_row = out.data_ptr(), _rows(out, T, width, "out")
+    if x8 is not None:
+        _matrix(x8, T, width, "x8", _CODES)
+        xp = x8.data_ptr()
+    if x8_scale is not None:
+        _matrix(x8_scale, T, width // 128, "x8_scale", _F32)
+        sp = x8_scale.data_ptr()
+    _flat(ws, 0, "ws", _U8)
+    dev = _device_of("moe_paged_attention", cache, batch, q, ws, out, x8, x8_scale)
+    _launch(lib.moe_paged_attention, "moe_paged_attention", dev, stream, cache.ref, batch.ref, q.data_ptr(), q_row,
+            T, Hq, scale, int(window), op, out_row, xp, sp, ws.data_ptr(), ws.numel())
 
 
 def _hptr(a, dtype):

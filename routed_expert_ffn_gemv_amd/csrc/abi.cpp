@@ -29,6 +29,7 @@ constexpr int kMaxLinearK = 32768;
 constexpr int kMaxLinearN = 1 << 24;
 constexpr int kMaxKvHeads = 256;
 constexpr int kMaxQHeads = 1024;
+constexpr int kMaxHeadGroup = 256;     // query heads per key head
 constexpr int kMaxBatch = 4096;
 constexpr int64_t kMaxPositions = int64_t(1) << 30;
 constexpr size_t kAlign = 256;
@@ -917,6 +918,52 @@ moe_status moe_rope_append(const moe_kv_cache* cache, const moe_kv_batch* batch,
   a.q = q;
   a.q_stride = q_stride;
   return device_status(launch_rope_append(a, static_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_paged_attention_workspace_size(int32_t T, int32_t B, int32_t Hq, int32_t Hkv,
+                                              int32_t D, size_t* bytes) {
+  if (!bytes || T < 0 || B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv) return MOE_ERR_INVALID;
+  if (T > kMaxT || B > kMaxBatch || Hq > kMaxQHeads || Hkv > kMaxKvHeads ||
+      Hq / Hkv > kMaxHeadGroup || (D != 64 && D != 128 && D != 256))
+    return MOE_ERR_UNSUPPORTED;
+  *bytes = up(attention_ws(T, Hq, Hkv, D));
+  return MOE_OK;
+}
+
+moe_status moe_paged_attention(const moe_kv_cache* cache, const moe_kv_batch* batch,
+                               const uint16_t* q, int64_t q_stride, int32_t T, int32_t Hq,
+                               float scale, int32_t window, uint16_t* out, int64_t out_stride,
+                               uint8_t* x8, float* x8_scale, void* ws, size_t ws_bytes,
+                               void* stream) {
+  AttnArgs a;
+  memset(&a, 0, sizeof(a));
+  moe_status s = check_kv(cache, batch, &a.kv);
+  if (s != MOE_OK) return s;
+  size_t need = 0;
+  s = moe_paged_attention_workspace_size(T, a.kv.B, Hq, a.kv.Hkv, a.kv.D, &need);
+  if (s != MOE_OK) return s;
+  if (x8 && a.kv.D % 128) return MOE_ERR_UNSUPPORTED;
+  if (!(scale > 0.0f) || !isfinite(scale) || window < 0) return MOE_ERR_INVALID;
+  if (T == 0) return MOE_OK;
+  const int64_t width = int64_t(Hq) * a.kv.D;
+  if (!q || (!out && !x8) || !x8 != !x8_scale || q_stride < width || (out && out_stride < width))
+    return MOE_ERR_INVALID;
+  if (!aligned(q, 2) || !aligned(out, 2) || !aligned(x8_scale, 4)) return MOE_ERR_INVALID;
+  if (!ws || !aligned(ws, kAlign)) return MOE_ERR_INVALID;
+  if (ws_bytes < need) return MOE_ERR_WORKSPACE;
+  a.q = q;
+  a.q_stride = q_stride;
+  a.T = T;
+  a.Hq = Hq;
+  a.G = Hq / a.kv.Hkv;
+  a.scale2 = scale * 1.44269504088896341f;   // log2(e)
+  a.window = window;
+  a.out = out;
+  a.out_stride = out ? out_stride : 0;
+  a.x8 = x8;
+  a.x8_scale = x8_scale;
+  a.ws = ws;
+  return device_status(launch_paged_attention(a, static_cast<hipStream_t>(stream)));
 }
 
 moe_status moe_sample_workspace_size(int32_t T, int32_t V, size_t* bytes) {

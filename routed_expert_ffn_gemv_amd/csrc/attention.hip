@@ -1,0 +1,832 @@
+// Attention of a step's new tokens over the paged cache of their sequences.
+//
+// Per new token and query head, over the positions p it sees:
+//   out = sum_p exp(s_p - m) v_p / sum_p exp(s_p - m),   s_p = scale * q . k_p
+// in one pass: a running m, sum and weighted sum of values.
+//
+// Rows and tiles.  The G = Hq / Hkv query heads that share a key head are
+// rows of one tile with it: row r of a tile is token r / G, head r % G, so
+// that keys and values are read once for all of them.  A tile has QT tokens
+// (QT * G <= 32 RW rows: 32 per wave, RW waves), and walks over the
+// positions in steps of KW * KS: KW groups of waves take KS each.
+//
+// Products.  Scores are formed as S^T = K Q^T (32 x 32 x 16 bf16 products:
+// positions are the instruction's rows, query rows its columns), so a lane
+// holds 16 positions of one query row: the row's maximum is 15 maxima and one
+// exchange with lane ^ 32, and the factors that rescale a row are the lane's
+// own.  The weights' order is already that of the second product's operand
+// (O^T = V^T P^T) if its position 8 h + j (h = lane / 32) is taken to be 8 (j
+// / 4) + 4 h + j % 4 of 16: the order of a sum's terms is free as long as
+// both operands agree, and the transposing LDS reads of V take four (16 bits)
+// or any eight (8 bits) positions at a time.
+//
+// Weights are rounded to bf16 for the second product (V is bf16 itself), off
+// by 2^-8 of a weight at most, and the sum that divides them is that of the
+// rounded ones: what is left is at most 2^-8 of the weighted mean of |v -
+// out|, and much less over many positions, whose roundings go either way.  With an 8-bit cache codes become bf16
+// (exact), a position's key scale multiplies its scores and its value scale
+// its weights before their rounding; the sum is then that of the unrounded.
+//
+// The running maximum is only raised when a row's grows by more than 2^8:
+// weights are then at most 2^8, sums of 2^30 of them far from fp32's end, and
+// most steps leave the output's registers alone.
+//
+// Work.  All tiles' steps form one line (sequence, key head, pairs of the
+// first and the last query tile, the second and the last but one ..., whose
+// steps together are about the same whatever the mask), cut into equal runs,
+// one per workgroup: a decode batch of any lengths, one long text and a
+// prompt fill the GPU alike.  A workgroup finds its run from the lengths
+// alone.  Tiles that are cut leave their parts (fp32, unnormalised) in the
+// workspace and join_kernel adds them up in order.
+
+#include <hip/hip_runtime.h>
+
+#include "kernels.h"
+
+namespace moe {
+namespace {
+
+typedef __attribute__((ext_vector_type(2))) float f32x2;
+typedef __attribute__((ext_vector_type(4))) float f32x4;
+typedef __attribute__((ext_vector_type(16))) float f32x16;
+typedef __attribute__((ext_vector_type(4))) short s16x4;
+typedef __attribute__((ext_vector_type(2))) int i32x2;
+typedef __attribute__((ext_vector_type(4))) __bf16 bf16x4;
+typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
+typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
+typedef u32x4 __attribute__((aligned(2))) u32x4_any;
+typedef u32x2 __attribute__((aligned(2))) u32x2_any;
+typedef uint32_t __attribute__((aligned(1))) u32_any;
+
+#define MOE_LDS __attribute__((address_space(3)))
+
+constexpr int kCus = 256;
+constexpr int kMaxLds = 160 * 1024;
+constexpr int kIds = 1024;                          // page numbers a workgroup holds at a time
+constexpr float kE4m3Max = 448.0f;
+constexpr float kScaleFloor = 448.0f * 0x1p-126f;   // keeps every scale a normal number
+constexpr float kRaise = 8.0f;                      // log2 of the largest weight
+
+__device__ const u32x4 kZeros = {0u, 0u, 0u, 0u};   // what a position that is not there reads
+
+// ---- loads straight to LDS, and waits for them
+//
+// In assembly, because the compiler waits for all of them before the next
+// read of any part of LDS.  vmcnt counts in the order of issue, the
+// compiler's own loads and stores among them, so the waits here are only
+// ever longer than need be.  A load writes no register.  Reads of what they
+// fill stay behind a wait that clobbers memory, and the loads stay behind
+// the wait or barrier after the last reads of what they overwrite, as
+// volatile assembly keeps its order.  The s_nop: 5 wait states between a
+// vector write of a scalar operand and its use here.
+#pragma clang diagnostic ignored "-Winline-asm"     // M0 among the clobbered registers
+
+__device__ __forceinline__ void to_lds16(const uint8_t* p, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(p) : "m0");
+}
+__device__ __forceinline__ void to_lds4(const void* p, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(p) : "m0");
+}
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  static_assert(N >= 0 && N <= 63, "vmcnt");
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+// This wave's reads of LDS have ended.
+__device__ __forceinline__ void wait_reads() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+// A barrier that leaves loads and stores under way.
+__device__ __forceinline__ void barrier_lds() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+__device__ __forceinline__ uint32_t lds_address(const MOE_LDS uint8_t* p) {
+  return __builtin_amdgcn_readfirstlane(uint32_t(reinterpret_cast<uintptr_t>(p)));
+}
+
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  const f32x2 v = {a, b};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2_t));
+}
+
+// Eight e4m3 codes as bf16 (exact).
+__device__ __forceinline__ bf16x8 from_codes(i32x2 c) {
+  u32x4 r;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    r[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[i], 1.0f, false));
+    r[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[i], 1.0f, true));
+  }
+  return __builtin_bit_cast(bf16x8, r);
+}
+
+// The value of lane ^ 32 and the lane's own, in one order for both.
+__device__ __forceinline__ f32x2 both_halves(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return f32x2{__uint_as_float(r[0]), __uint_as_float(r[1])};
+}
+
+__device__ __forceinline__ float exp2_fast(float v) { return __builtin_amdgcn_exp2f(v); }
+
+// ---- the line of work
+
+struct Seq {
+  int row0, n;          // its rows
+  int off;              // position of its first new token
+  int len;              // positions that may be there
+  int nq;               // query tiles
+  int64_t pair, mid;    // steps set aside for a pair of tiles and for an unpaired one in the middle
+  int64_t head;         // for a key head
+};
+
+template <int STEP>
+__device__ __forceinline__ int tile_steps(const AttnArgs& a, const Seq& s, int qt, int* k0) {
+  const int t0 = qt * a.QT, t1 = min(s.n, t0 + a.QT);
+  const int end = min(max(s.off + t1, 0), s.len);
+  const int start = a.window ? max(s.off + t0 - (a.window - 1), 0) : 0;
+  *k0 = start / STEP;
+  return max(1, (end + STEP - 1) / STEP - *k0);
+}
+
+template <int STEP>
+__device__ __forceinline__ Seq seq_of(const AttnArgs& a, int b) {
+  Seq s;
+  s.row0 = min(max(a.kv.q_off[b], 0), a.T);
+  s.n = min(max(a.kv.q_off[b + 1], s.row0), a.T) - s.row0;
+  const int len = min(max(a.kv.kv_len[b], 0), 1 << 30);
+  s.off = len - s.n;
+  s.len = min(len, a.kv.max_pages << a.kv.page_shift);
+  s.nq = (s.n + a.QT - 1) / a.QT;
+  s.pair = s.mid = s.head = 0;
+  if (!s.n) return s;
+  // the most steps that a tile takes
+  int64_t most = (s.len + STEP - 1) / STEP;
+  if (a.window) most = min(most, (int64_t(a.window) + a.QT) / STEP + 2);
+  most = max(most, int64_t(1));
+  s.pair = 2 * most;
+  // tiles qt and nq - 1 - qt end at positions that add up to the same
+  if (s.off >= 0) s.pair = min(s.pair, (2 * int64_t(s.off) + int64_t(s.nq + 1) * a.QT) / STEP + 2);
+  int k0;
+  if (s.nq & 1) s.mid = tile_steps<STEP>(a, s, s.nq / 2, &k0);
+  s.head = (s.nq / 2) * s.pair + s.mid;
+  return s;
+}
+
+// Sum over the workgroup and the exclusive prefix of 64-bit numbers.
+template <int THREADS>
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* tmp, int64_t* total) {
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+  int64_t x = v;
+#pragma unroll
+  for (int d = 1; d < kWave; d <<= 1) {
+    const int64_t y = __shfl_up(x, d, kWave);
+    if (lane >= d) x += y;
+  }
+  __syncthreads();
+  if (lane == kWave - 1) tmp[wave] = x;
+  __syncthreads();
+  int64_t before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / kWave; ++w) {
+    if (w < wave) before += tmp[w];
+    all += tmp[w];
+  }
+  *total = all;
+  return before + x - v;
+}
+
+// What join_kernel needs of the tile that runs through the start of a
+// workgroup's run, at the first such start of a tile.
+struct Joint {
+  int32_t parts;        // 0: nothing to join here
+  int32_t first;        // the workgroup with the first part (its second slot; the others': their first)
+  int32_t row0, tokens, head;
+  int32_t pad[3];
+};
+
+// Rows of the tile: query head and row of the batch.
+struct RowAt {
+  int row, head;
+};
+
+// A token's output, four columns per lane (D / 4 lanes a row).
+__device__ __forceinline__ void store_row4(const AttnArgs& a, int64_t row, int head, int D, int col, f32x4 v) {
+  if (a.out) {
+    const u32x2 p = {pack2(v[0], v[1]), pack2(v[2], v[3])};
+    *reinterpret_cast<u32x2_any*>(a.out + row * a.out_stride + int64_t(head) * D + col) = p;
+  }
+  if (a.x8) {
+    // 128 columns share a scale: 32 lanes
+    float m = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
+    m = fmaxf(m, dpp_f32<0xB1>(m));
+    m = fmaxf(m, dpp_f32<0x4E>(m));
+    m = fmaxf(m, dpp_f32<0x141>(m));
+    m = fmaxf(m, dpp_f32<0x140>(m));
+    m = fmaxf(m, __shfl_xor(m, 16, kWave));
+    const float s = fmaxf(m, kScaleFloor) / kE4m3Max;
+    int c = __builtin_amdgcn_cvt_pk_fp8_f32(v[0] / s, v[1] / s, 0, false);
+    c = __builtin_amdgcn_cvt_pk_fp8_f32(v[2] / s, v[3] / s, c, true);
+    const int64_t at = (row * a.Hq + head) * D + col;
+    *reinterpret_cast<u32_any*>(a.x8 + at) = uint32_t(c);
+    if (col % 128 == 0) a.x8_scale[at / 128] = s;
+  }
+}
+
+// ---- the kernel
+
+template <int D_, bool F8_, int RW_, int KW_, int KS_, int NS_>
+struct Shape {
+  static constexpr int D = D_, RW = RW_, KW = KW_, KS = KS_, NS = NS_;
+  static constexpr bool F8 = F8_;
+  static constexpr int kWaves = RW * KW, kThreads = kWaves * kWave;
+  static constexpr int kRows = 32 * RW;
+  static constexpr int kStep = KW * KS;
+  static constexpr int kPitch = D * (F8 ? 1 : 2);           // bytes of a position's row
+  static constexpr int kChunks = kPitch / 16;
+  static constexpr int kArea = KS * kPitch;                 // keys (or values) of a group's step
+  static constexpr int kLoads = kArea / 1024;               // 1 KiB loads for it
+  static constexpr int kRing = KW * NS * 2 * kArea;
+  static constexpr int kScales = F8 ? KW * (NS + 1) * 2 * KS * 4 : 0;
+  static constexpr int kCols = D < 128 ? D : 128;           // columns of an epilogue's round
+  static constexpr int kOutPitch = kCols + 4;               // (rows 4 banks apart)
+  static constexpr int kOut = kWaves * 32 * kOutPitch * 4;
+  static constexpr int kData = kRing + kScales > kOut ? kRing + kScales : kOut;
+  static constexpr int kLds = kData + kIds * 4 + kWaves * 32 * 8;
+  static constexpr int kPerCu = kMaxLds / (kLds + 512) >= 2 && kThreads <= 256 ? 2 : 1;
+  static_assert(kLds + 512 <= kMaxLds && (RW == 1 || NS == 2) && (KS == 32 || KS == 64), "shape");
+  static_assert(RW == 1 || 2 * kLoads % RW == 0, "loads");
+
+  // Permutations of a row's 16-byte chunks in LDS, so that what is read
+  // together meets no bank twice: keys, 16 rows of one chunk; values, 4 rows
+  // of 4 chunks (16 bits) or 8 of 2 (8 bits).
+  static __device__ __forceinline__ int key_swizzle(int row) {
+    return kPitch >= 256 ? row & 15 : kPitch == 128 ? (row >> 1) & 7 : (row >> 2) & 3;
+  }
+  static __device__ __forceinline__ int value_swizzle(int row) {
+    if (!F8) return kPitch >= 256 ? (row & 3) << 2 : ((row >> 1) & 1) << 2;
+    if (kPitch == 256) return ((row & 3) | ((row >> 1) & 4)) << 1;
+    if (kPitch == 128) return (((row >> 1) & 1) | ((row >> 2) & 2)) << 1;
+    return ((row >> 3) & 1) << 1;
+  }
+};
+
+template <class S>
+__global__ __launch_bounds__(S::kThreads, S::kPerCu * S::kThreads / 256) void attention_kernel(const AttnArgs a) {
+  constexpr int D = S::D, RW = S::RW, KW = S::KW, KS = S::KS, NS = S::NS, STEP = S::kStep, NB = KS / 32;
+  constexpr bool F8 = S::F8;
+  extern __shared__ __align__(256) uint8_t smem[];
+  __shared__ int64_t scan_tmp[S::kWaves];
+  __shared__ int64_t found[2];
+  MOE_LDS uint8_t* const lds = (MOE_LDS uint8_t*)smem;
+  int32_t* const ids = reinterpret_cast<int32_t*>(smem + S::kData);
+  f32x2* const stats = reinterpret_cast<f32x2*>(smem + S::kData + kIds * 4);   // [waves][32]: maximum, sum
+
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int kw = wave / RW, rw = wave % RW;
+  const int col = lane & 31, half = lane >> 5;
+  // neighbouring runs on one XCD (workgroups go to the 8 in turn): they share keys and values
+  const int me = int(blockIdx.x & 7) * (a.grid >> 3) + int(blockIdx.x >> 3);
+
+  // where this workgroup's run starts
+  int64_t total = 0, mine = 0;
+  for (int base = 0; base < a.kv.B; base += S::kThreads) {
+    const int b = base + threadIdx.x;
+    mine = b < a.kv.B ? a.kv.Hkv * seq_of<STEP>(a, b).head : 0;
+    int64_t sum;
+    block_scan<S::kThreads>(mine, scan_tmp, &sum);
+    total += sum;
+  }
+  const int64_t run = max(int64_t(a.min_steps), (total + a.grid - 1) / a.grid);
+  int64_t x = me * run;
+  const int64_t x1 = min(total, x + run);
+  Joint* const joint = static_cast<Joint*>(a.joints) + me;
+  if (x >= total) {
+    if (threadIdx.x == 0) joint->parts = 0;
+    return;
+  }
+  int64_t before = 0;
+  for (int base = 0; base < a.kv.B; base += S::kThreads) {
+    const int b = base + threadIdx.x;
+    if (a.kv.B > S::kThreads) mine = b < a.kv.B ? a.kv.Hkv * seq_of<STEP>(a, b).head : 0;
+    int64_t sum;
+    const int64_t at = before + block_scan<S::kThreads>(mine, scan_tmp, &sum);
+    if (mine > 0 && x >= at && x < at + mine) found[0] = b, found[1] = x - at;
+    before += sum;
+    if (x < before) break;
+  }
+  __syncthreads();
+  int b = __builtin_amdgcn_readfirstlane(int(found[0]));
+  int64_t r = found[1];
+  r = (int64_t(__builtin_amdgcn_readfirstlane(int(r >> 32))) << 32) |
+      uint32_t(__builtin_amdgcn_readfirstlane(int(r)));
+  bool starts = true;       // the run's first tile
+
+  while (x < x1) {
+    const Seq s = seq_of<STEP>(a, b);
+    if (r >= a.kv.Hkv * s.head) {
+      ++b, r = 0;
+      continue;
+    }
+    // which tile, and from which of its steps
+    const int h = int(r / s.head);
+    const int64_t in_head = r - h * s.head;
+    const int pairs = s.nq / 2;
+    int qt, tile0, steps;           // query tile; its first step; its number of steps
+    int from;                       // steps done by the workgroups before
+    if (in_head >= pairs * s.pair) {
+      qt = pairs;
+      steps = tile_steps<STEP>(a, s, qt, &tile0);
+      from = int(in_head - pairs * s.pair);
+    } else {
+      qt = int(in_head / s.pair);
+      from = int(in_head - qt * s.pair);
+      steps = tile_steps<STEP>(a, s, qt, &tile0);
+      if (from >= steps) {
+        from -= steps;
+        qt = s.nq - 1 - qt;
+        steps = tile_steps<STEP>(a, s, qt, &tile0);
+        if (from >= steps) {        // what the pair does not need
+          const int64_t skip = s.pair - (in_head - int64_t(s.nq - 1 - qt) * s.pair);
+          x += skip, r += skip;
+          starts = false;
+          if (threadIdx.x == 0 && x - skip == me * run) joint->parts = 0;
+          continue;
+        }
+      }
+    }
+    const int take = int(min(int64_t(steps - from), x1 - x));
+    const bool whole = from == 0 && take == steps;
+    const int t0 = qt * a.QT, nt = min(s.n - t0, a.QT);
+    const int slot = me * 2 + (from == 0 ? 1 : 0);
+    if (starts && threadIdx.x == 0) {
+      const int64_t begin = x - from, end = begin + steps;
+      const int64_t first = begin / run, last = (end - 1) / run;
+      Joint j;
+      j.parts = from > 0 && first == me - 1 ? int(last - first + 1) : 0;
+      j.first = int(first);
+      j.row0 = s.row0 + t0;
+      j.tokens = nt;
+      j.head = h;
+      *joint = j;
+    }
+    starts = false;
+    x += take, r += take;
+
+    // ---- the tile's queries: this wave's 32 rows, as the products' right operand
+    const int lr = rw * 32 + col;                       // this lane's row of the tile
+    const int token = lr / a.G;
+    const bool live = token < nt;
+    const int rpos = live ? s.off + t0 + token : -1;    // the last position it sees
+    const int rfirst = a.window ? max(rpos - (a.window - 1), 0) : 0;
+    bf16x8 q[D / 16];
+    {
+      const uint16_t* qp = a.q + int64_t(s.row0 + t0 + (live ? token : 0)) * a.q_stride +
+                           int64_t(h * a.G + (lr - token * a.G)) * D + half * 8;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        u32x4 v = {0u, 0u, 0u, 0u};
+        if (live) v = *reinterpret_cast<const u32x4_any*>(qp + i * 16);
+        q[i] = __builtin_bit_cast(bf16x8, v);
+      }
+    }
+    // what every row of this wave sees, and what any does
+    const int wave_t1 = min(nt - 1, (rw * 32 + 31) / a.G), wave_t0 = min(rw * 32 / a.G, nt - 1);
+    const bool wave_live = rw * 32 / a.G < nt;
+    const int sees_all = s.off + t0 + wave_t0;                                    // up to here
+    const int sees_any = wave_live ? s.off + t0 + wave_t1 : -1;
+    const int from_all = a.window ? s.off + t0 + wave_t1 - (a.window - 1) : 0;     // from here
+    const int from_any = a.window ? s.off + t0 + wave_t0 - (a.window - 1) : 0;
+
+    f32x16 o[D / 32];
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) o[i][j] = 0.0f;
+    float mref = -INFINITY, sum = 0.0f;
+
+    // ---- the positions, as far as the page numbers held in LDS reach
+    const int64_t elem = F8 ? 1 : 2;
+    const uint8_t* const kbase = a.kv.k + int64_t(h) * a.kv.head_stride * elem;
+    const uint8_t* const vbase = a.kv.v + int64_t(h) * a.kv.head_stride * elem;
+    const int shift = a.kv.page_shift;
+    const int span = max(1, int(min(int64_t(kIds - 1) << shift, int64_t(1) << 30)) / STEP);
+    for (int s0 = 0; s0 < take; s0 += span) {
+      const int count = min(span, take - s0);
+      const int step0 = tile0 + from + s0;
+      const int page0 = int((int64_t(step0) * STEP) >> shift);
+      const int pages = int(((int64_t(step0 + count) * STEP - 1) >> shift) - page0) + 1;
+      __syncthreads();        // the ids, and all of LDS, have been used up
+      for (int i = threadIdx.x; i < pages; i += S::kThreads) {
+        int id = -1;
+        if (page0 + i < a.kv.max_pages) id = a.kv.page_table[b * a.kv.table_stride + page0 + i];
+        ids[i] = id >= 0 && id < a.kv.num_pages ? id : -1;
+      }
+      __syncthreads();
+
+      // page of a position, or -1 if the position is not there
+      auto page_of = [&](int pos) -> int { return pos < s.len ? ids[(pos >> shift) - page0] : -1; };
+      auto slot_lds = [&](int st, bool value) -> MOE_LDS uint8_t* {
+        return lds + ((kw * NS + st) * 2 + (value ? 1 : 0)) * S::kArea;
+      };
+      auto scales_of = [&](int i, bool value) -> MOE_LDS uint8_t* {
+        return lds + S::kRing + ((kw * (NS + 1) + i % (NS + 1)) * 2 + (value ? 1 : 0)) * KS * 4;
+      };
+      // load j of step i's keys or values
+      auto load = [&](int i, int j, bool value) {
+        const int row = j * (64 / S::kChunks) + lane / S::kChunks, pc = lane % S::kChunks;
+        const int pos = (step0 + i) * STEP + kw * KS + row;
+        const int id = page_of(pos);
+        const int c = pc ^ (value ? S::value_swizzle(row) : S::key_swizzle(row));
+        const uint8_t* p = (value ? vbase : kbase) +
+                           (id * a.kv.page_stride + (pos & ((1 << shift) - 1)) * a.kv.slot_stride) * elem + c * 16;
+        if (id < 0) p = reinterpret_cast<const uint8_t*>(&kZeros);
+        to_lds16(p, lds_address(slot_lds(i % NS, value) + j * 1024));
+      };
+      auto load_scales = [&](int i, bool value) {
+        // (32 positions: the lower half of the wave keys', the upper values')
+        const bool up = KS == 32 ? half : value;
+        const int row = KS == 32 ? col : lane;
+        const int pos = (step0 + i) * STEP + kw * KS + row;
+        const int id = page_of(pos);
+        const float* p = (up ? a.kv.v_scale : a.kv.k_scale) +
+                         ((int64_t(id) << shift) + (pos & ((1 << shift) - 1))) * a.kv.Hkv + h;
+        if (id < 0) p = reinterpret_cast<const float*>(&kZeros);
+        to_lds4(p, lds_address(scales_of(i, KS == 32 ? false : value)));
+      };
+      constexpr int kScaleLoads = F8 ? 1 : 0;      // with the keys of a wave's own step
+      auto load_keys = [&](int i) {
+#pragma unroll
+        for (int j = 0; j < S::kLoads; ++j) load(i, j, false);
+        if (F8) load_scales(i, false);
+      };
+      auto load_values = [&](int i) {
+#pragma unroll
+        for (int j = 0; j < S::kLoads; ++j) load(i, j, true);
+      };
+      // RW waves share a step's loads
+      auto load_shared = [&](int i) {
+#pragma unroll
+        for (int j = 0; j < 2 * S::kLoads / RW; ++j) {
+          const int g = rw * (2 * S::kLoads / RW) + j;
+          const bool value = g >= S::kLoads;
+          load(i, value ? g - S::kLoads : g, value);
+        }
+        if (F8 && rw < (KS == 32 ? 1 : 2)) load_scales(i, rw == 1);
+      };
+
+      if constexpr (RW == 1) {
+        for (int i = 0; i < NS && i < count; ++i) {
+          load_keys(i);
+          load_values(i);
+        }
+      } else {
+        load_shared(0);
+      }
+
+      for (int i = 0; i < count; ++i) {
+        if constexpr (RW == 1) {
+          // behind these keys: NS values and NS - 1 keys, if the end is not near
+          if (i + NS <= count)
+            wait_loads<(2 * NS - 1) * S::kLoads + (NS - 1) * kScaleLoads>();
+          else
+            wait_loads<0>();
+        } else {
+          wait_loads<0>();
+          barrier_lds();
+          if (i + 1 < count) load_shared(i + 1);
+        }
+        const int pos0 = (step0 + i) * STEP + kw * KS;      // this group's positions
+        MOE_LDS uint8_t* const kl = slot_lds(i % NS, false);
+        MOE_LDS uint8_t* const vl = slot_lds(i % NS, true);
+
+        // which of the positions are there
+        uint32_t there[NB];
+        bool all = true;
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+          there[n] = uint32_t(__ballot(page_of(pos0 + n * 32 + col) >= 0));
+          all = all && there[n] == 0xFFFFFFFFu;
+        }
+        const bool any = pos0 <= sees_any && pos0 + KS > from_any;
+        f32x16 sc[NB];
+        if (any) {
+#pragma unroll
+          for (int n = 0; n < NB; ++n) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) sc[n][j] = 0.0f;
+            const int row = n * 32 + col;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+              bf16x8 kf;
+              if (F8)
+                kf = from_codes(*(MOE_LDS i32x2*)(kl + row * S::kPitch + (k ^ S::key_swizzle(row)) * 16 + half * 8));
+              else
+                kf = *(MOE_LDS bf16x8*)(kl + row * S::kPitch + ((2 * k + half) ^ S::key_swizzle(row)) * 16);
+              sc[n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, q[k], sc[n], 0, 0, 0);
+            }
+          }
+          if (F8) {
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+#pragma unroll
+              for (int g = 0; g < 4; ++g) {
+                const f32x4 w = *(MOE_LDS f32x4*)(scales_of(i, false) + (n * 32 + 8 * g + 4 * half) * 4);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sc[n][4 * g + e] *= w[e];
+              }
+          }
+          if (!all || pos0 + KS - 1 > sees_all || pos0 < from_all) {
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                const int at = 8 * (j / 4) + 4 * half + j % 4, pos = pos0 + n * 32 + at;
+                const bool seen = ((there[n] >> at) & 1u) && pos <= rpos && pos >= rfirst;
+                if (!seen) sc[n][j] = -INFINITY;
+              }
+          }
+        }
+        if constexpr (RW == 1) {
+          wait_reads();
+          if (i + NS < count) load_keys(i + NS);
+        }
+        bf16x8 p[NB * 2];
+        if (any) {
+          float top = sc[0][0];
+#pragma unroll
+          for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) top = fmaxf(top, sc[n][j]);
+          const f32x2 tops = both_halves(top);
+          top = fmaxf(tops[0], tops[1]) * a.scale2;
+          if (__ballot(top > mref + kRaise)) {
+            const float m = fmaxf(mref, top);
+            const float f = m == -INFINITY ? 1.0f : exp2_fast(mref - m);
+            sum *= f;
+#pragma unroll
+            for (int n = 0; n < D / 32; ++n)
+#pragma unroll
+              for (int j = 0; j < 16; ++j) o[n][j] *= f;
+            mref = m;
+          }
+          const float m = mref == -INFINITY ? 0.0f : mref;
+#pragma unroll
+          for (int n = 0; n < NB; ++n) {
+            float w[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) w[j] = exp2_fast(fmaf(sc[n][j], a.scale2, -m));
+            if (F8) {
+#pragma unroll
+              for (int g = 0; g < 4; ++g) {
+                const f32x4 v = *(MOE_LDS f32x4*)(scales_of(i, KS != 32) +
+                                                  ((KS == 32 ? 32 : 0) + n * 32 + 8 * g + 4 * half) * 4);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  sum += w[4 * g + e];
+                  w[4 * g + e] *= v[e];
+                }
+              }
+            }
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+              u32x4 c;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                c[e] = pack2(w[8 * g + 2 * e], w[8 * g + 2 * e + 1]);
+                if (!F8) sum = dot2_bf16(c[e], 0x3F803F80u, sum);
+              }
+              p[2 * n + g] = __builtin_bit_cast(bf16x8, c);
+            }
+          }
+        }
+        if constexpr (RW == 1) {
+          // behind these values: NS keys and NS - 1 values
+          if (i + NS < count)
+            wait_loads<(2 * NS - 1) * S::kLoads + NS * kScaleLoads>();
+          else
+            wait_loads<0>();
+        }
+        if (any) {
+          const int li = lane & 15, cols16 = (lane >> 4) & 1;
+#pragma unroll
+          for (int n = 0; n < NB * 2; ++n) {
+#pragma unroll
+            for (int d = 0; d < D / 32; ++d) {
+              bf16x8 vf;
+              if (F8) {
+                const int e = li >> 1, row = n * 16 + 8 * (e >> 2) + 4 * half + (e & 3);
+                vf = from_codes(__builtin_amdgcn_ds_read_tr8_b64_v2i32(
+                    (MOE_LDS i32x2*)(vl + row * S::kPitch + ((2 * d + cols16) ^ S::value_swizzle(row)) * 16 +
+                                     (li & 1) * 8)));
+              } else {
+                s16x4 v[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const int row = n * 16 + 8 * e + 4 * half + (li >> 2);
+                  v[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                      (MOE_LDS s16x4*)(vl + row * S::kPitch +
+                                       ((4 * d + 2 * cols16 + ((li & 3) >> 1)) ^ S::value_swizzle(row)) * 16 +
+                                       (li & 1) * 8));
+                }
+                vf = __builtin_bit_cast(bf16x8, __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7));
+              }
+              o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, p[n], o[d], 0, 0, 0);
+            }
+          }
+        }
+        if constexpr (RW == 1) {
+          wait_reads();
+          if (i + NS < count) load_values(i + NS);
+        }
+      }
+    }
+
+    // ---- the tile's end: rows through LDS, 128 columns at a time
+    {
+      const f32x2 sums = both_halves(sum);
+      sum = sums[0] + sums[1];
+    }
+    __syncthreads();       // the steps' LDS has been used up
+    float m = mref;
+    float f = 1.0f;
+    if constexpr (KW > 1) {
+      if (half == 0) stats[wave * 32 + col] = f32x2{mref, sum};
+      __syncthreads();
+      f32x2 st[KW];
+#pragma unroll
+      for (int k = 0; k < KW; ++k) st[k] = stats[(k * RW + rw) * 32 + col], m = fmaxf(m, st[k][0]);
+      sum = 0.0f;
+#pragma unroll
+      for (int k = 0; k < KW; ++k) sum += m == -INFINITY ? 0.0f : st[k][1] * exp2_fast(st[k][0] - m);
+      f = m == -INFINITY ? 0.0f : exp2_fast(mref - m);
+    }
+    float* const part = a.parts + int64_t(slot) * S::kRows * (D + 2);
+    if (whole)
+      f = sum > 0.0f ? f / sum : 0.0f;
+    else if (kw == 0 && half == 0)
+      *reinterpret_cast<f32x2*>(part + S::kRows * D + lr * 2) = f32x2{m, sum};
+    float* const mine_out = reinterpret_cast<float*>(smem) + wave * 32 * S::kOutPitch;
+    constexpr int kLanes = S::kCols / 4, kRowsAt = 64 / kLanes;     // lanes of a row, rows at a time
+#pragma unroll
+    for (int c0 = 0; c0 < D; c0 += S::kCols) {
+#pragma unroll
+      for (int d = 0; d < S::kCols / 32; ++d)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          f32x4 v;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = o[c0 / 32 + d][4 * g + e] * f;
+          *reinterpret_cast<f32x4*>(mine_out + col * S::kOutPitch + d * 32 + 8 * g + 4 * half) = v;
+        }
+      __syncthreads();
+      // the KW waves of these rows take 32 / KW of them each
+#pragma unroll 1
+      for (int i = 0; i < 32 / KW; i += kRowsAt) {
+        const int row = kw * (32 / KW) + i + lane / kLanes, c = (lane % kLanes) * 4;
+        f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int k = 0; k < KW; ++k)
+          v += *reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(smem) +
+                                               ((k * RW + rw) * 32 + row) * S::kOutPitch + c);
+        const int tr = rw * 32 + row, tk = tr / a.G;
+        if (whole) {
+          if (tk < nt) store_row4(a, s.row0 + t0 + tk, h * a.G + tr - tk * a.G, D, c0 + c, v);
+        } else {
+          *reinterpret_cast<f32x4*>(part + tr * D + c0 + c) = v;
+        }
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// The parts of a cut tile, in order: out = sum_i exp2(m_i - m) o_i / sum_i
+// exp2(m_i - m) l_i.  A workgroup takes every gridDim.y-th row of the tile
+// that begins before blockIdx.x's run; its waves' lanes hold four columns of
+// a part each.
+template <int D>
+__global__ __launch_bounds__(256) void join_kernel(const AttnArgs a, int rows) {
+  constexpr int LANES = D / 4, PARTS = 256 / LANES;
+  __shared__ f32x4 acc[256];
+  __shared__ f32x2 stat[PARTS];
+  const Joint j = static_cast<const Joint*>(a.joints)[blockIdx.x];
+  if (j.parts == 0) return;
+  const int sub = threadIdx.x % LANES, p0 = threadIdx.x / LANES;
+  const int used = min(j.tokens * a.G, rows);
+  for (int row = blockIdx.y; row < used; row += gridDim.y) {
+    float m = -INFINITY, l = 0.0f;
+    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int p = p0; p < j.parts; p += PARTS) {
+      const int slot = (j.first + p) * 2 + (p == 0 ? 1 : 0);
+      const float* part = a.parts + int64_t(slot) * rows * (D + 2);
+      const f32x2 st = *reinterpret_cast<const f32x2*>(part + rows * D + row * 2);
+      const f32x4 w = *reinterpret_cast<const f32x4*>(part + row * D + sub * 4);
+      const float top = fmaxf(m, st[0]);
+      if (top == -INFINITY) continue;
+      const float f = exp2_fast(m - top), g = exp2_fast(st[0] - top);
+      l = l * f + st[1] * g;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = v[e] * f + w[e] * g;
+      m = top;
+    }
+    __syncthreads();
+    acc[threadIdx.x] = v;
+    if (sub == 0) stat[p0] = f32x2{m, l};
+    __syncthreads();
+    if (p0 == 0) {
+      float top = stat[0][0];
+#pragma unroll
+      for (int p = 1; p < PARTS; ++p) top = fmaxf(top, stat[p][0]);
+      float total = 0.0f;
+      v = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      if (top > -INFINITY) {
+#pragma unroll
+        for (int p = 0; p < PARTS; ++p) {
+          const float f = exp2_fast(stat[p][0] - top);
+          total += stat[p][1] * f;
+          const f32x4 w = acc[p * LANES + sub];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] += w[e] * f;
+        }
+      }
+      const float f = total > 0.0f ? 1.0f / total : 0.0f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] *= f;
+      const int tk = row / a.G;
+      store_row4(a, j.row0 + tk, j.head * a.G + row - tk * a.G, D, sub * 4, v);
+    }
+  }
+}
+
+// Dynamic LDS above 64 KiB has to be asked for.
+template <class Kernel>
+hipError_t allow_lds(Kernel kernel, int64_t bytes) {
+  if (bytes <= 64 * 1024) return hipSuccess;
+  return hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                             hipFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+}
+
+// Rows of a tile for so many rows per sequence.
+int rows_for(int64_t rows) { return rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256; }
+
+constexpr int kMaxGrid = 2 * kCus;
+constexpr size_t kJointBytes = kMaxGrid * sizeof(Joint);
+
+size_t parts_bytes(int rows, int D) {
+  return size_t(rows <= 128 ? kMaxGrid : kCus) * 2 * rows * (D + 2) * 4;
+}
+
+template <class S>
+hipError_t launch_shape(AttnArgs a, hipStream_t st) {
+  static_assert((S::kRows <= 128 ? kMaxGrid : kCus) >= kCus * S::kPerCu, "workspace");
+  a.QT = S::kRows / a.G;
+  a.joints = a.ws;
+  a.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + kJointBytes);
+  a.min_steps = 1;
+  // no more workgroups than steps there can be (a multiple of the 8 XCDs)
+  const int64_t tiles = int64_t(a.T) / a.QT + a.kv.B;
+  const int64_t steps = ((int64_t(a.kv.max_pages) << a.kv.page_shift) + S::kStep - 1) / S::kStep;
+  const int64_t most = tiles * a.kv.Hkv * (steps + 2);
+  const int64_t full = kCus * S::kPerCu;
+  a.grid = int((most < full ? most + 7 : full) / 8 * 8);
+  const auto kernel = attention_kernel<S>;
+  const hipError_t e = allow_lds(kernel, S::kLds);
+  if (e != hipSuccess) return e;
+  kernel<<<a.grid, S::kThreads, S::kLds, st>>>(a);
+  join_kernel<S::D><<<dim3(a.grid, S::kRows), 256, 0, st>>>(a, S::kRows);
+  return hipGetLastError();
+}
+
+template <int D, bool F8>
+hipError_t launch(const AttnArgs& a, hipStream_t st) {
+  // (an 8-bit cache needs half the LDS)
+  constexpr int NS = D == 256 && !F8 ? 1 : 2;
+  const int64_t tokens = (int64_t(a.T) + a.kv.B - 1) / a.kv.B;
+  switch (rows_for(tokens * a.G)) {
+    case 32:
+      return launch_shape<Shape<D, F8, 1, 4, 32, NS>>(a, st);
+    case 64:
+      return launch_shape<Shape<D, F8, 2, 2, 32, 2>>(a, st);
+    case 128:
+      return launch_shape<Shape<D, F8, 4, 1, 64, 2>>(a, st);
+    default:
+      return launch_shape<Shape<D, F8, 8, 1, 64, 2>>(a, st);
+  }
+}
+
+}  // namespace
+
+size_t attention_ws(int T, int Hq, int Hkv, int D) {
+  // (whatever B is: the tiles are no larger than one sequence's rows need)
+  const int rows = rows_for(int64_t(T > 0 ? T : 1) * (Hq / Hkv));
+  size_t most = 0;
+  for (int r = 32; r <= rows; r *= 2)
+    if (parts_bytes(r, D) > most) most = parts_bytes(r, D);
+  return kJointBytes + most;
+}
+
+hipError_t launch_paged_attention(const AttnArgs& a, hipStream_t st) {
+  if (a.kv.D == 64) return a.kv.f8 ? launch<64, true>(a, st) : launch<64, false>(a, st);
+  if (a.kv.D == 128) return a.kv.f8 ? launch<128, true>(a, st) : launch<128, false>(a, st);
+  return a.kv.f8 ? launch<256, true>(a, st) : launch<256, false>(a, st);
+}
+
+}  // namespace moe

@@ -155,6 +155,26 @@ struct RopeArgs {
 };
 hipError_t launch_rope_append(const RopeArgs& a, hipStream_t st);
 
+// attention over the paged cache
+struct AttnArgs {
+  KvArgs kv;
+  const uint16_t* q;           // bf16, T rows of Hq * D
+  int64_t q_stride;
+  int T, Hq, G;                // G = Hq / Hkv
+  float scale2;                // scale * log2(e)
+  int window;                  // 0: none
+  uint16_t* out;               // bf16 (may be null)
+  int64_t out_stride;
+  uint8_t* x8;                 // e4m3 [T][Hq * D] (may be null)
+  float* x8_scale;             // [T][Hq * D / 128]
+  void* ws;
+  int QT, grid, min_steps;     // set by the launcher, as what follows
+  void* joints;
+  float* parts;
+};
+size_t attention_ws(int T, int Hq, int Hkv, int D);
+hipError_t launch_paged_attention(const AttnArgs& a, hipStream_t st);
+
 // sampling: one token per row of logits
 struct SampleArgs {
   const void* logits;

@@ -57,14 +57,63 @@ BATCH_REFUSALS = [
 ]
 
 
+def _attend(cache=None, batch=None, **kw):
+    a = dict(q=FAKE, qs=4 * 128, T=5, Hq=4, scale=0.1, window=0, out=FAKE, os=4 * 128, x8=FAKE, sc=FAKE, ws=FAKE,
+             size=1 << 30)
+    a.update(kw)
+    cache = _cache() if cache is None else cache
+    batch = _batch() if batch is None else batch
+    return moe.lib.moe_paged_attention(ctypes.byref(cache), ctypes.byref(batch), *a.values(), None)
+
+
 @pytest.mark.parametrize("kw,status", CACHE_REFUSALS)
 def test_cache_refusals(kw, status):
     assert _append(cache=_cache(**kw)) == status
+    assert _attend(cache=_cache(**kw)) == status
 
 
 @pytest.mark.parametrize("kw,status", BATCH_REFUSALS)
 def test_batch_refusals(kw, status):
     assert _append(batch=_batch(**kw)) == status
+    assert _attend(batch=_batch(**kw)) == status
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(T=0), OK), (dict(T=-1), INVALID), (dict(T=(1 << 22) + 1), UNSUPPORTED), (dict(Hq=0), INVALID),
+    (dict(Hq=5), INVALID), (dict(Hq=1026), UNSUPPORTED), (dict(Hq=516), UNSUPPORTED), (dict(q=None), INVALID),
+    (dict(q=FAKE + 1), INVALID), (dict(qs=511), INVALID), (dict(out=None, x8=None, sc=None), INVALID),
+    (dict(x8=None), INVALID), (dict(sc=None), INVALID), (dict(out=FAKE + 1), INVALID), (dict(os=511), INVALID),
+    (dict(sc=FAKE + 2), INVALID), (dict(scale=0.0), INVALID), (dict(scale=-1.0), INVALID),
+    (dict(scale=float("nan")), INVALID), (dict(scale=float("inf")), INVALID), (dict(window=-1), INVALID),
+    (dict(ws=None), INVALID), (dict(ws=FAKE + 64), INVALID), (dict(size=1000), WORKSPACE),
+])
+def test_attend_refusals(kw, status):
+    assert _attend(**kw) == status
+
+
+def test_attend_in_8_bits_wants_whole_blocks():
+    cache = _cache(D=64, page_stride=16 * 2 * 64, slot_stride=128, head_stride=64)
+    assert _attend(cache=cache) == UNSUPPORTED
+    assert _attend(cache=cache, T=0, x8=None, sc=None) == OK
+
+
+def test_attend_workspace_size():
+    n = ctypes.c_size_t(0)
+    size = moe.lib.moe_paged_attention_workspace_size
+    assert size(1, 1, 16, 2, 256, None) == INVALID
+    assert size(-1, 1, 16, 2, 256, ctypes.byref(n)) == INVALID
+    assert size(1, 0, 16, 2, 256, ctypes.byref(n)) == INVALID
+    assert size(1, 1, 15, 2, 256, ctypes.byref(n)) == INVALID
+    for bad in ((1, 4097, 16, 2, 256), (1, 1, 16, 2, 96), (1, 1, 514, 2, 64), (1 << 23, 1, 16, 2, 64)):
+        assert size(*bad, ctypes.byref(n)) == UNSUPPORTED
+    for Hq, Hkv, D in ((16, 2, 256), (7, 7, 64), (256, 1, 128)):
+        last = 0
+        for T in (0, 1, 2, 5, 17, 100, 5000, 1 << 22):
+            a = moe.moe_paged_attention_workspace_size(T, 1, Hq, Hkv, D)
+            assert a >= last and a % 256 == 0 and a == moe.moe_paged_attention_workspace_size(T, 64, Hq, Hkv, D)
+            last = a
+    a = moe.moe_paged_attention_workspace_size(5, 3, 4, 2, 128)
+    assert _attend(size=a - 1) == WORKSPACE
 
 
 @pytest.mark.parametrize("kw,status", [
@@ -109,6 +158,40 @@ def test_binding_refusals():
         lambda: moe.KVBatch(n32, n32[:3], torch.zeros((3, 5))),
         lambda: moe.KVBatch(n32, n32[:3], torch.zeros((5, 3), dtype=torch.int32).t()),
         lambda: moe.KVBatch(n32, n32[:3], torch.zeros((3, 5), dtype=torch.int32)),   # not on a GPU
+    ):
+        with pytest.raises(ValueError):
+            bad()
+
+
+class _Anywhere:
+    """Stands for a KVCache and a KVBatch, on no GPU."""
+    D, Hkv, device, ref = 64, 2, 0, None
+
+
+def test_call_binding_refusals():
+    c = b = _Anywhere()
+    x, q = torch.zeros((5, 8 * 64), dtype=torch.bfloat16), torch.zeros((5, 4 * 64), dtype=torch.bfloat16)
+    w, freq, ws = torch.ones(64), torch.ones(16, dtype=torch.float64), torch.zeros(64, dtype=torch.uint8)
+    append, attend = moe.moe_rope_append, moe.moe_paged_attention
+    for bad in (
+        lambda: append(c, b, x, 5, 4, q),                                    # not on a GPU
+        lambda: append(c, b, x.double(), 5, 4, q),
+        lambda: append(c, b, x, 6, 4, q),
+        lambda: append(c, b, x, 5, 5, q),
+        lambda: append(c, b, x, 5, 4, q.float()),
+        lambda: append(c, b, x, 5, 4, q[:, :255]),
+        lambda: append(c, b, x, 5, 4, q, freq=freq.float()),
+        lambda: append(c, b, x, 5, 4, q, q_weight=w[:63]),
+        lambda: append(c, b, x, 5, 4, q, q_weight=w, k_weight=w.bfloat16()),
+        lambda: attend(c, b, q, 5, 4, 0.1, ws, out=q),                       # not on a GPU
+        lambda: attend(c, b, q.float(), 5, 4, 0.1, ws, out=q),
+        lambda: attend(c, b, q, 6, 4, 0.1, ws, out=q),
+        lambda: attend(c, b, q, 5, 4, 0.1, ws, out=q.float()),
+        lambda: attend(c, b, q, 5, 4, 0.1, ws, out=q[:4]),
+        lambda: attend(c, b, q, 5, 4, 0.1, ws.float(), out=q),
+        lambda: attend(c, b, q, 5, 4, 0.1, ws, x8=q, x8_scale=torch.zeros((5, 2))),
+        lambda: attend(c, b, q, 5, 4, 0.1, ws, x8=torch.zeros((5, 256), dtype=torch.uint8),
+                       x8_scale=torch.zeros((5, 1))),
     ):
         with pytest.raises(ValueError):
             bad()
@@ -190,12 +273,14 @@ def test_attend_by_hand():
     q, k = np.zeros((2, 2, 4)), np.ones((3, 1, 4))
     v = np.arange(3.0)[:, None, None] * np.ones((3, 1, 4))
     seen = np.array([True, True, True])
-    out, spread = ref.attend(q, k, v, [1, 2], seen, 1.0)
+    out, spread, level, _ = ref.attend(q, k, v, [1, 2], seen, 1.0)
     np.testing.assert_allclose(out[:, 0, 0], [0.5, 1.0])
     np.testing.assert_allclose(spread[:, 1, 0], [0.5, 2 / 3])
+    np.testing.assert_allclose(level[:, 1, 0], [0.5, 1.0])
     assert ref.attend(q, k, v, [1, 2], seen, 1.0, window=1)[0][:, 0, 0].tolist() == [1.0, 2.0]
     assert (ref.attend(q, k, v, [1, 2], ~seen, 1.0)[0] == 0).all()
     assert ref.attend(q, k, v, [-1, 0], seen, 1.0)[0][:, 0, 0].tolist() == [0.0, 0.0]
     q[0, 0] = [np.log(2), 0, 0, 0]
     k[1] = 0
-    assert ref.attend(q, k, v, [1, 2], seen, 1.0)[0][0, 0, 0] == pytest.approx(1 / 3)
+    out, _, _, mag = ref.attend(q, k, v, [1, 2], seen, 1.0)
+    assert out[0, 0, 0] == pytest.approx(1 / 3) and mag[0, 0, 0] == pytest.approx(np.log(2))
