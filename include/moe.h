@@ -439,7 +439,8 @@ moe_status moe_scaled_linear(const uint8_t* x8, const float* x_scale, int32_t T,
  * elements share a place.  fmt MOE_W_BF16: bf16 bits, strides multiples of 8;
  * MOE_W_E4M3: codes, strides multiples of 16, with one scale per (page, slot,
  * head) in k_scale and v_scale [num_pages][page_size][Hkv], contiguous (value
- * = code * scale).  k and v 16-byte aligned.  D: 64, 128 or 256, Hkv <= 256. */
+ * = code * scale).  k and v 16-byte aligned.  D: 64, 128 or 256, Hkv <= 256,
+ * strides <= 2^30. */
 typedef struct {
   int32_t num_pages, page_size, Hkv, D;
   int32_t fmt;

@@ -31,6 +31,7 @@ constexpr int kMaxKvHeads = 256;
 constexpr int kMaxQHeads = 1024;
 constexpr int kMaxHeadGroup = 256;     // query heads per key head
 constexpr int kMaxBatch = 4096;
+constexpr int64_t kMaxKvStride = int64_t(1) << 30;    // elements
 constexpr int64_t kMaxPositions = int64_t(1) << 30;
 constexpr size_t kAlign = 256;
 constexpr int kRouterGemmMinT = 256;       // tokens from which the router runs on MFMA
@@ -317,8 +318,10 @@ moe_status check_kv(const moe_kv_cache* c, const moe_kv_batch* b, KvArgs* a) {
   if (f8 && (!c->k_scale || !c->v_scale || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4)))
     return MOE_ERR_INVALID;
   const int64_t unit = f8 ? 16 : 8;
-  for (int64_t s : {c->page_stride, c->slot_stride, c->head_stride})
+  for (int64_t s : {c->page_stride, c->slot_stride, c->head_stride}) {
     if (s < c->D || s % unit) return MOE_ERR_INVALID;
+    if (s > kMaxKvStride) return MOE_ERR_UNSUPPORTED;
+  }
   if (b->B < 1 || b->max_pages < 1 || b->table_stride < b->max_pages) return MOE_ERR_INVALID;
   if (b->B > kMaxBatch || int64_t(b->max_pages) * c->page_size > kMaxPositions)
     return MOE_ERR_UNSUPPORTED;

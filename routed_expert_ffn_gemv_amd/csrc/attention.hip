@@ -232,9 +232,11 @@ __device__ __forceinline__ void store_row4(const AttnArgs& a, int64_t row, int h
 
 // ---- the kernel
 
-template <int D_, bool F8_, int RW_, int KW_, int KS_, int NS_>
+// PARTS: bf16 numbers that a weight is the sum of.
+template <int D_, bool F8_, int RW_, int KW_, int KS_, int NS_, int PARTS_>
 struct Shape {
   static constexpr int D = D_, RW = RW_, KW = KW_, KS = KS_, NS = NS_;
+  static constexpr int kParts = PARTS_;
   static constexpr bool F8 = F8_;
   static constexpr int kWaves = RW * KW, kThreads = kWaves * kWave;
   static constexpr int kRows = 32 * RW;
@@ -250,8 +252,8 @@ struct Shape {
   static constexpr int kOut = kWaves * 32 * kOutPitch * 4;
   static constexpr int kData = kRing + kScales > kOut ? kRing + kScales : kOut;
   static constexpr int kLds = kData + kIds * 4 + kWaves * 32 * 8;
-  static constexpr int kPerCu = kMaxLds / (kLds + 512) >= 2 && kThreads <= 256 ? 2 : 1;
-  static_assert(kLds + 512 <= kMaxLds && (RW == 1 || NS == 2) && (KS == 32 || KS == 64), "shape");
+  static constexpr int kPerCu = kMaxLds / (kLds + 256) >= 2 && kThreads <= 256 ? 2 : 1;
+  static_assert(kLds + 256 <= kMaxLds && (RW == 1 || NS == 2) && (KS == 32 || KS == 64), "shape");
   static_assert(RW == 1 || 2 * kLoads % RW == 0, "loads");
 
   // Permutations of a row's 16-byte chunks in LDS, so that what is read
@@ -271,7 +273,9 @@ struct Shape {
 template <class S>
 __global__ __launch_bounds__(S::kThreads, S::kPerCu * S::kThreads / 256) void attention_kernel(const AttnArgs a) {
   constexpr int D = S::D, RW = S::RW, KW = S::KW, KS = S::KS, NS = S::NS, STEP = S::kStep, NB = KS / 32;
+  constexpr int PARTS = S::kParts;
   constexpr bool F8 = S::F8;
+  constexpr int PITCH = S::kPitch, BANKS = PITCH < 256 ? PITCH : 256;   // (a row's part that chunks are permuted in)
   extern __shared__ __align__(256) uint8_t smem[];
   __shared__ int64_t scan_tmp[S::kWaves];
   __shared__ int64_t found[2];
@@ -400,12 +404,13 @@ __global__ __launch_bounds__(S::kThreads, S::kPerCu * S::kThreads / 256) void at
     for (int i = 0; i < D / 32; ++i)
 #pragma unroll
       for (int j = 0; j < 16; ++j) o[i][j] = 0.0f;
-    float mref = -INFINITY, sum = 0.0f;
+    float mref = -INFINITY, sum = 0.0f, lost = 0.0f;     // (what the sum's roundings lost)
 
     // ---- the positions, as far as the page numbers held in LDS reach
-    const int64_t elem = F8 ? 1 : 2;
-    const uint8_t* const kbase = a.kv.k + int64_t(h) * a.kv.head_stride * elem;
-    const uint8_t* const vbase = a.kv.v + int64_t(h) * a.kv.head_stride * elem;
+    constexpr int ELEM = F8 ? 1 : 2;
+    const uint8_t* const kbase = a.kv.k + int64_t(h) * a.kv.head_stride * ELEM;
+    const uint8_t* const vbase = a.kv.v + int64_t(h) * a.kv.head_stride * ELEM;
+    const uint32_t page_bytes = uint32_t(a.kv.page_stride) * ELEM, slot_bytes = uint32_t(a.kv.slot_stride) * ELEM;
     const int shift = a.kv.page_shift;
     const int span = max(1, int(min(int64_t(kIds - 1) << shift, int64_t(1) << 30)) / STEP);
     for (int s0 = 0; s0 < take; s0 += span) {
@@ -435,8 +440,8 @@ __global__ __launch_bounds__(S::kThreads, S::kPerCu * S::kThreads / 256) void at
         const int pos = (step0 + i) * STEP + kw * KS + row;
         const int id = page_of(pos);
         const int c = pc ^ (value ? S::value_swizzle(row) : S::key_swizzle(row));
-        const uint8_t* p = (value ? vbase : kbase) +
-                           (id * a.kv.page_stride + (pos & ((1 << shift) - 1)) * a.kv.slot_stride) * elem + c * 16;
+        const uint8_t* p = (value ? vbase : kbase) + uint64_t(uint32_t(id)) * page_bytes +
+                           uint64_t(uint32_t(pos & ((1 << shift) - 1))) * slot_bytes + c * 16;
         if (id < 0) p = reinterpret_cast<const uint8_t*>(&kZeros);
         to_lds16(p, lds_address(slot_lds(i % NS, value) + j * 1024));
       };
@@ -508,18 +513,25 @@ __global__ __launch_bounds__(S::kThreads, S::kPerCu * S::kThreads / 256) void at
         const bool any = pos0 <= sees_any && pos0 + KS > from_any;
         f32x16 sc[NB];
         if (any) {
+          // chunk c of a row lies at c ^ key_swizzle(row): with the lane's part
+          // of c in the address, the rest of it is an exclusive or (below 256
+          // bytes) and an offset; 32 rows further the permutation is the same
+          uint32_t at = uint32_t(reinterpret_cast<uintptr_t>(kl)) + col * PITCH +
+                        (F8 ? S::key_swizzle(col) * 16 + half * 8 : (S::key_swizzle(col) ^ half) * 16);
+          asm volatile("" : "+v"(at));     // (not to be kept for every step)
 #pragma unroll
           for (int n = 0; n < NB; ++n) {
 #pragma unroll
             for (int j = 0; j < 16; ++j) sc[n][j] = 0.0f;
-            const int row = n * 32 + col;
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
+              constexpr int UNIT = F8 ? 16 : 32;
+              const uint32_t from = (at ^ (k * UNIT % BANKS)) + k * UNIT / BANKS * BANKS + n * 32 * PITCH;
               bf16x8 kf;
               if (F8)
-                kf = from_codes(*(MOE_LDS i32x2*)(kl + row * S::kPitch + (k ^ S::key_swizzle(row)) * 16 + half * 8));
+                kf = from_codes(*(MOE_LDS i32x2*)(uintptr_t)from);
               else
-                kf = *(MOE_LDS bf16x8*)(kl + row * S::kPitch + ((2 * k + half) ^ S::key_swizzle(row)) * 16);
+                kf = *(MOE_LDS bf16x8*)(uintptr_t)from;
               sc[n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, q[k], sc[n], 0, 0, 0);
             }
           }
@@ -548,7 +560,7 @@ __global__ __launch_bounds__(S::kThreads, S::kPerCu * S::kThreads / 256) void at
           wait_reads();
           if (i + NS < count) load_keys(i + NS);
         }
-        bf16x8 p[NB * 2];
+        bf16x8 p[PARTS][NB * 2];
         if (any) {
           float top = sc[0][0];
 #pragma unroll
@@ -560,7 +572,7 @@ __global__ __launch_bounds__(S::kThreads, S::kPerCu * S::kThreads / 256) void at
           if (__ballot(top > mref + kRaise)) {
             const float m = fmaxf(mref, top);
             const float f = m == -INFINITY ? 1.0f : exp2_fast(mref - m);
-            sum *= f;
+            sum *= f, lost *= f;
 #pragma unroll
             for (int n = 0; n < D / 32; ++n)
 #pragma unroll
@@ -568,34 +580,48 @@ __global__ __launch_bounds__(S::kThreads, S::kPerCu * S::kThreads / 256) void at
             mref = m;
           }
           const float m = mref == -INFINITY ? 0.0f : mref;
+          float add = 0.0f;
 #pragma unroll
           for (int n = 0; n < NB; ++n) {
             float w[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) w[j] = exp2_fast(fmaf(sc[n][j], a.scale2, -m));
+            if (F8 || PARTS > 1) {
+              // (four sums side by side)
+              f32x4 s = {w[0], w[1], w[2], w[3]};
+#pragma unroll
+              for (int j = 4; j < 16; ++j) s[j % 4] += w[j];
+              add += (s[0] + s[1]) + (s[2] + s[3]);
+            }
             if (F8) {
 #pragma unroll
               for (int g = 0; g < 4; ++g) {
                 const f32x4 v = *(MOE_LDS f32x4*)(scales_of(i, KS != 32) +
                                                   ((KS == 32 ? 32 : 0) + n * 32 + 8 * g + 4 * half) * 4);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  sum += w[4 * g + e];
-                  w[4 * g + e] *= v[e];
-                }
+                for (int e = 0; e < 4; ++e) w[4 * g + e] *= v[e];
               }
             }
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-              u32x4 c;
+            for (int k = 0; k < PARTS; ++k) {
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                c[e] = pack2(w[8 * g + 2 * e], w[8 * g + 2 * e + 1]);
-                if (!F8) sum = dot2_bf16(c[e], 0x3F803F80u, sum);
+              for (int g = 0; g < 2; ++g) {
+                u32x4 c;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  float* const x = w + 8 * g + 2 * e;
+                  c[e] = pack2(x[0], x[1]);
+                  if (!F8 && PARTS == 1) add = dot2_bf16(c[e], 0x3F803F80u, add);
+                  x[0] -= __uint_as_float(c[e] << 16), x[1] -= __uint_as_float(c[e] & 0xFFFF0000u);
+                }
+                p[k][2 * n + g] = __builtin_bit_cast(bf16x8, c);
               }
-              p[2 * n + g] = __builtin_bit_cast(bf16x8, c);
             }
           }
+          // a sum over a long text keeps what is small next to it
+          const float y = add - lost, s = sum + y;
+          lost = (s - sum) - y;
+          sum = s;
         }
         if constexpr (RW == 1) {
           // behind these values: NS keys and NS - 1 values
@@ -605,30 +631,31 @@ __global__ __launch_bounds__(S::kThreads, S::kPerCu * S::kThreads / 256) void at
             wait_loads<0>();
         }
         if (any) {
+          // lanes of 16 give the rows that the transposing read takes: 4 rows of
+          // 16 columns (16 bits), 8 of 16 (8 bits); the permutation as for keys
           const int li = lane & 15, cols16 = (lane >> 4) & 1;
+          const int row = F8 ? 8 * (li >> 3) + 4 * half + ((li >> 1) & 3) : 4 * half + (li >> 2);
+          const int chunk = F8 ? cols16 : 2 * cols16 + ((li & 3) >> 1);
+          uint32_t at = uint32_t(reinterpret_cast<uintptr_t>(vl)) + row * PITCH +
+                        (chunk ^ S::value_swizzle(row)) * 16 + (li & 1) * 8;
+          asm volatile("" : "+v"(at));
 #pragma unroll
           for (int n = 0; n < NB * 2; ++n) {
 #pragma unroll
             for (int d = 0; d < D / 32; ++d) {
+              constexpr int UNIT = F8 ? 32 : 64;
+              const uint32_t from = (at ^ (d * UNIT % BANKS)) + d * UNIT / BANKS * BANKS + n * 16 * PITCH;
               bf16x8 vf;
               if (F8) {
-                const int e = li >> 1, row = n * 16 + 8 * (e >> 2) + 4 * half + (e & 3);
-                vf = from_codes(__builtin_amdgcn_ds_read_tr8_b64_v2i32(
-                    (MOE_LDS i32x2*)(vl + row * S::kPitch + ((2 * d + cols16) ^ S::value_swizzle(row)) * 16 +
-                                     (li & 1) * 8)));
+                vf = from_codes(__builtin_amdgcn_ds_read_tr8_b64_v2i32((MOE_LDS i32x2*)(uintptr_t)from));
               } else {
-                s16x4 v[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  const int row = n * 16 + 8 * e + 4 * half + (li >> 2);
-                  v[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                      (MOE_LDS s16x4*)(vl + row * S::kPitch +
-                                       ((4 * d + 2 * cols16 + ((li & 3) >> 1)) ^ S::value_swizzle(row)) * 16 +
-                                       (li & 1) * 8));
-                }
-                vf = __builtin_bit_cast(bf16x8, __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7));
+                const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MOE_LDS s16x4*)(uintptr_t)from);
+                const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MOE_LDS s16x4*)(uintptr_t)(from + 8 * PITCH));
+                vf = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
               }
-              o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, p[n], o[d], 0, 0, 0);
+#pragma unroll
+              for (int k = PARTS - 1; k >= 0; --k)
+                o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, p[k][n], o[d], 0, 0, 0);
             }
           }
         }
@@ -795,20 +822,20 @@ hipError_t launch_shape(AttnArgs a, hipStream_t st) {
   return hipGetLastError();
 }
 
-template <int D, bool F8>
+template <int D, bool F8, int PARTS>
 hipError_t launch(const AttnArgs& a, hipStream_t st) {
   // (an 8-bit cache needs half the LDS)
-  constexpr int NS = D == 256 && !F8 ? 1 : 2;
+  constexpr int NS = D == 256 && !F8 ? 1 : 2, KS = D == 256 ? 32 : 64;
   const int64_t tokens = (int64_t(a.T) + a.kv.B - 1) / a.kv.B;
   switch (rows_for(tokens * a.G)) {
     case 32:
-      return launch_shape<Shape<D, F8, 1, 4, 32, NS>>(a, st);
+      return launch_shape<Shape<D, F8, 1, 4, 32, NS, 3>>(a, st);
     case 64:
-      return launch_shape<Shape<D, F8, 2, 2, 32, 2>>(a, st);
+      return launch_shape<Shape<D, F8, 2, 2, 32, 2, PARTS>>(a, st);
     case 128:
-      return launch_shape<Shape<D, F8, 4, 1, 64, 2>>(a, st);
+      return launch_shape<Shape<D, F8, 4, 1, KS, 2, PARTS>>(a, st);
     default:
-      return launch_shape<Shape<D, F8, 8, 1, 64, 2>>(a, st);
+      return launch_shape<Shape<D, F8, 8, 1, KS, 2, PARTS>>(a, st);
   }
 }
 
@@ -824,9 +851,13 @@ size_t attention_ws(int T, int Hq, int Hkv, int D) {
 }
 
 hipError_t launch_paged_attention(const AttnArgs& a, hipStream_t st) {
-  if (a.kv.D == 64) return a.kv.f8 ? launch<64, true>(a, st) : launch<64, false>(a, st);
-  if (a.kv.D == 128) return a.kv.f8 ? launch<128, true>(a, st) : launch<128, false>(a, st);
-  return a.kv.f8 ? launch<256, true>(a, st) : launch<256, false>(a, st);
+  const bool f8 = a.kv.f8, fine = a.x8 != nullptr;
+  if (a.kv.D == 64) return f8 ? launch<64, true, 1>(a, st) : launch<64, false, 1>(a, st);
+  if (a.kv.D == 128)
+    return f8 ? fine ? launch<128, true, 2>(a, st) : launch<128, true, 1>(a, st)
+              : fine ? launch<128, false, 2>(a, st) : launch<128, false, 1>(a, st);
+  return f8 ? fine ? launch<256, true, 2>(a, st) : launch<256, true, 1>(a, st)
+            : fine ? launch<256, false, 2>(a, st) : launch<256, false, 1>(a, st);
 }
 
 }  // namespace moe

@@ -47,7 +47,7 @@ CACHE_REFUSALS = [
     (dict(fmt=E4M3, k_scale=None), INVALID), (dict(fmt=E4M3, v_scale=None), INVALID),
     (dict(fmt=E4M3, k_scale=FAKE + 2), INVALID), (dict(fmt=E4M3, v_scale=FAKE + 1), INVALID),
     (dict(page_stride=127), INVALID), (dict(slot_stride=132), INVALID), (dict(head_stride=0), INVALID),
-    (dict(head_stride=-128), INVALID), (dict(fmt=E4M3, head_stride=136), INVALID),
+    (dict(head_stride=-128), INVALID), (dict(page_stride=(1 << 30) + 128), UNSUPPORTED), (dict(fmt=E4M3, head_stride=136), INVALID),
 ]
 BATCH_REFUSALS = [
     (dict(B=0), INVALID), (dict(B=4097), UNSUPPORTED), (dict(max_pages=0), INVALID), (dict(table_stride=7), INVALID),
