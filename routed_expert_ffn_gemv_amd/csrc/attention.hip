@@ -41,6 +41,8 @@
 
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "kernels.h"
 
 namespace moe {
@@ -66,6 +68,7 @@ constexpr int kIds = 1024;                          // page numbers a workgroup 
 constexpr float kE4m3Max = 448.0f;
 constexpr float kScaleFloor = 448.0f * 0x1p-126f;   // keeps every scale a normal number
 constexpr float kRaise = 8.0f;                      // log2 of the largest weight
+constexpr int kMaxGrid = 2 * kCus;
 
 __device__ const u32x4 kZeros = {0u, 0u, 0u, 0u};   // what a position that is not there reads
 
@@ -83,6 +86,10 @@ __device__ const u32x4 kZeros = {0u, 0u, 0u, 0u};   // what a position that is n
 
 __device__ __forceinline__ void to_lds16(const uint8_t* p, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(p) : "m0");
+}
+// From a scalar base and 32-bit offsets.
+__device__ __forceinline__ void to_lds16(const uint8_t* base, uint32_t at, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(at), "s"(base) : "m0");
 }
 __device__ __forceinline__ void to_lds4(const void* p, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dword %1, off" ::"s"(lds), "v"(p) : "m0");
@@ -107,6 +114,18 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2_t));
 }
 
+// Nothing is moved across by the compiler, which would read a product's
+// operand right before it to save registers.
+__device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0); }
+
+// The lane, computed anew: what a step derives from it is then not kept in
+// registers from step to step (heads of 256 leave none).
+__device__ __forceinline__ int lane_now() {
+  int l;
+  asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(l));
+  return l;
+}
+
 // Eight e4m3 codes as bf16 (exact).
 __device__ __forceinline__ bf16x8 from_codes(i32x2 c) {
   u32x4 r;
@@ -118,6 +137,9 @@ __device__ __forceinline__ bf16x8 from_codes(i32x2 c) {
   return __builtin_bit_cast(bf16x8, r);
 }
 
+__device__ __forceinline__ bf16x8 operand(i32x2 c) { return from_codes(c); }
+__device__ __forceinline__ bf16x8 operand(bf16x8 v) { return v; }
+
 // The value of lane ^ 32 and the lane's own, in one order for both.
 __device__ __forceinline__ f32x2 both_halves(float v) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
@@ -128,11 +150,22 @@ __device__ __forceinline__ float exp2_fast(float v) { return __builtin_amdgcn_ex
 
 // ---- the line of work
 
+// Quotient of two whole numbers, 0 <= a < 2^53, 0 < b < 2^53.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  if (__builtin_expect(((a | b) >> 32) == 0, 1)) return uint32_t(a) / uint32_t(b);
+  int64_t q = int64_t(double(a) / double(b));
+  const int64_t r = a - q * b;
+  if (r < 0) --q;
+  if (r >= b) ++q;
+  return q;
+}
+
 struct Seq {
   int row0, n;          // its rows
   int off;              // position of its first new token
   int len;              // positions that may be there
   int nq;               // query tiles
+  int most;             // steps of the longest
   int64_t pair, mid;    // steps set aside for a pair of tiles and for an unpaired one in the middle
   int64_t head;         // for a key head
 };
@@ -154,58 +187,128 @@ __device__ __forceinline__ Seq seq_of(const AttnArgs& a, int b) {
   const int len = min(max(a.kv.kv_len[b], 0), 1 << 30);
   s.off = len - s.n;
   s.len = min(len, a.kv.max_pages << a.kv.page_shift);
-  s.nq = (s.n + a.QT - 1) / a.QT;
+  s.nq = s.n <= a.QT ? (s.n > 0 ? 1 : 0) : (s.n + a.QT - 1) / a.QT;
   s.pair = s.mid = s.head = 0;
+  s.most = 0;
   if (!s.n) return s;
-  // the most steps that a tile takes
   int64_t most = (s.len + STEP - 1) / STEP;
   if (a.window) most = min(most, (int64_t(a.window) + a.QT) / STEP + 2);
-  most = max(most, int64_t(1));
-  s.pair = 2 * most;
-  // tiles qt and nq - 1 - qt end at positions that add up to the same
-  if (s.off >= 0) s.pair = min(s.pair, (2 * int64_t(s.off) + int64_t(s.nq + 1) * a.QT) / STEP + 2);
+  s.most = int(max(most, int64_t(1)));
+  if (s.nq > 1) {
+    s.pair = 2 * int64_t(s.most);
+    // tiles qt and nq - 1 - qt end at positions that add up to the same
+    if (s.off >= 0) s.pair = min(s.pair, (2 * int64_t(s.off) + int64_t(s.nq + 1) * a.QT) / STEP + 2);
+  }
   int k0;
   if (s.nq & 1) s.mid = tile_steps<STEP>(a, s, s.nq / 2, &k0);
   s.head = (s.nq / 2) * s.pair + s.mid;
   return s;
 }
 
-// Sum over the workgroup and the exclusive prefix of 64-bit numbers.
-template <int THREADS>
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* tmp, int64_t* total) {
-  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-  int64_t x = v;
-#pragma unroll
-  for (int d = 1; d < kWave; d <<= 1) {
-    const int64_t y = __shfl_up(x, d, kWave);
-    if (lane >= d) x += y;
+__device__ __forceinline__ int64_t lane_of(int64_t v, int lane) {
+  return (int64_t(__builtin_amdgcn_readlane(int(v >> 32), lane)) << 32) |
+         uint32_t(__builtin_amdgcn_readlane(int(v), lane));
+}
+__device__ __forceinline__ Seq lane_of(const Seq& s, int lane) {
+  Seq r;
+  r.row0 = __builtin_amdgcn_readlane(s.row0, lane);
+  r.n = __builtin_amdgcn_readlane(s.n, lane);
+  r.off = __builtin_amdgcn_readlane(s.off, lane);
+  r.len = __builtin_amdgcn_readlane(s.len, lane);
+  r.nq = __builtin_amdgcn_readlane(s.nq, lane);
+  r.most = __builtin_amdgcn_readlane(s.most, lane);
+  r.pair = lane_of(s.pair, lane);
+  r.mid = lane_of(s.mid, lane);
+  r.head = lane_of(s.head, lane);
+  return r;
+}
+
+// Where a workgroup's run begins and ends.
+struct Run {
+  int64_t total;        // steps of the line
+  int64_t length;       // of every run
+  bool whole;           // tiles are not cut: a run has those that begin in it
+  int b;                // sequence of the first step
+  int64_t r;            // its place in the sequence's part of the line
+  Seq s;
+};
+
+// 64 sequences at a time, by every wave for itself (no barrier, no LDS): once
+// for the line's length, and, if there are more than 64, again to find the
+// place.
+template <class S>
+__device__ __forceinline__ Run find_run(const AttnArgs& a, int me) {
+  const int lane = threadIdx.x & (kWave - 1);
+  Run run;
+  run.total = 0;
+  int64_t tiles = 0;
+  int most = 0;
+  Seq mine;
+  int64_t c = 0, upto = 0;
+  for (int base = 0; base < a.kv.B; base += kWave) {
+    const bool live = base + lane < a.kv.B;
+    mine = seq_of<S::kStep>(a, live ? base + lane : a.kv.B - 1);
+    c = live ? a.kv.Hkv * mine.head : 0;
+    upto = c;
+    int n = live ? mine.nq : 0, m = live ? mine.most : 0;
+    const int used = min(a.kv.B - base, kWave);
+    for (int d = 1; d < used; d <<= 1) {
+      const int64_t y = __shfl_up(upto, d, kWave);
+      if (lane >= d) upto += y;
+      n += __shfl_down(n, d, kWave);       // (lane 0 gets them all)
+      m = max(m, __shfl_down(m, d, kWave));
+    }
+    run.total += lane_of(upto, used - 1);
+    tiles += int64_t(__builtin_amdgcn_readlane(n, 0)) * a.kv.Hkv;
+    most = max(most, __builtin_amdgcn_readlane(m, 0));
   }
-  __syncthreads();
-  if (lane == kWave - 1) tmp[wave] = x;
-  __syncthreads();
-  int64_t before = 0, all = 0;
-#pragma unroll
-  for (int w = 0; w < THREADS / kWave; ++w) {
-    if (w < wave) before += tmp[w];
-    all += tmp[w];
+  run.length = quotient(run.total + a.grid - 1, a.grid);
+  // A cut tile's parts cost about kCut steps each to leave and to join.  Cut
+  // if the longest tile, or as many average ones as a workgroup gets, takes
+  // longer than equal runs and two cuts.
+  const int64_t rounds = quotient(tiles + a.grid - 1, a.grid);
+  run.whole = most <= run.length + 2 * S::kCut &&
+              rounds * run.total <= (run.length + 2 * S::kCut) * max(tiles, int64_t(1));
+  if (!run.whole) run.length = max(run.length, int64_t(S::kLeast));
+  const int64_t x = me * run.length;
+  run.b = 0, run.r = 0;
+  if (x >= run.total) return run;
+  int64_t before = 0;
+  for (int base = 0; base < a.kv.B; base += kWave) {
+    if (__builtin_expect(a.kv.B > kWave, 0)) {
+      const bool live = base + lane < a.kv.B;
+      mine = seq_of<S::kStep>(a, live ? base + lane : a.kv.B - 1);
+      c = live ? a.kv.Hkv * mine.head : 0;
+      upto = c;
+      for (int d = 1; d < kWave; d <<= 1) {
+        const int64_t y = __shfl_up(upto, d, kWave);
+        if (lane >= d) upto += y;
+      }
+    }
+    const uint64_t behind = __ballot(x < before + upto);
+    if (behind) {
+      const int at = __builtin_ctzll(behind);
+      run.b = base + at;
+      run.r = x - before - lane_of(upto, at) + lane_of(c, at);
+      run.s = lane_of(mine, at);
+      break;
+    }
+    before += lane_of(upto, kWave - 1);
   }
-  *total = all;
-  return before + x - v;
+  return run;
 }
 
 // What join_kernel needs of the tile that runs through the start of a
 // workgroup's run, at the first such start of a tile.
 struct Joint {
-  int32_t parts;        // 0: nothing to join here
   int32_t first;        // the workgroup with the first part (its second slot; the others': their first)
   int32_t row0, tokens, head;
-  int32_t pad[3];
 };
-
-// Rows of the tile: query head and row of the batch.
-struct RowAt {
-  int row, head;
-};
+// The number of its parts, 0: nothing to join here; then the Joints.
+__device__ __forceinline__ int32_t* joint_parts(const AttnArgs& a) { return static_cast<int32_t*>(a.joints); }
+__device__ __forceinline__ Joint* joint_at(const AttnArgs& a, int i) {
+  return reinterpret_cast<Joint*>(joint_parts(a) + kMaxGrid) + i;
+}
 
 // A token's output, four columns per lane (D / 4 lanes a row).
 __device__ __forceinline__ void store_row4(const AttnArgs& a, int64_t row, int head, int D, int col, f32x4 v) {
@@ -247,13 +350,19 @@ struct Shape {
   static constexpr int kLoads = kArea / 1024;               // 1 KiB loads for it
   static constexpr int kRing = KW * NS * 2 * kArea;
   static constexpr int kScales = F8 ? KW * (NS + 1) * 2 * KS * 4 : 0;
-  static constexpr int kCols = D < 128 ? D : 128;           // columns of an epilogue's round
+  // columns of an epilogue's round (a wave's rows go through LDS)
+  static constexpr int kCols = D < 128 || RW == 1 ? D : 128;
   static constexpr int kOutPitch = kCols + 4;               // (rows 4 banks apart)
   static constexpr int kOut = kWaves * 32 * kOutPitch * 4;
   static constexpr int kData = kRing + kScales > kOut ? kRing + kScales : kOut;
   static constexpr int kLds = kData + kIds * 4 + kWaves * 32 * 8;
   static constexpr int kPerCu = kMaxLds / (kLds + 256) >= 2 && kThreads <= 256 ? 2 : 1;
-  static_assert(kLds + 256 <= kMaxLds && (RW == 1 || NS == 2) && (KS == 32 || KS == 64), "shape");
+  static constexpr int kRowsAt = 64 / kChunks;              // positions of a 1 KiB load
+  // In steps: what a cut costs each side (the tile's rows in fp32 out and in),
+  // and the shortest run if tiles are cut.
+  static constexpr int kAhead = 4;                          // operand reads ahead of their products
+  static constexpr int kCut = RW, kLeast = RW;
+  static_assert(kLds + 256 <= kMaxLds && (RW == 1 || NS >= 2) && (KS == 32 || KS == 64), "shape");
   static_assert(RW == 1 || 2 * kLoads % RW == 0, "loads");
 
   // Permutations of a row's 16-byte chunks in LDS, so that what is read
@@ -275,10 +384,11 @@ __global__ __launch_bounds__(S::kThreads, S::kPerCu * S::kThreads / 256) void at
   constexpr int D = S::D, RW = S::RW, KW = S::KW, KS = S::KS, NS = S::NS, STEP = S::kStep, NB = KS / 32;
   constexpr int PARTS = S::kParts;
   constexpr bool F8 = S::F8;
+  constexpr int AHEAD = S::kAhead;
+  using KeyPart = std::conditional_t<F8, i32x2, bf16x8>;       // 8 columns (or positions) as they lie in LDS
+  using ValuePart = KeyPart;
   constexpr int PITCH = S::kPitch, BANKS = PITCH < 256 ? PITCH : 256;   // (a row's part that chunks are permuted in)
   extern __shared__ __align__(256) uint8_t smem[];
-  __shared__ int64_t scan_tmp[S::kWaves];
-  __shared__ int64_t found[2];
   MOE_LDS uint8_t* const lds = (MOE_LDS uint8_t*)smem;
   int32_t* const ids = reinterpret_cast<int32_t*>(smem + S::kData);
   f32x2* const stats = reinterpret_cast<f32x2*>(smem + S::kData + kIds * 4);   // [waves][32]: maximum, sum
@@ -286,51 +396,29 @@ __global__ __launch_bounds__(S::kThreads, S::kPerCu * S::kThreads / 256) void at
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int kw = wave / RW, rw = wave % RW;
   const int col = lane & 31, half = lane >> 5;
+  // (heads of 256 leave no registers for what a step derives from it)
+  auto lane_at = [&] { return D == 256 ? lane_now() : lane; };
   // neighbouring runs on one XCD (workgroups go to the 8 in turn): they share keys and values
   const int me = int(blockIdx.x & 7) * (a.grid >> 3) + int(blockIdx.x >> 3);
 
-  // where this workgroup's run starts
-  int64_t total = 0, mine = 0;
-  for (int base = 0; base < a.kv.B; base += S::kThreads) {
-    const int b = base + threadIdx.x;
-    mine = b < a.kv.B ? a.kv.Hkv * seq_of<STEP>(a, b).head : 0;
-    int64_t sum;
-    block_scan<S::kThreads>(mine, scan_tmp, &sum);
-    total += sum;
-  }
-  const int64_t run = max(int64_t(a.min_steps), (total + a.grid - 1) / a.grid);
-  int64_t x = me * run;
-  const int64_t x1 = min(total, x + run);
-  Joint* const joint = static_cast<Joint*>(a.joints) + me;
-  if (x >= total) {
-    if (threadIdx.x == 0) joint->parts = 0;
+  const Run run = find_run<S>(a, me);
+  const int64_t x0 = me * run.length, x1 = min(run.total, x0 + run.length);
+  if (x0 >= x1) {
+    if (threadIdx.x == 0) joint_parts(a)[me] = 0;
     return;
   }
-  int64_t before = 0;
-  for (int base = 0; base < a.kv.B; base += S::kThreads) {
-    const int b = base + threadIdx.x;
-    if (a.kv.B > S::kThreads) mine = b < a.kv.B ? a.kv.Hkv * seq_of<STEP>(a, b).head : 0;
-    int64_t sum;
-    const int64_t at = before + block_scan<S::kThreads>(mine, scan_tmp, &sum);
-    if (mine > 0 && x >= at && x < at + mine) found[0] = b, found[1] = x - at;
-    before += sum;
-    if (x < before) break;
-  }
-  __syncthreads();
-  int b = __builtin_amdgcn_readfirstlane(int(found[0]));
-  int64_t r = found[1];
-  r = (int64_t(__builtin_amdgcn_readfirstlane(int(r >> 32))) << 32) |
-      uint32_t(__builtin_amdgcn_readfirstlane(int(r)));
-  bool starts = true;       // the run's first tile
+  int64_t x = x0, r = run.r;
+  int b = run.b;
+  Seq s = run.s;
 
   while (x < x1) {
-    const Seq s = seq_of<STEP>(a, b);
     if (r >= a.kv.Hkv * s.head) {
       ++b, r = 0;
+      s = seq_of<STEP>(a, b);
       continue;
     }
     // which tile, and from which of its steps
-    const int h = int(r / s.head);
+    const int h = a.kv.Hkv == 1 ? 0 : int(quotient(r, s.head));
     const int64_t in_head = r - h * s.head;
     const int pairs = s.nq / 2;
     int qt, tile0, steps;           // query tile; its first step; its number of steps
@@ -340,43 +428,52 @@ __global__ __launch_bounds__(S::kThreads, S::kPerCu * S::kThreads / 256) void at
       steps = tile_steps<STEP>(a, s, qt, &tile0);
       from = int(in_head - pairs * s.pair);
     } else {
-      qt = int(in_head / s.pair);
+      qt = int(quotient(in_head, s.pair));
       from = int(in_head - qt * s.pair);
       steps = tile_steps<STEP>(a, s, qt, &tile0);
       if (from >= steps) {
         from -= steps;
         qt = s.nq - 1 - qt;
         steps = tile_steps<STEP>(a, s, qt, &tile0);
-        if (from >= steps) {        // what the pair does not need
+        if (__builtin_expect(from >= steps, 0)) {      // what the pair does not need
+          if (threadIdx.x == 0 && x == x0) joint_parts(a)[me] = 0;
           const int64_t skip = s.pair - (in_head - int64_t(s.nq - 1 - qt) * s.pair);
           x += skip, r += skip;
-          starts = false;
-          if (threadIdx.x == 0 && x - skip == me * run) joint->parts = 0;
           continue;
         }
       }
     }
-    const int take = int(min(int64_t(steps - from), x1 - x));
-    const bool whole = from == 0 && take == steps;
     const int t0 = qt * a.QT, nt = min(s.n - t0, a.QT);
-    const int slot = me * 2 + (from == 0 ? 1 : 0);
-    if (starts && threadIdx.x == 0) {
-      const int64_t begin = x - from, end = begin + steps;
-      const int64_t first = begin / run, last = (end - 1) / run;
-      Joint j;
-      j.parts = from > 0 && first == me - 1 ? int(last - first + 1) : 0;
-      j.first = int(first);
-      j.row0 = s.row0 + t0;
-      j.tokens = nt;
-      j.head = h;
-      *joint = j;
+    if (x == x0 && threadIdx.x == 0) {
+      int parts = 0;
+      // (the tile's first cut is this one)
+      if (!run.whole && from > 0 && x - from >= x0 - run.length) {
+        parts = int(quotient(x - from + steps - 1, run.length)) - (me - 1) + 1;
+        Joint j;
+        j.first = me - 1;
+        j.row0 = s.row0 + t0;
+        j.tokens = nt;
+        j.head = h;
+        *joint_at(a, me) = j;
+      }
+      joint_parts(a)[me] = parts;
     }
-    starts = false;
+    int take = steps - from;
+    if (run.whole) {
+      if (from > 0) {               // the run before has it
+        x += take, r += take;
+        continue;
+      }
+    } else if (take > x1 - x) {
+      take = int(x1 - x);
+    }
+    const bool whole = take == steps;
+    const int slot = me * 2 + (from == 0 ? 1 : 0);
     x += take, r += take;
 
     // ---- the tile's queries: this wave's 32 rows, as the products' right operand
     const int lr = rw * 32 + col;                       // this lane's row of the tile
-    const int token = lr / a.G;
+    const int token = a.token_of(lr);
     const bool live = token < nt;
     const int rpos = live ? s.off + t0 + token : -1;    // the last position it sees
     const int rfirst = a.window ? max(rpos - (a.window - 1), 0) : 0;
@@ -392,8 +489,8 @@ __global__ __launch_bounds__(S::kThreads, S::kPerCu * S::kThreads / 256) void at
       }
     }
     // what every row of this wave sees, and what any does
-    const int wave_t1 = min(nt - 1, (rw * 32 + 31) / a.G), wave_t0 = min(rw * 32 / a.G, nt - 1);
-    const bool wave_live = rw * 32 / a.G < nt;
+    const int wave_t1 = min(nt - 1, a.token_of(rw * 32 + 31)), wave_t0 = min(a.token_of(rw * 32), nt - 1);
+    const bool wave_live = a.token_of(rw * 32) < nt;
     const int sees_all = s.off + t0 + wave_t0;                                    // up to here
     const int sees_any = wave_live ? s.off + t0 + wave_t1 : -1;
     const int from_all = a.window ? s.off + t0 + wave_t1 - (a.window - 1) : 0;     // from here
@@ -412,13 +509,14 @@ __global__ __launch_bounds__(S::kThreads, S::kPerCu * S::kThreads / 256) void at
     const uint8_t* const vbase = a.kv.v + int64_t(h) * a.kv.head_stride * ELEM;
     const uint32_t page_bytes = uint32_t(a.kv.page_stride) * ELEM, slot_bytes = uint32_t(a.kv.slot_stride) * ELEM;
     const int shift = a.kv.page_shift;
+    const bool one_page = (1 << shift) >= S::kRowsAt && slot_bytes <= 1u << 26;
     const int span = max(1, int(min(int64_t(kIds - 1) << shift, int64_t(1) << 30)) / STEP);
     for (int s0 = 0; s0 < take; s0 += span) {
       const int count = min(span, take - s0);
       const int step0 = tile0 + from + s0;
       const int page0 = int((int64_t(step0) * STEP) >> shift);
       const int pages = int(((int64_t(step0 + count) * STEP - 1) >> shift) - page0) + 1;
-      __syncthreads();        // the ids, and all of LDS, have been used up
+      barrier_lds();          // the ids, and all of LDS, have been used up
       for (int i = threadIdx.x; i < pages; i += S::kThreads) {
         int id = -1;
         if (page0 + i < a.kv.max_pages) id = a.kv.page_table[b * a.kv.table_stride + page0 + i];
@@ -434,21 +532,35 @@ __global__ __launch_bounds__(S::kThreads, S::kPerCu * S::kThreads / 256) void at
       auto scales_of = [&](int i, bool value) -> MOE_LDS uint8_t* {
         return lds + S::kRing + ((kw * (NS + 1) + i % (NS + 1)) * 2 + (value ? 1 : 0)) * KS * 4;
       };
-      // load j of step i's keys or values
-      auto load = [&](int i, int j, bool value) {
-        const int row = j * (64 / S::kChunks) + lane / S::kChunks, pc = lane % S::kChunks;
-        const int pos = (step0 + i) * STEP + kw * KS + row;
-        const int id = page_of(pos);
-        const int c = pc ^ (value ? S::value_swizzle(row) : S::key_swizzle(row));
-        const uint8_t* p = (value ? vbase : kbase) + uint64_t(uint32_t(id)) * page_bytes +
-                           uint64_t(uint32_t(pos & ((1 << shift) - 1))) * slot_bytes + c * 16;
-        if (id < 0) p = reinterpret_cast<const uint8_t*>(&kZeros);
-        to_lds16(p, lds_address(slot_lds(i % NS, value) + j * 1024));
+      // the lane's position (KS of them) of a step: its page, or -1
+      auto pages_of = [&](int i) -> int { return page_of((step0 + i) * STEP + kw * KS + (lane_at() & (KS - 1))); };
+      // Load j of step i's keys or values.  Where all positions are there and a
+      // load's lie in one page, its base is the wave's (`even`).
+      auto load = [&](int i, int j, bool value, bool even, int id_here, int l) {
+        const int row0 = j * S::kRowsAt, pos0 = (step0 + i) * STEP + kw * KS + row0;
+        const uint32_t to = lds_address(slot_lds(i % NS, value) + j * 1024);
+        const int swz0 = value ? S::value_swizzle(row0) : S::key_swizzle(row0);
+        // (row0's bits and those of the lane's row are apart, and so are their swizzles')
+        const int lrow = l / S::kChunks;
+        const int chunk = ((l % S::kChunks) ^ (value ? S::value_swizzle(lrow) : S::key_swizzle(lrow))) * 16;
+        if (even) {
+          const uint32_t id = __builtin_amdgcn_readlane(id_here, row0);
+          const uint8_t* base = (value ? vbase : kbase) + uint64_t(id) * page_bytes +
+                                uint64_t(uint32_t(pos0 & ((1 << shift) - 1))) * slot_bytes;
+          to_lds16(base, (chunk ^ (swz0 * 16)) + uint32_t(lrow) * slot_bytes, to);
+        } else {
+          const int pos = pos0 + lrow, id = page_of(pos);
+          const uint8_t* p = (value ? vbase : kbase) + uint64_t(uint32_t(id)) * page_bytes +
+                             uint64_t(uint32_t(pos & ((1 << shift) - 1))) * slot_bytes + (chunk ^ (swz0 * 16));
+          if (id < 0) p = reinterpret_cast<const uint8_t*>(&kZeros);
+          to_lds16(p, to);
+        }
       };
       auto load_scales = [&](int i, bool value) {
         // (32 positions: the lower half of the wave keys', the upper values')
-        const bool up = KS == 32 ? half : value;
-        const int row = KS == 32 ? col : lane;
+        const int l = lane_at();
+        const bool up = KS == 32 ? l >= 32 : value;
+        const int row = l & (KS - 1);
         const int pos = (step0 + i) * STEP + kw * KS + row;
         const int id = page_of(pos);
         const float* p = (up ? a.kv.v_scale : a.kv.k_scale) +
@@ -457,33 +569,44 @@ __global__ __launch_bounds__(S::kThreads, S::kPerCu * S::kThreads / 256) void at
         to_lds4(p, lds_address(scales_of(i, KS == 32 ? false : value)));
       };
       constexpr int kScaleLoads = F8 ? 1 : 0;      // with the keys of a wave's own step
-      auto load_keys = [&](int i) {
+      auto load_own = [&](int i, bool value) {
+        const int id = pages_of(i), l = lane_at();
+        if (one_page && __ballot(id < 0) == 0) {
 #pragma unroll
-        for (int j = 0; j < S::kLoads; ++j) load(i, j, false);
-        if (F8) load_scales(i, false);
-      };
-      auto load_values = [&](int i) {
-#pragma unroll
-        for (int j = 0; j < S::kLoads; ++j) load(i, j, true);
+          for (int j = 0; j < S::kLoads; ++j) load(i, j, value, true, id, l);
+        } else {
+#pragma unroll 1
+          for (int j = 0; j < S::kLoads; ++j) load(i, j, value, false, id, l);
+        }
+        if (F8 && !value) load_scales(i, false);
       };
       // RW waves share a step's loads
+      constexpr int kShare = 2 * S::kLoads / RW;
       auto load_shared = [&](int i) {
+        const int id = pages_of(i), l = lane_at();
+        if (one_page && __ballot(id < 0) == 0) {
 #pragma unroll
-        for (int j = 0; j < 2 * S::kLoads / RW; ++j) {
-          const int g = rw * (2 * S::kLoads / RW) + j;
-          const bool value = g >= S::kLoads;
-          load(i, value ? g - S::kLoads : g, value);
+          for (int j = 0; j < kShare; ++j) {
+            const int g = rw * kShare + j;
+            load(i, g % S::kLoads, g >= S::kLoads, true, id, l);
+          }
+        } else {
+#pragma unroll 1
+          for (int j = 0; j < kShare; ++j) {
+            const int g = rw * kShare + j;
+            load(i, g % S::kLoads, g >= S::kLoads, false, id, l);
+          }
         }
-        if (F8 && rw < (KS == 32 ? 1 : 2)) load_scales(i, rw == 1);
+        if (F8) load_scales(i, KS == 64 && (rw & 1));      // (by every wave: one count of loads for all)
       };
 
       if constexpr (RW == 1) {
         for (int i = 0; i < NS && i < count; ++i) {
-          load_keys(i);
-          load_values(i);
+          load_own(i, false);
+          load_own(i, true);
         }
       } else {
-        load_shared(0);
+        for (int i = 0; i < NS - 1 && i < count; ++i) load_shared(i);
       }
 
       for (int i = 0; i < count; ++i) {
@@ -494,9 +617,13 @@ __global__ __launch_bounds__(S::kThreads, S::kPerCu * S::kThreads / 256) void at
           else
             wait_loads<0>();
         } else {
-          wait_loads<0>();
+          // behind this step's loads: those of NS - 2 steps, if the end is not near
+          if (i + NS - 2 < count)
+            wait_loads<(NS - 2) * (kShare + kScaleLoads)>();
+          else
+            wait_loads<0>();
           barrier_lds();
-          if (i + 1 < count) load_shared(i + 1);
+          if (i + NS - 1 < count) load_shared(i + NS - 1);
         }
         const int pos0 = (step0 + i) * STEP + kw * KS;      // this group's positions
         MOE_LDS uint8_t* const kl = slot_lds(i % NS, false);
@@ -505,6 +632,7 @@ __global__ __launch_bounds__(S::kThreads, S::kPerCu * S::kThreads / 256) void at
         // which of the positions are there
         uint32_t there[NB];
         bool all = true;
+        const int l = lane_at(), col = l & 31, half = l >> 5;
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
           there[n] = uint32_t(__ballot(page_of(pos0 + n * 32 + col) >= 0));
@@ -518,22 +646,30 @@ __global__ __launch_bounds__(S::kThreads, S::kPerCu * S::kThreads / 256) void at
           // bytes) and an offset; 32 rows further the permutation is the same
           uint32_t at = uint32_t(reinterpret_cast<uintptr_t>(kl)) + col * PITCH +
                         (F8 ? S::key_swizzle(col) * 16 + half * 8 : (S::key_swizzle(col) ^ half) * 16);
-          asm volatile("" : "+v"(at));     // (not to be kept for every step)
+          constexpr int COUNT = NB * D / 16;
+          auto read = [&](int u) {
+            constexpr int UNIT = F8 ? 16 : 32;
+            const int n = u / (D / 16), k = u % (D / 16);
+            const uint32_t from = (at ^ (k * UNIT % BANKS)) + k * UNIT / BANKS * BANKS + n * 32 * PITCH;
+            return *(MOE_LDS KeyPart*)(uintptr_t)from;
+          };
+          KeyPart part[AHEAD];
 #pragma unroll
-          for (int n = 0; n < NB; ++n) {
+          for (int u = 0; u < AHEAD && u < COUNT; ++u) part[u] = read(u);
+          bf16x8 kf = operand(part[0]);
+          in_order();
 #pragma unroll
-            for (int j = 0; j < 16; ++j) sc[n][j] = 0.0f;
+          for (int u = 0; u < COUNT; ++u) {
+            const int n = u / (D / 16), k = u % (D / 16);
+            if (k == 0) {
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-              constexpr int UNIT = F8 ? 16 : 32;
-              const uint32_t from = (at ^ (k * UNIT % BANKS)) + k * UNIT / BANKS * BANKS + n * 32 * PITCH;
-              bf16x8 kf;
-              if (F8)
-                kf = from_codes(*(MOE_LDS i32x2*)(uintptr_t)from);
-              else
-                kf = *(MOE_LDS bf16x8*)(uintptr_t)from;
-              sc[n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, q[k], sc[n], 0, 0, 0);
+              for (int j = 0; j < 16; ++j) sc[n][j] = 0.0f;
             }
+            const bf16x8 now = kf;
+            if (u + AHEAD < COUNT) part[u % AHEAD] = read(u + AHEAD);
+            sc[n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(now, q[k], sc[n], 0, 0, 0);
+            if (u + 1 < COUNT) kf = operand(part[(u + 1) % AHEAD]);
+            in_order();
           }
           if (F8) {
 #pragma unroll
@@ -547,18 +683,20 @@ __global__ __launch_bounds__(S::kThreads, S::kPerCu * S::kThreads / 256) void at
           }
           if (!all || pos0 + KS - 1 > sees_all || pos0 < from_all) {
 #pragma unroll
-            for (int n = 0; n < NB; ++n)
+            for (int n = 0; n < NB; ++n) {
+              // a bit for each of the 32 positions that this lane's row sees
+              const int last = rpos - pos0 - n * 32, first = rfirst - pos0 - n * 32;
+              uint32_t sees = last >= 31 ? ~0u : last < 0 ? 0u : (2u << last) - 1u;
+              sees &= first <= 0 ? ~0u : first > 31 ? 0u : ~0u << first;
+              sees = (sees & there[n]) >> (4 * half);
 #pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                const int at = 8 * (j / 4) + 4 * half + j % 4, pos = pos0 + n * 32 + at;
-                const bool seen = ((there[n] >> at) & 1u) && pos <= rpos && pos >= rfirst;
-                if (!seen) sc[n][j] = -INFINITY;
-              }
+              for (int j = 0; j < 16; ++j) sc[n][j] = sees & (1u << (8 * (j / 4) + j % 4)) ? sc[n][j] : -INFINITY;
+            }
           }
         }
         if constexpr (RW == 1) {
           wait_reads();
-          if (i + NS < count) load_keys(i + NS);
+          if (i + NS < count) load_own(i + NS, false);
         }
         bf16x8 p[PARTS][NB * 2];
         if (any) {
@@ -631,37 +769,51 @@ __global__ __launch_bounds__(S::kThreads, S::kPerCu * S::kThreads / 256) void at
             wait_loads<0>();
         }
         if (any) {
-          // lanes of 16 give the rows that the transposing read takes: 4 rows of
-          // 16 columns (16 bits), 8 of 16 (8 bits); the permutation as for keys
-          const int li = lane & 15, cols16 = (lane >> 4) & 1;
-          const int row = F8 ? 8 * (li >> 3) + 4 * half + ((li >> 1) & 3) : 4 * half + (li >> 2);
-          const int chunk = F8 ? cols16 : 2 * cols16 + ((li & 3) >> 1);
-          uint32_t at = uint32_t(reinterpret_cast<uintptr_t>(vl)) + row * PITCH +
-                        (chunk ^ S::value_swizzle(row)) * 16 + (li & 1) * 8;
-          asm volatile("" : "+v"(at));
-#pragma unroll
-          for (int n = 0; n < NB * 2; ++n) {
-#pragma unroll
-            for (int d = 0; d < D / 32; ++d) {
-              constexpr int UNIT = F8 ? 32 : 64;
-              const uint32_t from = (at ^ (d * UNIT % BANKS)) + d * UNIT / BANKS * BANKS + n * 16 * PITCH;
-              bf16x8 vf;
-              if (F8) {
-                vf = from_codes(__builtin_amdgcn_ds_read_tr8_b64_v2i32((MOE_LDS i32x2*)(uintptr_t)from));
-              } else {
-                const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MOE_LDS s16x4*)(uintptr_t)from);
-                const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MOE_LDS s16x4*)(uintptr_t)(from + 8 * PITCH));
-                vf = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-              }
-#pragma unroll
-              for (int k = PARTS - 1; k >= 0; --k)
-                o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, p[k][n], o[d], 0, 0, 0);
+          // lanes of 16 give the rows that the transposing read takes: 4 rows of 16
+          // columns (16 bits), 8 of 16 (8 bits); the permutation as for keys
+          constexpr int VCOUNT = NB * 2 * D / 32;
+          uint32_t vat;
+          {
+            const int li = l & 15, cols16 = (l >> 4) & 1;
+            const int row = F8 ? 8 * (li >> 3) + 4 * half + ((li >> 1) & 3) : 4 * half + (li >> 2);
+            const int chunk = F8 ? cols16 : 2 * cols16 + ((li & 3) >> 1);
+            vat = uint32_t(reinterpret_cast<uintptr_t>(vl)) + row * PITCH + (chunk ^ S::value_swizzle(row)) * 16 +
+                  (li & 1) * 8;
+          }
+          auto value_part = [&](int u) {
+            constexpr int UNIT = F8 ? 32 : 64;
+            const int n = u / (D / 32), d = u % (D / 32);
+            const uint32_t from = (vat ^ (d * UNIT % BANKS)) + d * UNIT / BANKS * BANKS + n * 16 * PITCH;
+            ValuePart v;
+            if constexpr (F8) {
+              v = __builtin_amdgcn_ds_read_tr8_b64_v2i32((MOE_LDS i32x2*)(uintptr_t)from);
+            } else {
+              const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MOE_LDS s16x4*)(uintptr_t)from);
+              const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MOE_LDS s16x4*)(uintptr_t)(from + 8 * PITCH));
+              v = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
             }
+            return v;
+          };
+          ValuePart vpart[AHEAD];
+#pragma unroll
+            for (int u = 0; u < AHEAD && u < VCOUNT; ++u) vpart[u] = value_part(u);
+          bf16x8 vf = operand(vpart[0]);
+          in_order();
+#pragma unroll
+          for (int u = 0; u < VCOUNT; ++u) {
+            const int n = u / (D / 32), d = u % (D / 32);
+            const bf16x8 now = vf;
+            if (u + AHEAD < VCOUNT) vpart[u % AHEAD] = value_part(u + AHEAD);
+#pragma unroll
+            for (int k = PARTS - 1; k >= 0; --k)
+              o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(now, p[k][n], o[d], 0, 0, 0);
+            if (u + 1 < VCOUNT) vf = operand(vpart[(u + 1) % AHEAD]);
+            in_order();
           }
         }
         if constexpr (RW == 1) {
           wait_reads();
-          if (i + NS < count) load_values(i + NS);
+          if (i + NS < count) load_own(i + NS, true);
         }
       }
     }
@@ -671,12 +823,12 @@ __global__ __launch_bounds__(S::kThreads, S::kPerCu * S::kThreads / 256) void at
       const f32x2 sums = both_halves(sum);
       sum = sums[0] + sums[1];
     }
-    __syncthreads();       // the steps' LDS has been used up
+    barrier_lds();         // the steps' LDS has been used up
     float m = mref;
     float f = 1.0f;
     if constexpr (KW > 1) {
       if (half == 0) stats[wave * 32 + col] = f32x2{mref, sum};
-      __syncthreads();
+      barrier_lds();
       f32x2 st[KW];
 #pragma unroll
       for (int k = 0; k < KW; ++k) st[k] = stats[(k * RW + rw) * 32 + col], m = fmaxf(m, st[k][0]);
@@ -703,7 +855,7 @@ __global__ __launch_bounds__(S::kThreads, S::kPerCu * S::kThreads / 256) void at
           for (int e = 0; e < 4; ++e) v[e] = o[c0 / 32 + d][4 * g + e] * f;
           *reinterpret_cast<f32x4*>(mine_out + col * S::kOutPitch + d * 32 + 8 * g + 4 * half) = v;
         }
-      __syncthreads();
+      barrier_lds();
       // the KW waves of these rows take 32 / KW of them each
 #pragma unroll 1
       for (int i = 0; i < 32 / KW; i += kRowsAt) {
@@ -713,71 +865,126 @@ __global__ __launch_bounds__(S::kThreads, S::kPerCu * S::kThreads / 256) void at
         for (int k = 0; k < KW; ++k)
           v += *reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(smem) +
                                                ((k * RW + rw) * 32 + row) * S::kOutPitch + c);
-        const int tr = rw * 32 + row, tk = tr / a.G;
+        const int tr = rw * 32 + row, tk = a.token_of(tr);
         if (whole) {
           if (tk < nt) store_row4(a, s.row0 + t0 + tk, h * a.G + tr - tk * a.G, D, c0 + c, v);
         } else {
           *reinterpret_cast<f32x4*>(part + tr * D + c0 + c) = v;
         }
       }
-      __syncthreads();
+      barrier_lds();
     }
   }
 }
 
 // The parts of a cut tile, in order: out = sum_i exp2(m_i - m) o_i / sum_i
-// exp2(m_i - m) l_i.  A workgroup takes every gridDim.y-th row of the tile
-// that begins before blockIdx.x's run; its waves' lanes hold four columns of
-// a part each.
+// exp2(m_i - m) l_i.  Every workgroup counts the cut tiles' rows and takes its
+// share.  D / 4 lanes hold a row, four columns each: where there are many rows,
+// they go through a row's parts by themselves; where there are few, all
+// groups of lanes of a workgroup share a row's parts.
+constexpr int kJoinThreads = 512;
+
 template <int D>
-__global__ __launch_bounds__(256) void join_kernel(const AttnArgs a, int rows) {
-  constexpr int LANES = D / 4, PARTS = 256 / LANES;
-  __shared__ f32x4 acc[256];
-  __shared__ f32x2 stat[PARTS];
-  const Joint j = static_cast<const Joint*>(a.joints)[blockIdx.x];
-  if (j.parts == 0) return;
-  const int sub = threadIdx.x % LANES, p0 = threadIdx.x / LANES;
-  const int used = min(j.tokens * a.G, rows);
-  for (int row = blockIdx.y; row < used; row += gridDim.y) {
+__global__ __launch_bounds__(kJoinThreads) void join_kernel(const AttnArgs a, int rows) {
+  constexpr int LANES = D / 4, GROUPS = kJoinThreads / LANES, AHEAD = 8;
+  static_assert(kMaxGrid == kJoinThreads, "a thread per run");
+  __shared__ int32_t upto[kMaxGrid];       // rows of the cut tiles up to this one
+  __shared__ int32_t parts_of[kMaxGrid];
+  __shared__ Joint joints[kMaxGrid];
+  __shared__ int32_t waves[kJoinThreads / kWave];
+  __shared__ f32x4 acc[kJoinThreads];
+  __shared__ f32x2 stat[GROUPS];
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+  {
+    int n = 0;
+    if (int(threadIdx.x) < a.grid) {
+      const int parts = joint_parts(a)[threadIdx.x];
+      const Joint j = *joint_at(a, threadIdx.x);
+      parts_of[threadIdx.x] = parts;
+      joints[threadIdx.x] = j;
+      if (parts > 0) n = min(j.tokens * a.G, rows);
+    }
+#pragma unroll
+    for (int d = 1; d < kWave; d <<= 1) {
+      const int y = __shfl_up(n, d, kWave);
+      if (lane >= d) n += y;
+    }
+    if (lane == kWave - 1) waves[wave] = n;
+    __syncthreads();
+    for (int w = 0; w < wave; ++w) n += waves[w];
+    upto[threadIdx.x] = n;
+    __syncthreads();
+  }
+  const int total = upto[kMaxGrid - 1];
+  const int sub = threadIdx.x % LANES, group = threadIdx.x / LANES;
+  const bool many = total > int(gridDim.x) * 2;
+  const int split = many ? 1 : GROUPS;             // groups that share a row
+  const int stride = many ? int(gridDim.x) * GROUPS : int(gridDim.x);
+  for (int base = many ? int(blockIdx.x) * GROUPS : int(blockIdx.x); base < total; base += stride) {
+    const int item = many ? base + group : base;
+    const bool live = item < total;
+    int at = 0;
+    for (int d = kMaxGrid / 2; d; d >>= 1)
+      if (upto[at + d - 1] <= item) at += d;
+    at = min(at, kMaxGrid - 1);
+    const Joint j = joints[at];
+    const int parts = live ? parts_of[at] : 0;
+    const int row = item - (at ? upto[at - 1] : 0);
     float m = -INFINITY, l = 0.0f;
     f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int p = p0; p < j.parts; p += PARTS) {
-      const int slot = (j.first + p) * 2 + (p == 0 ? 1 : 0);
-      const float* part = a.parts + int64_t(slot) * rows * (D + 2);
-      const f32x2 st = *reinterpret_cast<const f32x2*>(part + rows * D + row * 2);
-      const f32x4 w = *reinterpret_cast<const f32x4*>(part + row * D + sub * 4);
-      const float top = fmaxf(m, st[0]);
-      if (top == -INFINITY) continue;
-      const float f = exp2_fast(m - top), g = exp2_fast(st[0] - top);
-      l = l * f + st[1] * g;
+    for (int p = many ? 0 : group; p < parts; p += split * AHEAD) {
+      f32x2 st[AHEAD];
+      f32x4 w[AHEAD];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = v[e] * f + w[e] * g;
-      m = top;
-    }
-    __syncthreads();
-    acc[threadIdx.x] = v;
-    if (sub == 0) stat[p0] = f32x2{m, l};
-    __syncthreads();
-    if (p0 == 0) {
-      float top = stat[0][0];
-#pragma unroll
-      for (int p = 1; p < PARTS; ++p) top = fmaxf(top, stat[p][0]);
-      float total = 0.0f;
-      v = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      if (top > -INFINITY) {
-#pragma unroll
-        for (int p = 0; p < PARTS; ++p) {
-          const float f = exp2_fast(stat[p][0] - top);
-          total += stat[p][1] * f;
-          const f32x4 w = acc[p * LANES + sub];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] += w[e] * f;
+      for (int k = 0; k < AHEAD; ++k) {
+        st[k] = f32x2{-INFINITY, 0.0f};
+        const int pk = p + k * split;
+        if (pk < parts) {
+          const int slot = (j.first + pk) * 2 + (pk == 0 ? 1 : 0);
+          const float* part = a.parts + int64_t(slot) * rows * (D + 2);
+          st[k] = *reinterpret_cast<const f32x2*>(part + rows * D + row * 2);
+          w[k] = *reinterpret_cast<const f32x4*>(part + row * D + sub * 4);
         }
       }
-      const float f = total > 0.0f ? 1.0f / total : 0.0f;
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k) {
+        const float top = fmaxf(m, st[k][0]);
+        if (st[k][0] == -INFINITY) continue;
+        const float f = exp2_fast(m - top), g = exp2_fast(st[k][0] - top);
+        l = l * f + st[k][1] * g;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = v[e] * f + w[k][e] * g;
+        m = top;
+      }
+    }
+    if (!many) {
+      __syncthreads();
+      acc[threadIdx.x] = v;
+      if (sub == 0) stat[group] = f32x2{m, l};
+      __syncthreads();
+      if (group == 0) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int p = 0; p < GROUPS; ++p) top = fmaxf(top, stat[p][0]);
+        l = 0.0f;
+        v = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        if (top > -INFINITY) {
+#pragma unroll
+          for (int p = 0; p < GROUPS; ++p) {
+            const float f = exp2_fast(stat[p][0] - top);
+            l += stat[p][1] * f;
+            const f32x4 w = acc[p * LANES + sub];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] += w[e] * f;
+          }
+        }
+      }
+    }
+    if (live && (many || group == 0)) {
+      const float f = l > 0.0f ? 1.0f / l : 0.0f;
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] *= f;
-      const int tk = row / a.G;
+      const int tk = a.token_of(row);
       store_row4(a, j.row0 + tk, j.head * a.G + row - tk * a.G, D, sub * 4, v);
     }
   }
@@ -794,8 +1001,7 @@ hipError_t allow_lds(Kernel kernel, int64_t bytes) {
 // Rows of a tile for so many rows per sequence.
 int rows_for(int64_t rows) { return rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256; }
 
-constexpr int kMaxGrid = 2 * kCus;
-constexpr size_t kJointBytes = kMaxGrid * sizeof(Joint);
+constexpr size_t kJointBytes = kMaxGrid * (sizeof(int32_t) + sizeof(Joint));
 
 size_t parts_bytes(int rows, int D) {
   return size_t(rows <= 128 ? kMaxGrid : kCus) * 2 * rows * (D + 2) * 4;
@@ -807,7 +1013,7 @@ hipError_t launch_shape(AttnArgs a, hipStream_t st) {
   a.QT = S::kRows / a.G;
   a.joints = a.ws;
   a.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + kJointBytes);
-  a.min_steps = 1;
+  a.inv_g = (65536 + a.G - 1) / a.G;
   // no more workgroups than steps there can be (a multiple of the 8 XCDs)
   const int64_t tiles = int64_t(a.T) / a.QT + a.kv.B;
   const int64_t steps = ((int64_t(a.kv.max_pages) << a.kv.page_shift) + S::kStep - 1) / S::kStep;
@@ -818,7 +1024,7 @@ hipError_t launch_shape(AttnArgs a, hipStream_t st) {
   const hipError_t e = allow_lds(kernel, S::kLds);
   if (e != hipSuccess) return e;
   kernel<<<a.grid, S::kThreads, S::kLds, st>>>(a);
-  join_kernel<S::D><<<dim3(a.grid, S::kRows), 256, 0, st>>>(a, S::kRows);
+  join_kernel<S::D><<<2 * kCus, kJoinThreads, 0, st>>>(a, S::kRows);
   return hipGetLastError();
 }
 

@@ -168,9 +168,11 @@ struct AttnArgs {
   uint8_t* x8;                 // e4m3 [T][Hq * D] (may be null)
   float* x8_scale;             // [T][Hq * D / 128]
   void* ws;
-  int QT, grid, min_steps;     // set by the launcher, as what follows
+  int QT, grid, inv_g;         // set by the launcher, as what follows
   void* joints;
   float* parts;
+  // row / G, row <= 256
+  __device__ __forceinline__ int token_of(int row) const { return row * inv_g >> 16; }
 };
 size_t attention_ws(int T, int Hq, int Hkv, int D);
 hipError_t launch_paged_attention(const AttnArgs& a, hipStream_t st);
