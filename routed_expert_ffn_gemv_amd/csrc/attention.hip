@@ -53,6 +53,7 @@ typedef __attribute__((ext_vector_type(4))) float f32x4;
 typedef __attribute__((ext_vector_type(16))) float f32x16;
 typedef __attribute__((ext_vector_type(4))) short s16x4;
 typedef __attribute__((ext_vector_type(2))) int i32x2;
+typedef __attribute__((ext_vector_type(4))) int i32x4;
 typedef __attribute__((ext_vector_type(4))) __bf16 bf16x4;
 typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
 typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
@@ -233,35 +234,35 @@ struct Run {
   Seq s;
 };
 
-// 64 sequences at a time, by every wave for itself (no barrier, no LDS): once
-// for the line's length, and, if there are more than 64, again to find the
-// place.
+// By every wave for itself (no barrier, no LDS): a lane has neighbouring
+// sequences.
 template <class S>
 __device__ __forceinline__ Run find_run(const AttnArgs& a, int me) {
   const int lane = threadIdx.x & (kWave - 1);
+  const int each = (a.kv.B + kWave - 1) / kWave;
   Run run;
-  run.total = 0;
-  int64_t tiles = 0;
-  int most = 0;
   Seq mine;
-  int64_t c = 0, upto = 0;
-  for (int base = 0; base < a.kv.B; base += kWave) {
-    const bool live = base + lane < a.kv.B;
-    mine = seq_of<S::kStep>(a, live ? base + lane : a.kv.B - 1);
-    c = live ? a.kv.Hkv * mine.head : 0;
-    upto = c;
-    int n = live ? mine.nq : 0, m = live ? mine.most : 0;
-    const int used = min(a.kv.B - base, kWave);
-    for (int d = 1; d < used; d <<= 1) {
-      const int64_t y = __shfl_up(upto, d, kWave);
-      if (lane >= d) upto += y;
-      n += __shfl_down(n, d, kWave);       // (lane 0 gets them all)
-      m = max(m, __shfl_down(m, d, kWave));
+  int64_t c = 0;
+  int n = 0, most = 0;
+  for (int i = 0; i < each; ++i) {
+    const int b = lane * each + i;
+    mine = seq_of<S::kStep>(a, min(b, a.kv.B - 1));
+    if (b < a.kv.B) {
+      c += a.kv.Hkv * mine.head;
+      n += mine.nq;
+      most = max(most, mine.most);
     }
-    run.total += lane_of(upto, used - 1);
-    tiles += int64_t(__builtin_amdgcn_readlane(n, 0)) * a.kv.Hkv;
-    most = max(most, __builtin_amdgcn_readlane(m, 0));
   }
+  int64_t upto = c;
+  for (int d = 1; d < kWave && d < a.kv.B; d <<= 1) {
+    const int64_t y = __shfl_up(upto, d, kWave);
+    if (lane >= d) upto += y;
+    n += __shfl_down(n, d, kWave);       // (lane 0 gets them all)
+    most = max(most, __shfl_down(most, d, kWave));
+  }
+  run.total = lane_of(upto, min(a.kv.B, kWave) - 1);
+  const int64_t tiles = int64_t(__builtin_amdgcn_readlane(n, 0)) * a.kv.Hkv;
+  most = __builtin_amdgcn_readlane(most, 0);
   run.length = quotient(run.total + a.grid - 1, a.grid);
   // A cut tile's parts cost about kCut steps each to leave and to join.  Cut
   // if the longest tile, or as many average ones as a workgroup gets, takes
@@ -273,28 +274,13 @@ __device__ __forceinline__ Run find_run(const AttnArgs& a, int me) {
   const int64_t x = me * run.length;
   run.b = 0, run.r = 0;
   if (x >= run.total) return run;
-  int64_t before = 0;
-  for (int base = 0; base < a.kv.B; base += kWave) {
-    if (__builtin_expect(a.kv.B > kWave, 0)) {
-      const bool live = base + lane < a.kv.B;
-      mine = seq_of<S::kStep>(a, live ? base + lane : a.kv.B - 1);
-      c = live ? a.kv.Hkv * mine.head : 0;
-      upto = c;
-      for (int d = 1; d < kWave; d <<= 1) {
-        const int64_t y = __shfl_up(upto, d, kWave);
-        if (lane >= d) upto += y;
-      }
-    }
-    const uint64_t behind = __ballot(x < before + upto);
-    if (behind) {
-      const int at = __builtin_ctzll(behind);
-      run.b = base + at;
-      run.r = x - before - lane_of(upto, at) + lane_of(c, at);
-      run.s = lane_of(mine, at);
-      break;
-    }
-    before += lane_of(upto, kWave - 1);
-  }
+  const int at = __builtin_ctzll(__ballot(x < upto));
+  run.b = at * each;
+  run.r = x - lane_of(upto, at) + lane_of(c, at);
+  if (each == 1)
+    run.s = lane_of(mine, at);
+  else
+    run.s = seq_of<S::kStep>(a, run.b);
   return run;
 }
 
@@ -336,13 +322,14 @@ __device__ __forceinline__ void store_row4(const AttnArgs& a, int64_t row, int h
 // ---- the kernel
 
 // PARTS: bf16 numbers that a weight is the sum of.
-template <int D_, bool F8_, int RW_, int KW_, int KS_, int NS_, int PARTS_>
+template <int D_, bool F8_, int RB_, int RW_, int KW_, int KS_, int NS_, int PARTS_>
 struct Shape {
-  static constexpr int D = D_, RW = RW_, KW = KW_, KS = KS_, NS = NS_;
+  static constexpr int D = D_, RB = RB_, RW = RW_, KW = KW_, KS = KS_, NS = NS_;
   static constexpr int kParts = PARTS_;
   static constexpr bool F8 = F8_;
   static constexpr int kWaves = RW * KW, kThreads = kWaves * kWave;
-  static constexpr int kRows = 32 * RW;
+  static constexpr int kRows = RB * RW;
+  static constexpr int kGroups = 64 / RB;                   // lanes of a row
   static constexpr int kStep = KW * KS;
   static constexpr int kPitch = D * (F8 ? 1 : 2);           // bytes of a position's row
   static constexpr int kChunks = kPitch / 16;
@@ -353,9 +340,9 @@ struct Shape {
   // columns of an epilogue's round (a wave's rows go through LDS)
   static constexpr int kCols = D < 128 || RW == 1 ? D : 128;
   static constexpr int kOutPitch = kCols + 4;               // (rows 4 banks apart)
-  static constexpr int kOut = kWaves * 32 * kOutPitch * 4;
+  static constexpr int kOut = kWaves * RB * kOutPitch * 4;
   static constexpr int kData = kRing + kScales > kOut ? kRing + kScales : kOut;
-  static constexpr int kLds = kData + kIds * 4 + kWaves * 32 * 8;
+  static constexpr int kLds = kData + kIds * 4 + kWaves * RB * 8;
   static constexpr int kPerCu = kMaxLds / (kLds + 256) >= 2 && kThreads <= 256 ? 2 : 1;
   static constexpr int kRowsAt = 64 / kChunks;              // positions of a 1 KiB load
   // In steps: what a cut costs each side (the tile's rows in fp32 out and in),
@@ -365,37 +352,85 @@ struct Shape {
   static_assert(kLds + 256 <= kMaxLds && (RW == 1 || NS >= 2) && (KS == 32 || KS == 64), "shape");
   static_assert(RW == 1 || 2 * kLoads % RW == 0, "loads");
 
-  // Permutations of a row's 16-byte chunks in LDS, so that what is read
-  // together meets no bank twice: keys, 16 rows of one chunk; values, 4 rows
-  // of 4 chunks (16 bits) or 8 of 2 (8 bits).
+  // Permutations of a row's 16-byte chunks in LDS (row parts of 256 bytes),
+  // so that what is read together meets no bank twice: keys, 16 rows of one
+  // chunk; values, with r0, r1 ... the bits of a row: in 16 bits 4 rows of 4
+  // chunks (32 query rows) or 8 of 2 (16), told apart by r0 r1 and r0 r1 r2; in
+  // 8 bits 8 rows of 2 chunks, by r0 r1 r3, or 16 of one, by r0 r1 r2 r4.  All
+  // are sums of bits: of a row's parts, the sum of theirs.
   static __device__ __forceinline__ int key_swizzle(int row) {
     return kPitch >= 256 ? row & 15 : kPitch == 128 ? (row >> 1) & 7 : (row >> 2) & 3;
   }
   static __device__ __forceinline__ int value_swizzle(int row) {
-    if (!F8) return kPitch >= 256 ? (row & 3) << 2 : ((row >> 1) & 1) << 2;
-    if (kPitch == 256) return ((row & 3) | ((row >> 1) & 4)) << 1;
-    if (kPitch == 128) return (((row >> 1) & 1) | ((row >> 2) & 2)) << 1;
-    return ((row >> 3) & 1) << 1;
+    const int r2 = (row >> 2) & 1;
+    if (!F8) return kPitch >= 256 ? (row & 3) << 2 | r2 << 1 : (row & 2) << 1 | r2 << 1;
+    const int r34 = ((row >> 3) ^ (row >> 4)) & 1;
+    if (kPitch == 256) return r34 << 3 | (row & 3) << 1 | r2;
+    if (kPitch == 128) return r34 << 2 | (row & 2) | r2;
+    return r34 << 1 | r2;
+  }
+};
+
+// One product of 16 or 32 rows, and what a lane holds of its result.
+template <int RB>
+struct Product;
+template <>
+struct Product<32> {
+  typedef f32x16 Acc;
+  static __device__ __forceinline__ Acc add(bf16x8 x, bf16x8 y, Acc c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, y, c, 0, 0, 0);
+  }
+  // Maximum (sum) over the lanes of a row.
+  static __device__ __forceinline__ float row_max(float v) {
+    const f32x2 h = both_halves(v);
+    return fmaxf(h[0], h[1]);
+  }
+  static __device__ __forceinline__ float row_sum(float v) {
+    const f32x2 h = both_halves(v);
+    return h[0] + h[1];
+  }
+};
+template <>
+struct Product<16> {
+  typedef f32x4 Acc;
+  static __device__ __forceinline__ Acc add(bf16x8 x, bf16x8 y, Acc c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, y, c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ float row_max(float v) {
+    v = fmaxf(v, __shfl_xor(v, 16, kWave));
+    return Product<32>::row_max(v);
+  }
+  static __device__ __forceinline__ float row_sum(float v) {
+    v += __shfl_xor(v, 16, kWave);
+    return Product<32>::row_sum(v);
   }
 };
 
 template <class S>
 __global__ __launch_bounds__(S::kThreads, S::kPerCu * S::kThreads / 256) void attention_kernel(const AttnArgs a) {
-  constexpr int D = S::D, RW = S::RW, KW = S::KW, KS = S::KS, NS = S::NS, STEP = S::kStep, NB = KS / 32;
+  constexpr int D = S::D, RB = S::RB, RW = S::RW, KW = S::KW, KS = S::KS, NS = S::NS, STEP = S::kStep;
+  // A product's inner length is KK: 16 columns of 32 rows or 32 of 16.  A lane's
+  // EACH results of a product are rows (positions, columns) place(e) of its RB.
+  constexpr int GROUPS = S::kGroups, KK = 8 * GROUPS, EACH = RB * RB / 64;
+  constexpr int NB = KS / RB, NP = KS / KK;       // products for a step's positions: scores, values
+  using P = Product<RB>;
+  auto place = [](int e) { return e / 4 * (4 * GROUPS) + e % 4; };     // (and 4 times the lane's group)
   constexpr int PARTS = S::kParts;
   constexpr bool F8 = S::F8;
   constexpr int AHEAD = S::kAhead;
-  using KeyPart = std::conditional_t<F8, i32x2, bf16x8>;       // 8 columns (or positions) as they lie in LDS
-  using ValuePart = KeyPart;
+  // Operands as they lie in LDS: 16 bytes of a key row (8-bit: two products'),
+  // 8 positions of a value column.
+  using KeyPart = std::conditional_t<F8, i32x4, bf16x8>;
+  using ValuePart = std::conditional_t<F8, i32x2, bf16x8>;
   constexpr int PITCH = S::kPitch, BANKS = PITCH < 256 ? PITCH : 256;   // (a row's part that chunks are permuted in)
   extern __shared__ __align__(256) uint8_t smem[];
   MOE_LDS uint8_t* const lds = (MOE_LDS uint8_t*)smem;
   int32_t* const ids = reinterpret_cast<int32_t*>(smem + S::kData);
-  f32x2* const stats = reinterpret_cast<f32x2*>(smem + S::kData + kIds * 4);   // [waves][32]: maximum, sum
+  f32x2* const stats = reinterpret_cast<f32x2*>(smem + S::kData + kIds * 4);   // [waves][RB]: maximum, sum
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int kw = wave / RW, rw = wave % RW;
-  const int col = lane & 31, half = lane >> 5;
+  const int col = lane % RB, part_of_row = lane / RB;
   // (heads of 256 leave no registers for what a step derives from it)
   auto lane_at = [&] { return D == 256 ? lane_now() : lane; };
   // neighbouring runs on one XCD (workgroups go to the 8 in turn): they share keys and values
@@ -413,8 +448,8 @@ __global__ __launch_bounds__(S::kThreads, S::kPerCu * S::kThreads / 256) void at
 
   while (x < x1) {
     if (r >= a.kv.Hkv * s.head) {
-      ++b, r = 0;
-      s = seq_of<STEP>(a, b);
+      r -= a.kv.Hkv * s.head;
+      s = seq_of<STEP>(a, ++b);
       continue;
     }
     // which tile, and from which of its steps
@@ -472,35 +507,37 @@ __global__ __launch_bounds__(S::kThreads, S::kPerCu * S::kThreads / 256) void at
     x += take, r += take;
 
     // ---- the tile's queries: this wave's 32 rows, as the products' right operand
-    const int lr = rw * 32 + col;                       // this lane's row of the tile
+    const int lr = rw * RB + col;                       // this lane's row of the tile
     const int token = a.token_of(lr);
     const bool live = token < nt;
     const int rpos = live ? s.off + t0 + token : -1;    // the last position it sees
     const int rfirst = a.window ? max(rpos - (a.window - 1), 0) : 0;
-    bf16x8 q[D / 16];
+    bf16x8 q[D / KK];
     {
       const uint16_t* qp = a.q + int64_t(s.row0 + t0 + (live ? token : 0)) * a.q_stride +
-                           int64_t(h * a.G + (lr - token * a.G)) * D + half * 8;
+                           int64_t(h * a.G + (lr - token * a.G)) * D + part_of_row * (F8 ? 16 : 8);
+      // (8-bit keys: a lane's 16 columns are two products')
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
+      for (int i = 0; i < D / KK; ++i) {
         u32x4 v = {0u, 0u, 0u, 0u};
-        if (live) v = *reinterpret_cast<const u32x4_any*>(qp + i * 16);
+        const int c = F8 ? i / 2 * (2 * KK) + i % 2 * 8 : i * KK;
+        if (live) v = *reinterpret_cast<const u32x4_any*>(qp + c);
         q[i] = __builtin_bit_cast(bf16x8, v);
       }
     }
     // what every row of this wave sees, and what any does
-    const int wave_t1 = min(nt - 1, a.token_of(rw * 32 + 31)), wave_t0 = min(a.token_of(rw * 32), nt - 1);
-    const bool wave_live = a.token_of(rw * 32) < nt;
+    const int wave_t1 = min(nt - 1, a.token_of(rw * RB + RB - 1)), wave_t0 = min(a.token_of(rw * RB), nt - 1);
+    const bool wave_live = a.token_of(rw * RB) < nt;
     const int sees_all = s.off + t0 + wave_t0;                                    // up to here
     const int sees_any = wave_live ? s.off + t0 + wave_t1 : -1;
     const int from_all = a.window ? s.off + t0 + wave_t1 - (a.window - 1) : 0;     // from here
     const int from_any = a.window ? s.off + t0 + wave_t0 - (a.window - 1) : 0;
 
-    f32x16 o[D / 32];
+    typename P::Acc o[D / RB];
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i)
+    for (int i = 0; i < D / RB; ++i)
 #pragma unroll
-      for (int j = 0; j < 16; ++j) o[i][j] = 0.0f;
+      for (int j = 0; j < EACH; ++j) o[i][j] = 0.0f;
     float mref = -INFINITY, sum = 0.0f, lost = 0.0f;     // (what the sum's roundings lost)
 
     // ---- the positions, as far as the page numbers held in LDS reach
@@ -630,67 +667,91 @@ __global__ __launch_bounds__(S::kThreads, S::kPerCu * S::kThreads / 256) void at
         MOE_LDS uint8_t* const vl = slot_lds(i % NS, true);
 
         // which of the positions are there
-        uint32_t there[NB];
+        const int l = lane_at(), col = l % RB, group = l / RB;
+        uint32_t there[KS / 32];
         bool all = true;
-        const int l = lane_at(), col = l & 31, half = l >> 5;
 #pragma unroll
-        for (int n = 0; n < NB; ++n) {
-          there[n] = uint32_t(__ballot(page_of(pos0 + n * 32 + col) >= 0));
+        for (int n = 0; n < KS / 32; ++n) {
+          there[n] = uint32_t(__ballot(page_of(pos0 + n * 32 + (l & 31)) >= 0));
           all = all && there[n] == 0xFFFFFFFFu;
         }
         const bool any = pos0 <= sees_any && pos0 + KS > from_any;
-        f32x16 sc[NB];
+        typename P::Acc sc[NB];
         if (any) {
           // chunk c of a row lies at c ^ key_swizzle(row): with the lane's part
           // of c in the address, the rest of it is an exclusive or (below 256
-          // bytes) and an offset; 32 rows further the permutation is the same
-          uint32_t at = uint32_t(reinterpret_cast<uintptr_t>(kl)) + col * PITCH +
-                        (F8 ? S::key_swizzle(col) * 16 + half * 8 : (S::key_swizzle(col) ^ half) * 16);
-          constexpr int COUNT = NB * D / 16;
+          // bytes) and an offset; RB rows further the permutation is the same
+          // or differs by key_swizzle(RB)
+          const uint32_t at = uint32_t(reinterpret_cast<uintptr_t>(kl)) + col * PITCH +
+                              (S::key_swizzle(col) ^ group) * 16;
+          constexpr int ROW = D / KK / (F8 ? 2 : 1), COUNT = NB * ROW;      // reads
           auto read = [&](int u) {
-            constexpr int UNIT = F8 ? 16 : 32;
-            const int n = u / (D / 16), k = u % (D / 16);
-            const uint32_t from = (at ^ (k * UNIT % BANKS)) + k * UNIT / BANKS * BANKS + n * 32 * PITCH;
-            return *(MOE_LDS KeyPart*)(uintptr_t)from;
+            const int n = u / ROW, k = u % ROW;
+            const uint32_t x = k * 16 * GROUPS ^ (S::key_swizzle(n * RB) * 16);
+            return *(MOE_LDS KeyPart*)(uintptr_t)((at ^ (x % BANKS)) + x / BANKS * BANKS + n * RB * PITCH);
           };
           KeyPart part[AHEAD];
 #pragma unroll
           for (int u = 0; u < AHEAD && u < COUNT; ++u) part[u] = read(u);
-          bf16x8 kf = operand(part[0]);
-          in_order();
-#pragma unroll
-          for (int u = 0; u < COUNT; ++u) {
-            const int n = u / (D / 16), k = u % (D / 16);
-            if (k == 0) {
-#pragma unroll
-              for (int j = 0; j < 16; ++j) sc[n][j] = 0.0f;
-            }
-            const bf16x8 now = kf;
-            if (u + AHEAD < COUNT) part[u % AHEAD] = read(u + AHEAD);
-            sc[n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(now, q[k], sc[n], 0, 0, 0);
-            if (u + 1 < COUNT) kf = operand(part[(u + 1) % AHEAD]);
+          if constexpr (F8) {
+            bf16x8 lo = from_codes(i32x2{part[0][0], part[0][1]}), hi;
             in_order();
+#pragma unroll
+            for (int u = 0; u < COUNT; ++u) {
+              const int n = u / ROW, k = u % ROW * 2;
+              if (k == 0) {
+#pragma unroll
+                for (int j = 0; j < EACH; ++j) sc[n][j] = 0.0f;
+              }
+              const KeyPart now = part[u % AHEAD];
+              if (u + AHEAD < COUNT) part[u % AHEAD] = read(u + AHEAD);
+              sc[n] = P::add(lo, q[k], sc[n]);
+              hi = from_codes(i32x2{now[2], now[3]});
+              in_order();
+              sc[n] = P::add(hi, q[k + 1], sc[n]);
+              if (u + 1 < COUNT) lo = from_codes(i32x2{part[(u + 1) % AHEAD][0], part[(u + 1) % AHEAD][1]});
+              in_order();
+            }
+          } else {
+            in_order();
+#pragma unroll
+            for (int u = 0; u < COUNT; ++u) {
+              const int n = u / ROW, k = u % ROW;
+              if (k == 0) {
+#pragma unroll
+                for (int j = 0; j < EACH; ++j) sc[n][j] = 0.0f;
+              }
+              const KeyPart now = part[u % AHEAD];
+              if (u + AHEAD < COUNT) part[u % AHEAD] = read(u + AHEAD);
+              sc[n] = P::add(now, q[k], sc[n]);
+              in_order();
+            }
           }
           if (F8) {
 #pragma unroll
             for (int n = 0; n < NB; ++n)
 #pragma unroll
-              for (int g = 0; g < 4; ++g) {
-                const f32x4 w = *(MOE_LDS f32x4*)(scales_of(i, false) + (n * 32 + 8 * g + 4 * half) * 4);
+              for (int g = 0; g < EACH / 4; ++g) {
+                const f32x4 w = *(MOE_LDS f32x4*)(scales_of(i, false) + (n * RB + place(4 * g) + 4 * group) * 4);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) sc[n][4 * g + e] *= w[e];
               }
           }
           if (!all || pos0 + KS - 1 > sees_all || pos0 < from_all) {
 #pragma unroll
-            for (int n = 0; n < NB; ++n) {
+            for (int n = 0; n < KS / 32; ++n) {
               // a bit for each of the 32 positions that this lane's row sees
               const int last = rpos - pos0 - n * 32, first = rfirst - pos0 - n * 32;
               uint32_t sees = last >= 31 ? ~0u : last < 0 ? 0u : (2u << last) - 1u;
               sees &= first <= 0 ? ~0u : first > 31 ? 0u : ~0u << first;
-              sees = (sees & there[n]) >> (4 * half);
+              sees = (sees & there[n]) >> (4 * group);
 #pragma unroll
-              for (int j = 0; j < 16; ++j) sc[n][j] = sees & (1u << (8 * (j / 4) + j % 4)) ? sc[n][j] : -INFINITY;
+              for (int m = 0; m < 32 / RB; ++m)
+#pragma unroll
+                for (int j = 0; j < EACH; ++j) {
+                  const int k = n * (32 / RB) + m;
+                  sc[k][j] = sees & (1u << (m * RB + place(j))) ? sc[k][j] : -INFINITY;
+                }
             }
           }
         }
@@ -698,62 +759,56 @@ __global__ __launch_bounds__(S::kThreads, S::kPerCu * S::kThreads / 256) void at
           wait_reads();
           if (i + NS < count) load_own(i + NS, false);
         }
-        bf16x8 p[PARTS][NB * 2];
+        bf16x8 p[PARTS][NP];
         if (any) {
           float top = sc[0][0];
 #pragma unroll
           for (int n = 0; n < NB; ++n)
 #pragma unroll
-            for (int j = 0; j < 16; ++j) top = fmaxf(top, sc[n][j]);
-          const f32x2 tops = both_halves(top);
-          top = fmaxf(tops[0], tops[1]) * a.scale2;
+            for (int j = 0; j < EACH; ++j) top = fmaxf(top, sc[n][j]);
+          top = P::row_max(top) * a.scale2;
           if (__ballot(top > mref + kRaise)) {
             const float m = fmaxf(mref, top);
             const float f = m == -INFINITY ? 1.0f : exp2_fast(mref - m);
             sum *= f, lost *= f;
 #pragma unroll
-            for (int n = 0; n < D / 32; ++n)
+            for (int n = 0; n < D / RB; ++n)
 #pragma unroll
-              for (int j = 0; j < 16; ++j) o[n][j] *= f;
+              for (int j = 0; j < EACH; ++j) o[n][j] *= f;
             mref = m;
           }
           const float m = mref == -INFINITY ? 0.0f : mref;
           float add = 0.0f;
+          // eight weights at a time: a product's operand
 #pragma unroll
-          for (int n = 0; n < NB; ++n) {
-            float w[16];
+          for (int n = 0; n < NP; ++n) {
+            float w[8];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) w[j] = exp2_fast(fmaf(sc[n][j], a.scale2, -m));
-            if (F8 || PARTS > 1) {
-              // (four sums side by side)
-              f32x4 s = {w[0], w[1], w[2], w[3]};
-#pragma unroll
-              for (int j = 4; j < 16; ++j) s[j % 4] += w[j];
-              add += (s[0] + s[1]) + (s[2] + s[3]);
+            for (int j = 0; j < 8; ++j) {
+              const int e = n * 8 + j;
+              w[j] = exp2_fast(fmaf(sc[e / EACH][e % EACH], a.scale2, -m));
             }
+            if (F8 || PARTS > 1) add += ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
             if (F8) {
 #pragma unroll
-              for (int g = 0; g < 4; ++g) {
+              for (int g = 0; g < 2; ++g) {
                 const f32x4 v = *(MOE_LDS f32x4*)(scales_of(i, KS != 32) +
-                                                  ((KS == 32 ? 32 : 0) + n * 32 + 8 * g + 4 * half) * 4);
+                                                  ((KS == 32 ? 32 : 0) + n * KK + place(4 * g) + 4 * group) * 4);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) w[4 * g + e] *= v[e];
               }
             }
 #pragma unroll
             for (int k = 0; k < PARTS; ++k) {
+              u32x4 c;
 #pragma unroll
-              for (int g = 0; g < 2; ++g) {
-                u32x4 c;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  float* const x = w + 8 * g + 2 * e;
-                  c[e] = pack2(x[0], x[1]);
-                  if (!F8 && PARTS == 1) add = dot2_bf16(c[e], 0x3F803F80u, add);
-                  x[0] -= __uint_as_float(c[e] << 16), x[1] -= __uint_as_float(c[e] & 0xFFFF0000u);
-                }
-                p[k][2 * n + g] = __builtin_bit_cast(bf16x8, c);
+              for (int e = 0; e < 4; ++e) {
+                float* const x = w + 2 * e;
+                c[e] = pack2(x[0], x[1]);
+                if (!F8 && PARTS == 1) add = dot2_bf16(c[e], 0x3F803F80u, add);
+                x[0] -= __uint_as_float(c[e] << 16), x[1] -= __uint_as_float(c[e] & 0xFFFF0000u);
               }
+              p[k][n] = __builtin_bit_cast(bf16x8, c);
             }
           }
           // a sum over a long text keeps what is small next to it
@@ -769,45 +824,46 @@ __global__ __launch_bounds__(S::kThreads, S::kPerCu * S::kThreads / 256) void at
             wait_loads<0>();
         }
         if (any) {
-          // lanes of 16 give the rows that the transposing read takes: 4 rows of 16
+          // 16 lanes give the rows that the transposing read takes: 4 rows of 16
           // columns (16 bits), 8 of 16 (8 bits); the permutation as for keys
-          constexpr int VCOUNT = NB * 2 * D / 32;
-          uint32_t vat;
-          {
-            const int li = l & 15, cols16 = (l >> 4) & 1;
-            const int row = F8 ? 8 * (li >> 3) + 4 * half + ((li >> 1) & 3) : 4 * half + (li >> 2);
-            const int chunk = F8 ? cols16 : 2 * cols16 + ((li & 3) >> 1);
-            vat = uint32_t(reinterpret_cast<uintptr_t>(vl)) + row * PITCH + (chunk ^ S::value_swizzle(row)) * 16 +
-                  (li & 1) * 8;
-          }
-          auto value_part = [&](int u) {
-            constexpr int UNIT = F8 ? 32 : 64;
-            const int n = u / (D / 32), d = u % (D / 32);
-            const uint32_t from = (vat ^ (d * UNIT % BANKS)) + d * UNIT / BANKS * BANKS + n * 16 * PITCH;
+          const int li = l & 15, cols16 = RB == 32 ? (l >> 4) & 1 : 0;
+          const int row = 4 * group + (F8 ? (li >> 3) * (4 * GROUPS) + ((li >> 1) & 3) : li >> 2);
+          const int chunk = F8 ? cols16 : 2 * cols16 + ((li & 3) >> 1);
+          const uint32_t at = uint32_t(reinterpret_cast<uintptr_t>(vl)) + row * PITCH +
+                              (chunk ^ S::value_swizzle(row)) * 16 + (li & 1) * 8;
+          constexpr int COLS = D / RB, COUNT = NP * COLS;
+          auto read = [&](int u) {
+            constexpr int UNIT = F8 ? RB : 2 * RB;
+            const int n = u / COLS;
+            const uint32_t x = u % COLS * UNIT;
+            auto from = [&](int r) {       // r rows further
+              const uint32_t y = x ^ (S::value_swizzle(r) * 16);
+              return (at ^ (y % BANKS)) + y / BANKS * BANKS + r * PITCH;
+            };
             ValuePart v;
             if constexpr (F8) {
-              v = __builtin_amdgcn_ds_read_tr8_b64_v2i32((MOE_LDS i32x2*)(uintptr_t)from);
+              v = __builtin_amdgcn_ds_read_tr8_b64_v2i32((MOE_LDS i32x2*)(uintptr_t)from(n * KK));
             } else {
-              const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MOE_LDS s16x4*)(uintptr_t)from);
-              const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MOE_LDS s16x4*)(uintptr_t)(from + 8 * PITCH));
+              const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MOE_LDS s16x4*)(uintptr_t)from(n * KK));
+              const s16x4 hi =
+                  __builtin_amdgcn_ds_read_tr16_b64_v4i16((MOE_LDS s16x4*)(uintptr_t)from(n * KK + 4 * GROUPS));
               v = __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
             }
             return v;
           };
-          ValuePart vpart[AHEAD];
+          ValuePart part[AHEAD];
 #pragma unroll
-            for (int u = 0; u < AHEAD && u < VCOUNT; ++u) vpart[u] = value_part(u);
-          bf16x8 vf = operand(vpart[0]);
+          for (int u = 0; u < AHEAD && u < COUNT; ++u) part[u] = read(u);
+          bf16x8 vf = operand(part[0]);
           in_order();
 #pragma unroll
-          for (int u = 0; u < VCOUNT; ++u) {
-            const int n = u / (D / 32), d = u % (D / 32);
+          for (int u = 0; u < COUNT; ++u) {
+            const int n = u / COLS, d = u % COLS;
             const bf16x8 now = vf;
-            if (u + AHEAD < VCOUNT) vpart[u % AHEAD] = value_part(u + AHEAD);
+            if (u + AHEAD < COUNT) part[u % AHEAD] = read(u + AHEAD);
 #pragma unroll
-            for (int k = PARTS - 1; k >= 0; --k)
-              o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(now, p[k][n], o[d], 0, 0, 0);
-            if (u + 1 < VCOUNT) vf = operand(vpart[(u + 1) % AHEAD]);
+            for (int k = PARTS - 1; k >= 0; --k) o[d] = P::add(now, p[k][n], o[d]);
+            if (u + 1 < COUNT) vf = operand(part[(u + 1) % AHEAD]);
             in_order();
           }
         }
@@ -819,19 +875,16 @@ __global__ __launch_bounds__(S::kThreads, S::kPerCu * S::kThreads / 256) void at
     }
 
     // ---- the tile's end: rows through LDS, 128 columns at a time
-    {
-      const f32x2 sums = both_halves(sum);
-      sum = sums[0] + sums[1];
-    }
+    sum = P::row_sum(sum);
     barrier_lds();         // the steps' LDS has been used up
     float m = mref;
     float f = 1.0f;
     if constexpr (KW > 1) {
-      if (half == 0) stats[wave * 32 + col] = f32x2{mref, sum};
+      if (part_of_row == 0) stats[wave * RB + col] = f32x2{mref, sum};
       barrier_lds();
       f32x2 st[KW];
 #pragma unroll
-      for (int k = 0; k < KW; ++k) st[k] = stats[(k * RW + rw) * 32 + col], m = fmaxf(m, st[k][0]);
+      for (int k = 0; k < KW; ++k) st[k] = stats[(k * RW + rw) * RB + col], m = fmaxf(m, st[k][0]);
       sum = 0.0f;
 #pragma unroll
       for (int k = 0; k < KW; ++k) sum += m == -INFINITY ? 0.0f : st[k][1] * exp2_fast(st[k][0] - m);
@@ -840,32 +893,32 @@ __global__ __launch_bounds__(S::kThreads, S::kPerCu * S::kThreads / 256) void at
     float* const part = a.parts + int64_t(slot) * S::kRows * (D + 2);
     if (whole)
       f = sum > 0.0f ? f / sum : 0.0f;
-    else if (kw == 0 && half == 0)
+    else if (kw == 0 && part_of_row == 0)
       *reinterpret_cast<f32x2*>(part + S::kRows * D + lr * 2) = f32x2{m, sum};
-    float* const mine_out = reinterpret_cast<float*>(smem) + wave * 32 * S::kOutPitch;
+    float* const mine_out = reinterpret_cast<float*>(smem) + wave * RB * S::kOutPitch;
     constexpr int kLanes = S::kCols / 4, kRowsAt = 64 / kLanes;     // lanes of a row, rows at a time
 #pragma unroll
     for (int c0 = 0; c0 < D; c0 += S::kCols) {
 #pragma unroll
-      for (int d = 0; d < S::kCols / 32; ++d)
+      for (int d = 0; d < S::kCols / RB; ++d)
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
+        for (int g = 0; g < EACH / 4; ++g) {
           f32x4 v;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = o[c0 / 32 + d][4 * g + e] * f;
-          *reinterpret_cast<f32x4*>(mine_out + col * S::kOutPitch + d * 32 + 8 * g + 4 * half) = v;
+          for (int e = 0; e < 4; ++e) v[e] = o[c0 / RB + d][4 * g + e] * f;
+          *reinterpret_cast<f32x4*>(mine_out + col * S::kOutPitch + d * RB + place(4 * g) + 4 * part_of_row) = v;
         }
       barrier_lds();
-      // the KW waves of these rows take 32 / KW of them each
+      // the KW waves of these rows take RB / KW of them each
 #pragma unroll 1
-      for (int i = 0; i < 32 / KW; i += kRowsAt) {
-        const int row = kw * (32 / KW) + i + lane / kLanes, c = (lane % kLanes) * 4;
+      for (int i = 0; i < RB / KW; i += kRowsAt) {
+        const int row = kw * (RB / KW) + i + lane / kLanes, c = (lane % kLanes) * 4;
         f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int k = 0; k < KW; ++k)
           v += *reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(smem) +
-                                               ((k * RW + rw) * 32 + row) * S::kOutPitch + c);
-        const int tr = rw * 32 + row, tk = a.token_of(tr);
+                                               ((k * RW + rw) * RB + row) * S::kOutPitch + c);
+        const int tr = rw * RB + row, tk = a.token_of(tr);
         if (whole) {
           if (tk < nt) store_row4(a, s.row0 + t0 + tk, h * a.G + tr - tk * a.G, D, c0 + c, v);
         } else {
@@ -999,7 +1052,7 @@ hipError_t allow_lds(Kernel kernel, int64_t bytes) {
 }
 
 // Rows of a tile for so many rows per sequence.
-int rows_for(int64_t rows) { return rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256; }
+int rows_for(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256; }
 
 constexpr size_t kJointBytes = kMaxGrid * (sizeof(int32_t) + sizeof(Joint));
 
@@ -1034,14 +1087,16 @@ hipError_t launch(const AttnArgs& a, hipStream_t st) {
   constexpr int NS = D == 256 && !F8 ? 1 : 2, KS = D == 256 ? 32 : 64;
   const int64_t tokens = (int64_t(a.T) + a.kv.B - 1) / a.kv.B;
   switch (rows_for(tokens * a.G)) {
+    case 16:
+      return launch_shape<Shape<D, F8, 16, 1, 4, 32, NS, 3>>(a, st);
     case 32:
-      return launch_shape<Shape<D, F8, 1, 4, 32, NS, 3>>(a, st);
+      return launch_shape<Shape<D, F8, 32, 1, 4, 32, NS, 3>>(a, st);
     case 64:
-      return launch_shape<Shape<D, F8, 2, 2, 32, 2, PARTS>>(a, st);
+      return launch_shape<Shape<D, F8, 32, 2, 2, 32, 2, PARTS>>(a, st);
     case 128:
-      return launch_shape<Shape<D, F8, 4, 1, KS, 2, PARTS>>(a, st);
+      return launch_shape<Shape<D, F8, 32, 4, 1, KS, 2, PARTS>>(a, st);
     default:
-      return launch_shape<Shape<D, F8, 8, 1, KS, 2, PARTS>>(a, st);
+      return launch_shape<Shape<D, F8, 32, 8, 1, KS, 2, PARTS>>(a, st);
   }
 }
 
@@ -1051,7 +1106,7 @@ size_t attention_ws(int T, int Hq, int Hkv, int D) {
   // (whatever B is: the tiles are no larger than one sequence's rows need)
   const int rows = rows_for(int64_t(T > 0 ? T : 1) * (Hq / Hkv));
   size_t most = 0;
-  for (int r = 32; r <= rows; r *= 2)
+  for (int r = 16; r <= rows; r *= 2)
     if (parts_bytes(r, D) > most) most = parts_bytes(r, D);
   return kJointBytes + most;
 }
