@@ -660,7 +660,6 @@ __global__ __launch_bounds__(S::kThreads, S::kPerCu * S::kThreads / 256) void at
           else
             wait_loads<0>();
           barrier_lds();
-          if (i + NS - 1 < count) load_shared(i + NS - 1);
         }
         const int pos0 = (step0 + i) * STEP + kw * KS;      // this group's positions
         MOE_LDS uint8_t* const kl = slot_lds(i % NS, false);
@@ -685,6 +684,7 @@ __global__ __launch_bounds__(S::kThreads, S::kPerCu * S::kThreads / 256) void at
           const uint32_t at = uint32_t(reinterpret_cast<uintptr_t>(kl)) + col * PITCH +
                               (S::key_swizzle(col) ^ group) * 16;
           constexpr int ROW = D / KK / (F8 ? 2 : 1), COUNT = NB * ROW;      // reads
+          __builtin_amdgcn_s_setprio(1);
           auto read = [&](int u) {
             const int n = u / ROW, k = u % ROW;
             const uint32_t x = k * 16 * GROUPS ^ (S::key_swizzle(n * RB) * 16);
@@ -758,9 +758,12 @@ __global__ __launch_bounds__(S::kThreads, S::kPerCu * S::kThreads / 256) void at
         if constexpr (RW == 1) {
           wait_reads();
           if (i + NS < count) load_own(i + NS, false);
+        } else if (i + NS - 1 < count) {
+          load_shared(i + NS - 1);      // (not where all waves leave the barrier together)
         }
         bf16x8 p[PARTS][NP];
         if (any) {
+          __builtin_amdgcn_s_setprio(0);
           float top = sc[0][0];
 #pragma unroll
           for (int n = 0; n < NB; ++n)
@@ -832,6 +835,7 @@ __global__ __launch_bounds__(S::kThreads, S::kPerCu * S::kThreads / 256) void at
           const uint32_t at = uint32_t(reinterpret_cast<uintptr_t>(vl)) + row * PITCH +
                               (chunk ^ S::value_swizzle(row)) * 16 + (li & 1) * 8;
           constexpr int COLS = D / RB, COUNT = NP * COLS;
+          __builtin_amdgcn_s_setprio(1);
           auto read = [&](int u) {
             constexpr int UNIT = F8 ? RB : 2 * RB;
             const int n = u / COLS;
@@ -1086,7 +1090,19 @@ hipError_t launch(const AttnArgs& a, hipStream_t st) {
   // (an 8-bit cache needs half the LDS)
   constexpr int NS = D == 256 && !F8 ? 1 : 2, KS = D == 256 ? 32 : 64;
   const int64_t tokens = (int64_t(a.T) + a.kv.B - 1) / a.kv.B;
-  switch (rows_for(tokens * a.G)) {
+  // Tall tiles multiply at twice the rate of those of 64 rows, but cutting them
+  // moves rows * D * 4 bytes per workgroup out and in again: only for steps of
+  // many products (as far as the host can tell: the tables may be wider than
+  // the texts are long).  512 tokens from the start, 16 heads of 256: 35 us with
+  // 64 rows, 75 with 256; 64 tokens at 8000: 47, 66; 525 tokens at 7001, 15 heads
+  // of 64: 61, 128 rows 53, 256 60; 2428 tokens, windows of 1024, 20 heads of 128:
+  // 78, 59, 57.
+  const int64_t cap = int64_t(a.kv.max_pages) << a.kv.page_shift;
+  const int64_t seen = a.window && a.window < cap ? a.window : cap;
+  const double work = double(a.T) * a.Hq * double(seen) * D;
+  const int64_t tallest = work < 2.5e9 ? 64 : work < 5e9 ? 128 : 256;
+  const int64_t rows = tokens * a.G < tallest ? tokens * a.G : tallest > a.G ? tallest : a.G;
+  switch (rows_for(rows)) {
     case 16:
       return launch_shape<Shape<D, F8, 16, 1, 4, 32, NS, 3>>(a, st);
     case 32:
