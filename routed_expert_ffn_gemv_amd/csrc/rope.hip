@@ -10,12 +10,16 @@
 // Angles: position * freq in 64 bits, less its whole turns, so that a far
 // position loses nothing; the rest of a turn goes to fp32 sines.
 //
-// One workgroup per token (for few tokens per part of a token's rows): a lane
-// holds 8 columns, D / 8 lanes a row, 256 threads 8 to 32 rows at a time.  The
-// token's cosines and sines are computed once, by one thread per pair, and
-// kept in registers for all rows, as a lane's columns are always the same.
-// A column's partner is read from LDS, where column c lies at (c % 8) * lanes
-// + c / 8: neighbouring lanes then read neighbouring words whatever R is.
+// A lane holds 8 columns, D / 8 lanes a row, 256 threads 8 to 32 rows at a
+// time.  For many tokens a workgroup takes four, whose sequences, positions and
+// sines its four waves find side by side before any row is touched (that
+// chain of loads takes longer than a token's rows: 32,768 tokens of 16 + 2 x 2
+// heads of 256 took 188 us with a token per workgroup, 164
+// so: a thread has three rows of the next under way); for few tokens a
+// workgroup takes a part of one's rows.  A token's cosines and sines stay in
+// registers for all its rows, as a lane's columns are always the same.  A
+// column's partner is read from LDS, where column c lies at (c % 8) * lanes + c /
+// 8: neighbouring lanes then read neighbouring words whatever R is.
 
 #include <hip/hip_runtime.h>
 
@@ -50,6 +54,33 @@ __device__ __forceinline__ void load8(const void* p, int fmt, int64_t i, float* 
     }
   }
 }
+
+// Eight columns as they lie in memory.
+template <int FMT>
+struct Raw {
+  u32x4 words[FMT == MOE_W_F32 ? 2 : 1];
+  __device__ __forceinline__ void load(const void* p, int64_t i) {
+    if (FMT == MOE_W_F32) {
+      const f32x4_any* q = reinterpret_cast<const f32x4_any*>(static_cast<const float*>(p) + i);
+      words[0] = __builtin_bit_cast(u32x4, f32x4(q[0]));
+      words[FMT == MOE_W_F32] = __builtin_bit_cast(u32x4, f32x4(q[1]));
+    } else {
+      words[0] = *reinterpret_cast<const u32x4_any*>(static_cast<const uint16_t*>(p) + i);
+    }
+  }
+  __device__ __forceinline__ void values(float* v) const {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (FMT == MOE_W_F32) {
+        v[j] = __uint_as_float(words[0][j]);
+        v[4 + j] = __uint_as_float(words[FMT == MOE_W_F32][j]);
+      } else {
+        v[2 * j] = __uint_as_float(words[0][j] << 16);
+        v[2 * j + 1] = __uint_as_float(words[0][j] & 0xFFFF0000u);
+      }
+    }
+  }
+};
 
 __device__ __forceinline__ u32x4 pack8(const float* v) {
   u32x4 r;
@@ -87,142 +118,194 @@ __device__ __forceinline__ int sequence_of(const int32_t* q_off, int B, int t) {
   return lo;
 }
 
-template <int D>
+// Where a token's keys and values go.
+struct Place {
+  int page;            // -1: nowhere
+  int slot;
+  bool live;           // of some sequence
+};
+
+// TOKENS: 1 (all waves look it up) or one per wave.
+template <int D, int TOKENS, int FMT>
 __global__ __launch_bounds__(kThreads) void rope_kernel(const RopeArgs a) {
-  constexpr int LPR = D / 8, ROWS = kThreads / LPR;
-  __shared__ f32x2 turn[D / 2];
+  constexpr int LPR = D / 8, ROWS = kThreads / LPR, AHEAD = 3;
+  __shared__ f32x2 turn[TOKENS][D / 2];
+  __shared__ Place places[TOKENS];
   __shared__ float part[kThreads * 8];
-  const int t = blockIdx.x;
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+  const int t0 = blockIdx.x * TOKENS, tokens = min(TOKENS, a.T - t0);
   const int sub = threadIdx.x % LPR, row0 = blockIdx.y * ROWS + threadIdx.x / LPR;
   const int step = gridDim.y * ROWS;
   const int rows = a.Hq + 2 * a.kv.Hkv;
-  const int64_t base = int64_t(t) * a.stride + sub * 8;
-
-  float next[8];
-  if (row0 < rows) load8(a.qkv, a.fmt, base + int64_t(row0) * D, next);
-
-  const int b = __builtin_amdgcn_readfirstlane(sequence_of(a.kv.q_off, a.kv.B, t));
-  if (b >= a.kv.B) return;
-  const int first = a.kv.q_off[b], end = a.kv.q_off[b + 1];
-  if (t < first || t >= end) return;
-  // (64 bits: the three numbers are the caller's)
-  const int64_t pos = int64_t(a.kv.kv_len[b]) - end + t;
-  int64_t place = -1;                    // the position's index among all pages' slots
-  int page = -1;
-  if (pos >= 0 && pos < (int64_t(a.kv.max_pages) << a.kv.page_shift)) {
-    page = a.kv.page_table[b * a.kv.table_stride + (pos >> a.kv.page_shift)];
-    if (page < 0 || page >= a.kv.num_pages) page = -1;
-  }
-  const int slot = int(pos & ((1 << a.kv.page_shift) - 1));
-  if (page >= 0) place = (int64_t(page) << a.kv.page_shift) + slot;
-
   const int half = a.R / 2;
-  if (threadIdx.x < half) {
-    const double turns = double(pos) * a.freq[threadIdx.x] * 0.15915494309189533577;   // 1 / (2 pi)
-    float s, c;
-    sincospif(2.0f * float(turns - rint(turns)), &s, &c);
-    turn[threadIdx.x] = f32x2{c * a.rot_scale, s * a.rot_scale};
-  }
-  __syncthreads();
-  // column sub * 8 + j becomes v * co + partner * si
-  float co[8], si[8];
+
+  // a thread's next three rows, as they are
+  Raw<FMT> now[AHEAD], next[AHEAD];
+  auto fetch = [&](int tok, int r, Raw<FMT>* to) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int c = sub * 8 + j;
-    co[j] = 1.0f, si[j] = 0.0f;
-    if (c < a.R) {
-      const int p = a.interleaved ? c >> 1 : c < half ? c : c - half;
-      const bool one = a.interleaved ? !(c & 1) : c < half;
-      co[j] = turn[p][0];
-      si[j] = one ? -turn[p][1] : turn[p][1];
+    for (int k = 0; k < AHEAD; ++k)
+      if (tok < tokens && r + k * step < rows)
+        to[k].load(a.qkv, int64_t(t0 + tok) * a.stride + (r + k * step) * D + sub * 8);
+  };
+  fetch(0, row0, next);
+
+  {
+    const int tok = TOKENS == 1 ? 0 : wave, t = t0 + tok;
+    const int b = tok < tokens ? __builtin_amdgcn_readfirstlane(sequence_of(a.kv.q_off, a.kv.B, t)) : a.kv.B;
+    Place p = {-1, 0, false};
+    if (b < a.kv.B) {
+      const int first = a.kv.q_off[b], end = a.kv.q_off[b + 1];
+      p.live = t >= first && t < end;
+      // (64 bits: the three numbers are the caller's)
+      const int64_t pos = int64_t(a.kv.kv_len[b]) - end + t;
+      if (pos >= 0 && pos < (int64_t(a.kv.max_pages) << a.kv.page_shift)) {
+        p.page = a.kv.page_table[b * a.kv.table_stride + (pos >> a.kv.page_shift)];
+        if (p.page < 0 || p.page >= a.kv.num_pages) p.page = -1;
+      }
+      p.slot = int(pos & ((1 << a.kv.page_shift) - 1));
+      for (int j = TOKENS == 1 ? int(threadIdx.x) : lane; j < half; j += TOKENS == 1 ? kThreads : kWave) {
+        const double turns = double(pos) * a.freq[j] * 0.15915494309189533577;   // 1 / (2 pi)
+        float s, c;
+        sincospif(2.0f * float(turns - rint(turns)), &s, &c);
+        turn[tok][j] = f32x2{c * a.rot_scale, s * a.rot_scale};
+      }
+    }
+    if (lane == 0) places[tok] = p;
+  }
+  float weights[2][8];
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    if (k ? a.k_weight : a.q_weight) load8(k ? a.k_weight : a.q_weight, a.weight_fmt, sub * 8, weights[k]);
+  __syncthreads();
+  if (row0 >= rows) return;
+
+  // lanes whose columns all stay as they are take no part in the rotation
+  const bool turns = sub * 8 < a.R;
+  int partner[8];      // where each column's lies in LDS
+  if (turns) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int c = sub * 8 + j, o = c >= a.R ? c : c < half ? c + half : c - half;
+      partner[j] = (o & 7) * LPR + (o >> 3);
     }
   }
   float* mine = part + threadIdx.x / LPR * D;
 
-  for (int r = row0; r < rows; r += step) {
-    float v[8];
+#pragma unroll 1
+  for (int tok = 0; tok < tokens; ++tok) {
+    const Place place = places[tok];
+    // column sub * 8 + j becomes v * co + partner * si
+    float co[8], si[8];
+    if (turns && place.live) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = next[j];
-    if (r + step < rows) load8(a.qkv, a.fmt, base + int64_t(r + step) * D, next);
-    const bool key = r >= a.Hq, value = r >= a.Hq + a.kv.Hkv;
-    if (!value) {
-      const void* weight = key ? a.k_weight : a.q_weight;
-      if (weight) {
-        float w[8], ss = 0.0f;
-        load8(weight, a.weight_fmt, sub * 8, w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) ss = fmaf(v[j], v[j], ss);
-        ss = group_sum<LPR>(ss);
-        const float inv = 1.0f / sqrtf(ss * (1.0f / D) + a.eps);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = v[j] * inv * w[j];
-      }
-      if (a.interleaved) {
-#pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-          const float x = v[j], y = v[j + 1];
-          v[j] = x * co[j] + y * si[j];
-          v[j + 1] = y * co[j + 1] + x * si[j + 1];
-        }
-      } else if (a.R) {
-        // (a row's lanes are of one wave, whose LDS accesses stay in order)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) mine[j * LPR + sub] = v[j];
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int c = sub * 8 + j, o = c < half ? c + half : c - half;
-          if (c < a.R) v[j] = v[j] * co[j] + mine[(o & 7) * LPR + (o >> 3)] * si[j];
-        }
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
+      for (int j = 0; j < 8; ++j) {
+        const int c = sub * 8 + j;
+        const bool in = c < a.R, one = a.interleaved ? !(j & 1) : c < half;
+        const f32x2 w = turn[tok][!in ? 0 : a.interleaved ? c >> 1 : one ? c : c - half];
+        co[j] = in ? w[0] : 1.0f;
+        si[j] = in ? one ? -w[1] : w[1] : 0.0f;
       }
     }
-    if (!key) {
-      *reinterpret_cast<u32x4_any*>(a.q + int64_t(t) * a.q_stride + r * D + sub * 8) = pack8(v);
-      continue;
-    }
-    if (place < 0) continue;
-    const int h = r - a.Hq - (value ? a.kv.Hkv : 0);
-    const int64_t at = page * a.kv.page_stride + slot * a.kv.slot_stride + h * a.kv.head_stride + sub * 8;
-    uint8_t* to = value ? a.kv.v : a.kv.k;
-    if (!a.kv.f8) {
-      *reinterpret_cast<u32x4*>(to + at * 2) = pack8(v);
-      continue;
-    }
-    float m = 0.0f;
+    const int64_t t = t0 + tok;
+#pragma unroll 1
+    for (int r0 = row0; r0 < rows; r0 += AHEAD * step) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[j]));
-    m = group_max<LPR>(m);
-    const float s = fmaxf(m, kScaleFloor) / kE4m3Max;
-    u32x2 q;
+      for (int k = 0; k < AHEAD; ++k) now[k] = next[k];
+      if (r0 + AHEAD * step < rows)
+        fetch(tok, r0 + AHEAD * step, next);
+      else
+        fetch(tok + 1, row0, next);
+      if (!place.live) continue;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      int p = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i] / s, v[4 * i + 1] / s, 0, false);
-      q[i] = uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i + 2] / s, v[4 * i + 3] / s, p, true));
+      for (int k = 0; k < AHEAD; ++k) {
+        const int r = r0 + k * step;
+        if (r >= rows) break;
+        float v[8];
+        now[k].values(v);
+        const bool key = r >= a.Hq, value = r >= a.Hq + a.kv.Hkv;
+        if (!value) {
+          if (key ? a.k_weight : a.q_weight) {
+            float ss = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) ss = fmaf(v[j], v[j], ss);
+            ss = group_sum<LPR>(ss);
+            const float inv = rsqrtf(ss * (1.0f / D) + a.eps);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = v[j] * inv * (key ? weights[1][j] : weights[0][j]);
+          }
+          if (turns) {
+            if (a.interleaved) {
+#pragma unroll
+              for (int j = 0; j < 8; j += 2) {
+                const float x = v[j], y = v[j + 1];
+                v[j] = x * co[j] + y * si[j];
+                v[j + 1] = y * co[j + 1] + x * si[j + 1];
+              }
+            } else {
+              // (a row's lanes are of one wave, whose LDS accesses stay in order)
+#pragma unroll
+              for (int j = 0; j < 8; ++j) mine[j * LPR + sub] = v[j];
+              __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+              __builtin_amdgcn_wave_barrier();
+              __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+#pragma unroll
+              for (int j = 0; j < 8; ++j) v[j] = v[j] * co[j] + mine[partner[j]] * si[j];
+              __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+              __builtin_amdgcn_wave_barrier();
+            }
+          }
+        }
+        if (!key) {
+          *reinterpret_cast<u32x4_any*>(a.q + t * a.q_stride + r * D + sub * 8) = pack8(v);
+          continue;
+        }
+        if (place.page < 0) continue;
+        const int h = r - a.Hq - (value ? a.kv.Hkv : 0);
+        const int64_t at = place.page * a.kv.page_stride + place.slot * a.kv.slot_stride + h * a.kv.head_stride + sub * 8;
+        uint8_t* to = value ? a.kv.v : a.kv.k;
+        if (!a.kv.f8) {
+          *reinterpret_cast<u32x4*>(to + at * 2) = pack8(v);
+          continue;
+        }
+        float m = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[j]));
+        m = group_max<LPR>(m);
+        const float s = fmaxf(m, kScaleFloor) / kE4m3Max;
+        const float inv = 1.0f / s;
+        u32x2 q;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int p = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i] * inv, v[4 * i + 1] * inv, 0, false);
+          q[i] = uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i + 2] * inv, v[4 * i + 3] * inv, p, true));
+        }
+        *reinterpret_cast<u32x2*>(to + at) = q;
+        if (sub == 0)
+          (value ? a.kv.v_scale : a.kv.k_scale)[((int64_t(place.page) << a.kv.page_shift) + place.slot) * a.kv.Hkv + h] = s;
+      }
     }
-    *reinterpret_cast<u32x2*>(to + at) = q;
-    if (sub == 0) (value ? a.kv.v_scale : a.kv.k_scale)[place * a.kv.Hkv + h] = s;
   }
 }
 
-template <int D>
+template <int D, int FMT>
 hipError_t launch(const RopeArgs& a, hipStream_t st) {
-  constexpr int ROWS = kThreads / (D / 8);
-  const int parts = (a.Hq + 2 * a.kv.Hkv + ROWS - 1) / ROWS;
-  const dim3 grid(a.T, a.T < 1024 ? parts : 1);
-  rope_kernel<D><<<grid, kThreads, 0, st>>>(a);
+  constexpr int ROWS = kThreads / (D / 8), TOKENS = kThreads / kWave;
+  if (a.T >= 1024) {
+    rope_kernel<D, TOKENS, FMT><<<(a.T + TOKENS - 1) / TOKENS, kThreads, 0, st>>>(a);
+  } else {
+    const int parts = (a.Hq + 2 * a.kv.Hkv + ROWS - 1) / ROWS;
+    rope_kernel<D, 1, FMT><<<dim3(a.T, parts), kThreads, 0, st>>>(a);
+  }
   return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_rope_append(const RopeArgs& a, hipStream_t st) {
-  if (a.kv.D == 64) return launch<64>(a, st);
-  if (a.kv.D == 128) return launch<128>(a, st);
-  return launch<256>(a, st);
+  const bool f32 = a.fmt == MOE_W_F32;
+  if (a.kv.D == 64) return f32 ? launch<64, MOE_W_F32>(a, st) : launch<64, MOE_W_BF16>(a, st);
+  if (a.kv.D == 128) return f32 ? launch<128, MOE_W_F32>(a, st) : launch<128, MOE_W_BF16>(a, st);
+  return f32 ? launch<256, MOE_W_F32>(a, st) : launch<256, MOE_W_BF16>(a, st);
 }
 
 }  // namespace moe
