@@ -105,13 +105,37 @@ def test_one_token(D, cache, length):
     _check(Setup([(1, length)], 2, D, cache), 6)
 
 
+def _wide(T, Hq, D, height, page=16):
+    """Pages of a table so wide that tiles get `height` rows (they are at most
+    64, 128 or 256 tall below 2.5e9, below 5e9 and from 5e9 products of the
+    step on, which the host counts by the table's width)."""
+    return int({64: 0, 128: 3.5e9, 256: 6e9}[height] / (T * Hq * D * page)) + 40
+
+
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("cache", ["bf16", "f8"])
-@pytest.mark.parametrize("new", [2, 9, 17, 40, 70])
+@pytest.mark.parametrize("new,height", [(2, 64), (9, 64), (17, 64), (40, 64), (33, 128), (40, 256), (70, 256)])
 @pytest.mark.parametrize("before", [0, 1, 77])
-def test_chunks(D, cache, new, before):
-    """All four tile heights (32 to 256 rows), with and without a past."""
-    _check(Setup([(new, before + new)], 2, D, cache), 8, rows=24)
+def test_chunks(D, cache, new, height, before):
+    """All tile heights (16 to 256 rows), with and without a past."""
+    _check(Setup([(new, before + new)], 2, D, cache, max_pages=_wide(new, 8, D, height)), 8, rows=24)
+
+
+@pytest.mark.parametrize("D,cache", [(64, "bf16"), (128, "f8"), (256, "bf16"), (256, "f8")])
+@pytest.mark.parametrize("height", [64, 128, 256])
+def test_tall_tiles(D, cache, height):
+    """Several tiles per sequence, cut and whole, ragged, windows, 8-bit
+    outputs, pages that are not there, at every height."""
+    want = ("out", "x8") if D > 64 else ("out",)
+    rows = [(150, 700), (0, 3), (97, 97), (1, 400)]
+    T, Hq = 248, 12
+    s = Setup(rows, 2, D, cache, page=8, max_pages=_wide(T, Hq, D, height, 8))
+    _check(s, Hq, want=want, rows=5)
+    _check(s, Hq, want=want, rows=5, window=70)
+    s.table[0, 30:41] = -1
+    _check(s, Hq, want=want, rows=5)
+    # few rows that one sequence brings to a long text: every tile is cut
+    _check(Setup([(33, 3001)], 1, D, cache, page=32, max_pages=_wide(33, 8, D, height, 32)), 8, rows=3)
 
 
 @pytest.mark.parametrize("Hq,Hkv", [(1, 1), (5, 5), (6, 2), (7, 1), (33, 1), (48, 1), (100, 1), (200, 1)])
