@@ -152,6 +152,15 @@ def test_more_than_a_thousand_tokens():
     _check(Setup([(1100, 1500), (13, 13)], 2, 64, page=32), 9, 50, True)
 
 
+@pytest.mark.parametrize("D,Hq,interleaved,x_dtype,cache", [
+    (64, 1, False, torch.float32, "bf16"), (128, 5, True, torch.bfloat16, "f8"), (256, 14, False, torch.bfloat16, "bf16")])
+def test_four_tokens_per_workgroup(D, Hq, interleaved, x_dtype, cache):
+    """More than 8192 rows: sequences that end inside a workgroup's four, rows
+    of none, positions that are not there, rows in several rounds."""
+    rows = [(8001, 8050), (0, 7), (3, 2), (170, 200), (1, 1), (19, 40)]
+    _check(Setup(rows, 2, D, cache, page=32, first=2, behind=3), Hq, D // 2, interleaved, x_dtype=x_dtype)
+
+
 def test_positions_that_are_not_there():
     """Pages out of range, positions behind the table and before the start:
     keys and values dropped, queries written."""
