@@ -543,8 +543,9 @@ moe_status moe_rope_append(const moe_kv_cache* cache, const moe_kv_batch* batch,
  * need their element's alignment only.  The order of the sums depends on the
  * lengths of all sequences, T and the shapes: calls of one batch give
  * identical bits, a sequence in another batch may differ in its last ones.
- * Fastest where Hq / Hkv * T / B, the rows of a sequence, are near those of
- * every sequence.  ws: moe_paged_attention_workspace_size bytes (no less for
+ * The host chooses the kernel from T, B, the heads, the window and the table's
+ * width (it does not see the lengths): tables as wide as the texts are long
+ * are best, and B without many sequences of no new tokens.  ws: moe_paged_attention_workspace_size bytes (no less for
  * a larger T; at present the same for every B), 256-byte aligned, in use by
  * one call at a time; what it holds before a call does not matter. */
 moe_status moe_paged_attention_workspace_size(int32_t T, int32_t B, int32_t Hq, int32_t Hkv,

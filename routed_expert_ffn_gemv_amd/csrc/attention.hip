@@ -7,23 +7,28 @@
 // Rows and tiles.  The G = Hq / Hkv query heads that share a key head are
 // rows of one tile with it: row r of a tile is token r / G, head r % G, so
 // that keys and values are read once for all of them.  A tile has QT tokens
-// (QT * G <= 32 RW rows: 32 per wave, RW waves), and walks over the
-// positions in steps of KW * KS: KW groups of waves take KS each.
+// (QT * G <= RB RW rows: RB = 16 or 32 per wave, RW waves), and walks over the
+// positions in steps of KW * KS: KW groups of waves take KS each.  Up to 32
+// rows four waves take positions of their own, with no barrier between them;
+// taller tiles share what they load.
 //
-// Products.  Scores are formed as S^T = K Q^T (32 x 32 x 16 bf16 products:
-// positions are the instruction's rows, query rows its columns), so a lane
-// holds 16 positions of one query row: the row's maximum is 15 maxima and one
-// exchange with lane ^ 32, and the factors that rescale a row are the lane's
-// own.  The weights' order is already that of the second product's operand
-// (O^T = V^T P^T) if its position 8 h + j (h = lane / 32) is taken to be 8 (j
-// / 4) + 4 h + j % 4 of 16: the order of a sum's terms is free as long as
-// both operands agree, and the transposing LDS reads of V take four (16 bits)
-// or any eight (8 bits) positions at a time.
+// Products.  Scores are formed as S^T = K Q^T (32 x 32 x 16 bf16 products, or
+// 16 x 16 x 32: positions are the instruction's rows, query rows its columns),
+// so a lane holds 16 (8) of 32 positions of one query row: the row's maximum
+// is its own and one (two) exchanges between lanes, and the factors that
+// rescale a row are the lane's own.  The weights' order is already that of
+// the second product's operand (O^T = V^T P^T) if its position 8 h + j (h =
+// lane / RB, of g = 64 / RB) is taken to be 4 g (j / 4) + 4 h + j % 4: the order
+// of a sum's terms is free as long as both operands agree, and the transposing
+// LDS reads of V take four (16 bits) or any eight (8 bits) positions at a time.
 //
 // Weights are rounded to bf16 for the second product (V is bf16 itself), off
 // by 2^-8 of a weight at most, and the sum that divides them is that of the
 // rounded ones: what is left is at most 2^-8 of the weighted mean of |v -
-// out|, and much less over many positions, whose roundings go either way.  With an 8-bit cache codes become bf16
+// out|, and much less over many positions, whose roundings go either way.
+// For 8-bit outputs, whose scales are fp32, a weight is the sum of two bf16
+// numbers (half as much again to multiply), and for up to 32 rows, where HBM
+// is what counts, of three.  With an 8-bit cache codes become bf16
 // (exact), a position's key scale multiplies its scores and its value scale
 // its weights before their rounding; the sum is then that of the unrounded.
 //
@@ -38,6 +43,12 @@
 // prompt fill the GPU alike.  A workgroup finds its run from the lengths
 // alone.  Tiles that are cut leave their parts (fp32, unnormalised) in the
 // workspace and join_kernel adds them up in order.
+//
+// What bounds it (16 query and 2 key heads of 256): decode HBM (64 x 8192
+// positions: 205 us, 5.2 TB/s; 5.18 is a copy's rate), a prompt the products and
+// exponentials (16,384 tokens: 2110-2240 us, 1,000-1,040 TFLOP/s; an 8192^3
+// library product 1,176), one token at 4097 a chain of loads and two launches
+// (15.9 us).
 
 #include <hip/hip_runtime.h>
 
@@ -345,9 +356,9 @@ struct Shape {
   static constexpr int kLds = kData + kIds * 4 + kWaves * RB * 8;
   static constexpr int kPerCu = kMaxLds / (kLds + 256) >= 2 && kThreads <= 256 ? 2 : 1;
   static constexpr int kRowsAt = 64 / kChunks;              // positions of a 1 KiB load
+  static constexpr int kAhead = 4;                          // operand reads ahead of their products
   // In steps: what a cut costs each side (the tile's rows in fp32 out and in),
   // and the shortest run if tiles are cut.
-  static constexpr int kAhead = 4;                          // operand reads ahead of their products
   static constexpr int kCut = RW, kLeast = RW;
   static_assert(kLds + 256 <= kMaxLds && (RW == 1 || NS >= 2) && (KS == 32 || KS == 64), "shape");
   static_assert(RW == 1 || 2 * kLoads % RW == 0, "loads");

@@ -129,7 +129,7 @@ struct Place {
 // TOKENS: 1 (all waves look it up) or one per wave.
 template <int D, int TOKENS, int FMT>
 __global__ __launch_bounds__(kThreads) void rope_kernel(const RopeArgs a) {
-  constexpr int LPR = D / 8, ROWS = kThreads / LPR, AHEAD = 3;
+  constexpr int LPR = D / 8, ROWS = kThreads / LPR, AHEAD = TOKENS == 1 ? 1 : 3;
   __shared__ f32x2 turn[TOKENS][D / 2];
   __shared__ Place places[TOKENS];
   __shared__ float part[kThreads * 8];
@@ -140,7 +140,7 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(const RopeArgs a) {
   const int rows = a.Hq + 2 * a.kv.Hkv;
   const int half = a.R / 2;
 
-  // a thread's next three rows, as they are
+  // a thread's next rows, as they are (one workgroup per token: one, for more of them at once)
   Raw<FMT> now[AHEAD], next[AHEAD];
   auto fetch = [&](int tok, int r, Raw<FMT>* to) {
 #pragma unroll
@@ -294,7 +294,7 @@ hipError_t launch(const RopeArgs& a, hipStream_t st) {
   constexpr int ROWS = kThreads / (D / 8), TOKENS = kThreads / kWave;
   // Four tokens per workgroup from 8 workgroups per CU on: 32,768 tokens of 20
   // heads of 256 take 149 us (one each: 188), but 2196 of 15 heads of 64 take 9.0
-  // (7.0), as half of the CUs get two.
+  // (7.9), as half of the CUs get two.
   if (a.T >= 8192) {
     rope_kernel<D, TOKENS, FMT><<<(a.T + TOKENS - 1) / TOKENS, kThreads, 0, st>>>(a);
   } else {
