@@ -538,7 +538,7 @@ moe_status moe_rope_append(const moe_kv_cache* cache, const moe_kv_batch* batch,
  *     moe_add_rmsnorm writes x8: [T][Hq * D] and [T][Hq * D / 128], contiguous
  *     (may be NULL, both or neither; D 128 or 256, else MOE_ERR_UNSUPPORTED)
  * At least one of out and x8 is not NULL; rows of no sequence are left as
- * they were.  No output overlaps an input.  scale > 0 and finite, window >=
+ * they were.  No output overlaps an input.  2^-64 <= scale <= 2^64, window >=
  * 0, Hq a multiple of Hkv, Hq <= 1024, Hq / Hkv <= 256, T <= 2^22; pointers
  * need their element's alignment only.  The order of the sums depends on the
  * lengths of all sequences, T and the shapes: calls of one batch give

@@ -946,7 +946,7 @@ moe_status moe_paged_attention(const moe_kv_cache* cache, const moe_kv_batch* ba
   s = moe_paged_attention_workspace_size(T, a.kv.B, Hq, a.kv.Hkv, a.kv.D, &need);
   if (s != MOE_OK) return s;
   if (x8 && a.kv.D % 128) return MOE_ERR_UNSUPPORTED;
-  if (!(scale > 0.0f) || !isfinite(scale) || window < 0) return MOE_ERR_INVALID;
+  if (!(scale >= 0x1p-64f && scale <= 0x1p64f) || window < 0) return MOE_ERR_INVALID;
   if (T == 0) return MOE_OK;
   const int64_t width = int64_t(Hq) * a.kv.D;
   if (!q || (!out && !x8) || !x8 != !x8_scale || q_stride < width || (out && out_stride < width))
@@ -960,7 +960,7 @@ moe_status moe_paged_attention(const moe_kv_cache* cache, const moe_kv_batch* ba
   a.Hq = Hq;
   a.G = Hq / a.kv.Hkv;
   a.scale2 = scale * 1.44269504088896341f;   // log2(e)
-  a.window = window;
+  a.window = window < kMaxPositions ? window : 0;   // (no position is further back)
   a.out = out;
   a.out_stride = out ? out_stride : 0;
   a.x8 = x8;

@@ -83,7 +83,7 @@ def test_batch_refusals(kw, status):
     (dict(Hq=5), INVALID), (dict(Hq=1026), UNSUPPORTED), (dict(Hq=516), UNSUPPORTED), (dict(q=None), INVALID),
     (dict(q=FAKE + 1), INVALID), (dict(qs=511), INVALID), (dict(out=None, x8=None, sc=None), INVALID),
     (dict(x8=None), INVALID), (dict(sc=None), INVALID), (dict(out=FAKE + 1), INVALID), (dict(os=511), INVALID),
-    (dict(sc=FAKE + 2), INVALID), (dict(scale=0.0), INVALID), (dict(scale=-1.0), INVALID),
+    (dict(sc=FAKE + 2), INVALID), (dict(scale=0.0), INVALID), (dict(scale=1e-30), INVALID), (dict(scale=1e30), INVALID), (dict(scale=-1.0), INVALID),
     (dict(scale=float("nan")), INVALID), (dict(scale=float("inf")), INVALID), (dict(window=-1), INVALID),
     (dict(ws=None), INVALID), (dict(ws=FAKE + 64), INVALID), (dict(size=1000), WORKSPACE),
 ])

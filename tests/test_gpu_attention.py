@@ -218,6 +218,12 @@ def test_rows_that_see_nothing():
             if D == 256:
                 assert (x8[none] & 127 == 0).all() and (sc[none] == 2.0 ** -126).all()
             _check(s, 4, window=9)
+            for window in (2 ** 30 - 1, 2 ** 30, 2 ** 31 - 1):       # (and positions below zero)
+                _check(s, 4, window=window)
+    # rows before and behind the text's start in one wave
+    s = Setup([(40, 25), (16, 9)], 2, 64)
+    for window in (0, 3, 2 ** 31 - 1):
+        _check(s, 4, window=window)
 
 
 def test_positions_behind_the_table():
