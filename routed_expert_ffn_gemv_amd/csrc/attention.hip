@@ -45,10 +45,10 @@
 // workspace and join_kernel adds them up in order.
 //
 // What bounds it (16 query and 2 key heads of 256): decode HBM (64 x 8192
-// positions: 205 us, 5.2 TB/s; 5.18 is a copy's rate), a prompt the products and
+// positions: 200 us, 5.4 TB/s; 5.18 is a copy's rate), a prompt the products and
 // exponentials (16,384 tokens: 2110-2240 us, 1,000-1,040 TFLOP/s; an 8192^3
 // library product 1,176), one token at 4097 a chain of loads and two launches
-// (15.9 us).
+// (15.0 us).
 
 #include <hip/hip_runtime.h>
 
@@ -517,7 +517,7 @@ __global__ __launch_bounds__(S::kThreads, S::kPerCu * S::kThreads / 256) void at
     const int slot = me * 2 + (from == 0 ? 1 : 0);
     x += take, r += take;
 
-    // ---- the tile's queries: this wave's 32 rows, as the products' right operand
+    // ---- the tile's queries: this wave's rows, as the products' right operand
     const int lr = rw * RB + col;                       // this lane's row of the tile
     const int token = a.token_of(lr);
     const bool live = token < nt;
@@ -557,7 +557,7 @@ __global__ __launch_bounds__(S::kThreads, S::kPerCu * S::kThreads / 256) void at
     const uint8_t* const vbase = a.kv.v + int64_t(h) * a.kv.head_stride * ELEM;
     const uint32_t page_bytes = uint32_t(a.kv.page_stride) * ELEM, slot_bytes = uint32_t(a.kv.slot_stride) * ELEM;
     const int shift = a.kv.page_shift;
-    const bool one_page = (1 << shift) >= S::kRowsAt && slot_bytes <= 1u << 26;
+    const bool one_page = (1 << shift) >= (RW == 1 ? 16 : S::kRowsAt) && slot_bytes <= 1u << 26;
     const int span = max(1, int(min(int64_t(kIds - 1) << shift, int64_t(1) << 30)) / STEP);
     for (int s0 = 0; s0 < take; s0 += span) {
       const int count = min(span, take - s0);
@@ -620,8 +620,26 @@ __global__ __launch_bounds__(S::kThreads, S::kPerCu * S::kThreads / 256) void at
       auto load_own = [&](int i, bool value) {
         const int id = pages_of(i), l = lane_at();
         if (one_page && __ballot(id < 0) == 0) {
+          // 16 positions from one base (a page lookup for every load: one token
+          // 15.9 us instead of 15.0, four 29.2 instead of 27.8)
+          const int lrow = l / S::kChunks;
+          const int chunk = ((l % S::kChunks) ^ (value ? S::value_swizzle(lrow) : S::key_swizzle(lrow))) * 16;
+          const uint32_t from = uint32_t(lrow) * slot_bytes;
+          const uint32_t to = lds_address(slot_lds(i % NS, value));
 #pragma unroll
-          for (int j = 0; j < S::kLoads; ++j) load(i, j, value, true, id, l);
+          for (int g = 0; g < KS / 16; ++g) {
+            const int pos0 = (step0 + i) * STEP + kw * KS + g * 16;
+            const uint8_t* base = (value ? vbase : kbase) +
+                                  uint64_t(uint32_t(__builtin_amdgcn_readlane(id, g * 16))) * page_bytes +
+                                  uint64_t(uint32_t(pos0 & ((1 << shift) - 1))) * slot_bytes;
+#pragma unroll
+            for (int j = 0; j < 16 / S::kRowsAt; ++j) {
+              const int row0 = g * 16 + j * S::kRowsAt;
+              const int swz0 = value ? S::value_swizzle(row0) : S::key_swizzle(row0);
+              to_lds16(base, (chunk ^ (swz0 * 16)) + from, to + row0 * PITCH);
+              base += uint32_t(S::kRowsAt) * slot_bytes;
+            }
+          }
         } else {
 #pragma unroll 1
           for (int j = 0; j < S::kLoads; ++j) load(i, j, value, false, id, l);
