@@ -462,7 +462,7 @@ const char* moe_status_string(int32_t s) {
   }
 }
 
-int32_t moe_version(void) { return 102; }
+int32_t moe_version(void) { return 103; }
 
 moe_status moe_workspace_size(const moe_layer_desc* desc, int32_t T, size_t* bytes) {
   const moe_status s = check_desc(desc);
