@@ -274,12 +274,13 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(const RopeArgs a) {
         for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[j]));
         m = group_max<LPR>(m);
         const float s = fmaxf(m, kScaleFloor) / kE4m3Max;
-        const float inv = 1.0f / s;
+        // (the division itself, not a product with the scale's inverse: one rounding
+        // less before the code is chosen)
         u32x2 q;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const int p = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i] * inv, v[4 * i + 1] * inv, 0, false);
-          q[i] = uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i + 2] * inv, v[4 * i + 3] * inv, p, true));
+          const int p = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i] / s, v[4 * i + 1] / s, 0, false);
+          q[i] = uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i + 2] / s, v[4 * i + 3] / s, p, true));
         }
         *reinterpret_cast<u32x2*>(to + at) = q;
         if (sub == 0)
