@@ -507,11 +507,12 @@ moe_status moe_rope_frequencies(int32_t R, double theta, int32_t scaling, double
  *       cos(angle_j), s = rot_scale * sin(angle_j) the pair (a1, a2) becomes
  *       (a1 c - a2 s, a2 c + a1 s).  Pair j is columns j and j + R / 2, or 2 j
  *       and 2 j + 1 (interleaved != 0).  R = 0: no rotation (freq not read).
+ *       Columns from R on stay as they are, infinities and NaN included.
  * in fp32, rounded once.  Queries go to q (bf16, T rows of Hq * D, q_stride
  * from row to row; q equal to a bf16 qkv with its stride: in place), keys
  * and (as they are) values to their position's place in the cache; in
  * MOE_W_E4M3 with scale = max(amax, 448 * 2^-126) / 448 per row of D, code =
- * e4m3(value / scale).  Keys and values of positions that are not there are
+ * e4m3(value / scale); NaN columns are NaN codes and left out of amax.  Keys and values of positions that are not there are
  * dropped, their queries written.  Rows of no sequence are left as they were,
  * and so is all of the cache but the new positions.  No other output overlaps
  * an input; two tokens that share a place leave one of theirs.  Limits: T <=

@@ -180,13 +180,18 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(const RopeArgs a) {
   __syncthreads();
   if (row0 >= rows) return;
 
-  // lanes whose columns all stay as they are take no part in the rotation
-  const bool turns = sub * 8 < a.R;
+  // lanes whose columns all stay as they are take no part in the rotation; one
+  // that holds column R rotates those before it and keeps the others' values (a
+  // product with a cosine of 1 and a sine of 0 would make NaN of an infinity).
+  // Only where R is not a multiple of 8: looked at for every row, 32,768 tokens
+  // of 20 heads of 256 took 166 us in place of 147.
+  const bool turns = sub * 8 < a.R, mixed = a.R % 8 != 0;
+  const int turning = a.R - sub * 8;     // the lane's first so many columns
   int partner[8];      // where each column's lies in LDS
   if (turns) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int c = sub * 8 + j, o = c >= a.R ? c : c < half ? c + half : c - half;
+      const int c = sub * 8 + j, o = j >= turning ? c : c < half ? c + half : c - half;
       partner[j] = (o & 7) * LPR + (o >> 3);
     }
   }
@@ -201,10 +206,10 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(const RopeArgs a) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int c = sub * 8 + j;
-        const bool in = c < a.R, one = a.interleaved ? !(j & 1) : c < half;
-        const f32x2 w = turn[tok][!in ? 0 : a.interleaved ? c >> 1 : one ? c : c - half];
-        co[j] = in ? w[0] : 1.0f;
-        si[j] = in ? one ? -w[1] : w[1] : 0.0f;
+        const bool one = a.interleaved ? !(j & 1) : c < half;
+        const f32x2 w = turn[tok][j >= turning ? 0 : a.interleaved ? c >> 1 : one ? c : c - half];
+        co[j] = w[0];
+        si[j] = one ? -w[1] : w[1];
       }
     }
     const int64_t t = t0 + tok;
@@ -238,6 +243,7 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(const RopeArgs a) {
             if (a.interleaved) {
 #pragma unroll
               for (int j = 0; j < 8; j += 2) {
+                if (mixed && j >= turning) continue;
                 const float x = v[j], y = v[j + 1];
                 v[j] = x * co[j] + y * si[j];
                 v[j + 1] = y * co[j + 1] + x * si[j + 1];
@@ -251,6 +257,11 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(const RopeArgs a) {
               __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 #pragma unroll
               for (int j = 0; j < 8; ++j) v[j] = v[j] * co[j] + mine[partner[j]] * si[j];
+              if (mixed) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                  if (j >= turning) v[j] = mine[j * LPR + sub];
+              }
               __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
               __builtin_amdgcn_wave_barrier();
             }
