@@ -27,8 +27,9 @@
  *  - Arguments are validated on the host before any launch.  On any error
  *    nothing is launched, nothing is written and a non-zero moe_status is
  *    returned.  A device fault surfaces at the caller's next synchronisation.
- *    T = 0 is a valid no-op (MOE_OK).  NaN/Inf inputs give unspecified
- *    values (never out-of-bounds accesses).
+ *    T = 0 is a valid no-op (MOE_OK).  Where a call does not
+ *    state them, NaN/Inf inputs give unspecified values (never out-of-bounds
+ *    accesses).
  *  - Row-major layouts; "K" is the contiguous (input) dimension.
  */
 #ifndef MOE_H
@@ -528,7 +529,10 @@ moe_status moe_rope_append(const moe_kv_cache* cache, const moe_kv_batch* batch,
  * head h reads key and value head h / (Hq / Hkv).  The token at position p
  * sees the positions p - window + 1 .. p (window 0: 0 .. p) that are there:
  *   s_i = scale * q . k_i     out = sum_i exp(s_i - max s) v_i / sum_i exp(s_i - max s)
- * A token that sees none gets zeros.  What lies in places of no position
+ * A token that sees none gets zeros.  A query that is not finite makes NaN of
+ * its own head's columns of its row (in x8 NaN codes, which its scale leaves
+ * out) and of nothing else, and so do scores of +infinity, of NaN, or of
+ * -infinity alone.  What lies in places of no position
  * seen (later slots of the last page, other pages) has no effect, NaN and
  * infinities included, except within a sequence's own kv_len positions, where
  * a NaN or infinity may reach every row of its step's tokens.  Scores,

@@ -34,7 +34,10 @@
 //
 // The running maximum is only raised when a row's grows by more than 2^8:
 // weights are then at most 2^8, sums of 2^30 of them far from fp32's end, and
-// most steps leave the output's registers alone.
+// most steps leave the output's registers alone.  It is -infinity as long as a
+// row has seen no position (then the row is zeros), and at least kLowest behind
+// that: a row of NaN scores, or of -infinity alone, is NaN as its formula's 0 / 0
+// is, in whole tiles and in cut ones.
 //
 // Work.  All tiles' steps form one line (sequence, key head, pairs of the
 // first and the last query tile, the second and the last but one ..., whose
@@ -80,6 +83,7 @@ constexpr int kIds = 1024;                          // page numbers a workgroup 
 constexpr float kE4m3Max = 448.0f;
 constexpr float kScaleFloor = 448.0f * 0x1p-126f;   // keeps every scale a normal number
 constexpr float kRaise = 8.0f;                      // log2 of the largest weight
+constexpr float kLowest = -3.402823466e38f;         // maximum of a row that has seen no finite score
 constexpr int kMaxGrid = 2 * kCus;
 
 __device__ const u32x4 kZeros = {0u, 0u, 0u, 0u};   // what a position that is not there reads
@@ -705,6 +709,7 @@ __global__ __launch_bounds__(S::kThreads, S::kPerCu * S::kThreads / 256) void at
         }
         const bool any = pos0 <= sees_any && pos0 + KS > from_any;
         typename P::Acc sc[NB];
+        float least = kLowest;      // -infinity: this lane's row sees none of the positions
         if (any) {
           // chunk c of a row lies at c ^ key_swizzle(row): with the lane's part
           // of c in the address, the rest of it is an exclusive or (below 256
@@ -767,13 +772,16 @@ __global__ __launch_bounds__(S::kThreads, S::kPerCu * S::kThreads / 256) void at
               }
           }
           if (!all || pos0 + KS - 1 > sees_all || pos0 < from_all) {
+            uint32_t some = 0;
 #pragma unroll
             for (int n = 0; n < KS / 32; ++n) {
               // a bit for each of the 32 positions that this lane's row sees
               const int last = rpos - pos0 - n * 32, first = rfirst - pos0 - n * 32;
               uint32_t sees = last >= 31 ? ~0u : last < 0 ? 0u : (2u << last) - 1u;
               sees &= first <= 0 ? ~0u : first > 31 ? 0u : ~0u << first;
-              sees = (sees & there[n]) >> (4 * group);
+              sees &= there[n];
+              some |= sees;
+              sees >>= 4 * group;
 #pragma unroll
               for (int m = 0; m < 32 / RB; ++m)
 #pragma unroll
@@ -782,6 +790,7 @@ __global__ __launch_bounds__(S::kThreads, S::kPerCu * S::kThreads / 256) void at
                   sc[k][j] = sees & (1u << (m * RB + place(j))) ? sc[k][j] : -INFINITY;
                 }
             }
+            least = some ? kLowest : -INFINITY;
           }
         }
         if constexpr (RW == 1) {
@@ -798,9 +807,10 @@ __global__ __launch_bounds__(S::kThreads, S::kPerCu * S::kThreads / 256) void at
           for (int n = 0; n < NB; ++n)
 #pragma unroll
             for (int j = 0; j < EACH; ++j) top = fmaxf(top, sc[n][j]);
-          top = P::row_max(top) * a.scale2;
+          top = fmaxf(P::row_max(top) * a.scale2, least);     // (NaN is no maximum)
           if (__ballot(top > mref + kRaise)) {
-            const float m = fmaxf(mref, top);
+            // (a row by its own scores alone, whatever the rows beside it do)
+            const float m = top > mref + kRaise ? top : mref;
             const float f = m == -INFINITY ? 1.0f : exp2_fast(mref - m);
             sum *= f, lost *= f;
 #pragma unroll
@@ -925,7 +935,7 @@ __global__ __launch_bounds__(S::kThreads, S::kPerCu * S::kThreads / 256) void at
     }
     float* const part = a.parts + int64_t(slot) * S::kRows * (D + 2);
     if (whole)
-      f = sum > 0.0f ? f / sum : 0.0f;
+      f = m == -INFINITY ? 0.0f : f / sum;
     else if (kw == 0 && part_of_row == 0)
       *reinterpret_cast<f32x2*>(part + S::kRows * D + lr * 2) = f32x2{m, sum};
     float* const mine_out = reinterpret_cast<float*>(smem) + wave * RB * S::kOutPitch;
@@ -1052,7 +1062,7 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(const AttnArgs a, in
         float top = -INFINITY;
 #pragma unroll
         for (int p = 0; p < GROUPS; ++p) top = fmaxf(top, stat[p][0]);
-        l = 0.0f;
+        m = top, l = 0.0f;
         v = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         if (top > -INFINITY) {
 #pragma unroll
@@ -1067,7 +1077,7 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(const AttnArgs a, in
       }
     }
     if (live && (many || group == 0)) {
-      const float f = l > 0.0f ? 1.0f / l : 0.0f;
+      const float f = m == -INFINITY ? 0.0f : 1.0f / l;
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] *= f;
       const int tk = a.token_of(row);
