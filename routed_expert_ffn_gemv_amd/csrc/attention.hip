@@ -32,12 +32,12 @@
 // (exact), a position's key scale multiplies its scores and its value scale
 // its weights before their rounding; the sum is then that of the unrounded.
 //
-// The running maximum is only raised when a row's grows by more than 2^8:
-// weights are then at most 2^8, sums of 2^30 of them far from fp32's end, and
-// most steps leave the output's registers alone.  It is -infinity as long as a
-// row has seen no position (then the row is zeros), and at least kLowest behind
-// that: a row of NaN scores, or of -infinity alone, is NaN as its formula's 0 / 0
-// is, in whole tiles and in cut ones.
+// The running maximum is raised to 2^8 above a row's largest when that passes
+// it: most steps leave the output's registers alone, and weights are at most 1,
+// so that a weighted sum stays finite as far as the values' own sum does.  It is
+// -infinity as long as a row has seen no position (then the row is zeros), and
+// at least kLowest behind that: a row of NaN scores, or of -infinity alone, is
+// NaN as its formula's 0 / 0 is, in whole tiles and in cut ones.
 //
 // Work.  All tiles' steps form one line (sequence, key head, pairs of the
 // first and the last query tile, the second and the last but one ..., whose
@@ -82,7 +82,7 @@ constexpr int kMaxLds = 160 * 1024;
 constexpr int kIds = 1024;                          // page numbers a workgroup holds at a time
 constexpr float kE4m3Max = 448.0f;
 constexpr float kScaleFloor = 448.0f * 0x1p-126f;   // keeps every scale a normal number
-constexpr float kRaise = 8.0f;                      // log2 of the largest weight
+constexpr float kRaise = 8.0f;                      // log2 of the maximum's headroom
 constexpr float kLowest = -3.402823466e38f;         // maximum of a row that has seen no finite score
 constexpr int kMaxGrid = 2 * kCus;
 
@@ -808,9 +808,9 @@ __global__ __launch_bounds__(S::kThreads, S::kPerCu * S::kThreads / 256) void at
 #pragma unroll
             for (int j = 0; j < EACH; ++j) top = fmaxf(top, sc[n][j]);
           top = fmaxf(P::row_max(top) * a.scale2, least);     // (NaN is no maximum)
-          if (__ballot(top > mref + kRaise)) {
+          if (__ballot(top > mref)) {
             // (a row by its own scores alone, whatever the rows beside it do)
-            const float m = top > mref + kRaise ? top : mref;
+            const float m = top > mref ? top + kRaise : mref;
             const float f = m == -INFINITY ? 1.0f : exp2_fast(mref - m);
             sum *= f, lost *= f;
 #pragma unroll
