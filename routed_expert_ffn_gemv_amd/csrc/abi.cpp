@@ -305,6 +305,30 @@ PrefillEvents* prefill_events() {
 bool act_fmt(int32_t fmt) { return fmt == MOE_W_F32 || fmt == MOE_W_BF16; }
 bool act_aligned(const void* p, int32_t fmt) { return aligned(p, fmt == MOE_W_F32 ? 4 : 2); }
 
+// Whether T rows of a_width bytes, a_stride from row to row, share a byte with T
+// rows of b.  Rows of one stride may lie beside each other (columns of one
+// allocation); null shares nothing.
+bool rows_meet(const void* a, int64_t a_stride, int64_t a_width, const void* b, int64_t b_stride,
+               int64_t b_width, int64_t T) {
+  if (!a || !b) return false;
+  const int64_t x = int64_t(reinterpret_cast<uintptr_t>(a)), y = int64_t(reinterpret_cast<uintptr_t>(b));
+  if (x + (T - 1) * a_stride + a_width <= y || y + (T - 1) * b_stride + b_width <= x) return false;
+  if (a_stride == b_stride) {
+    // row j of b begins d bytes into row j + rows of a
+    int64_t rows = (y - x) / a_stride, d = (y - x) % a_stride;
+    if (d < 0) d += a_stride, --rows;
+    auto there = [&](int64_t n) { return n > -T && n < T; };
+    return (d < a_width && there(rows)) || (d + b_width > a_stride && there(rows + 1));
+  }
+  for (int64_t i = 0; i < T; ++i) {
+    // the first row of b that ends behind row i of a's start
+    const int64_t at = x + i * a_stride, n = at - y - b_width;
+    const int64_t j = n < 0 ? 0 : n / b_stride + 1;
+    if (j < T && y + j * b_stride < at + a_width) return true;
+  }
+  return false;
+}
+
 // Checks a cache and a step's sequences and fills in what the kernels take.
 moe_status check_kv(const moe_kv_cache* c, const moe_kv_batch* b, KvArgs* a) {
   if (!c || !b) return MOE_ERR_INVALID;
@@ -954,6 +978,12 @@ moe_status moe_paged_attention(const moe_kv_cache* cache, const moe_kv_batch* ba
   if (!aligned(q, 2) || !aligned(out, 2) || !aligned(x8_scale, 4)) return MOE_ERR_INVALID;
   if (!ws || !aligned(ws, kAlign)) return MOE_ERR_INVALID;
   if (ws_bytes < need) return MOE_ERR_WORKSPACE;
+  // (a cut tile's queries are read while other tiles' outputs are written)
+  const int64_t blocks = width / 128;
+  if (rows_meet(q, q_stride * 2, width * 2, out, out_stride * 2, width * 2, T) ||
+      rows_meet(q, q_stride * 2, width * 2, x8, width, width, T) ||
+      rows_meet(q, q_stride * 2, width * 2, x8_scale, blocks * 4, blocks * 4, T))
+    return MOE_ERR_INVALID;
   a.q = q;
   a.q_stride = q_stride;
   a.T = T;
