@@ -513,10 +513,12 @@ moe_status moe_rope_frequencies(int32_t R, double theta, int32_t scaling, double
  * from row to row; q equal to a bf16 qkv with its stride: in place), keys
  * and (as they are) values to their position's place in the cache; in
  * MOE_W_E4M3 with scale = max(amax, 448 * 2^-126) / 448 per row of D, code =
- * e4m3(value / scale); NaN columns are NaN codes and left out of amax.  Keys and values of positions that are not there are
- * dropped, their queries written.  Rows of no sequence are left as they were,
- * and so is all of the cache but the new positions.  No other output overlaps
- * an input; two tokens that share a place leave one of theirs.  Limits: T <=
+ * e4m3(value / scale); NaN columns are NaN codes and left out of amax.  Keys
+ * and values of positions that are not there are dropped, their queries
+ * written.  Rows of no sequence are left as they were, and so is all of the
+ * cache but the new positions.  No other output overlaps an input (queries
+ * that share memory with other parts of qkv's rows are refused).  Places of two
+ * of the step's tokens hold some of either's columns afterwards.  Limits: T <=
  * 2^22, Hq <= 1024.  Results do not depend on T or on the run. */
 moe_status moe_rope_append(const moe_kv_cache* cache, const moe_kv_batch* batch, const void* qkv,
                            int32_t qkv_fmt, int64_t stride, int32_t T, int32_t Hq,
@@ -543,8 +545,8 @@ moe_status moe_rope_append(const moe_kv_cache* cache, const moe_kv_batch* batch,
  *     moe_add_rmsnorm writes x8: [T][Hq * D] and [T][Hq * D / 128], contiguous
  *     (may be NULL, both or neither; D 128 or 256, else MOE_ERR_UNSUPPORTED)
  * At least one of out and x8 is not NULL; rows of no sequence are left as
- * they were.  No output overlaps an input.  2^-64 <= scale <= 2^64, window >=
- * 0, Hq a multiple of Hkv, Hq <= 1024, Hq / Hkv <= 256, T <= 2^22; pointers
+ * they were.  No output overlaps an input (one that shares memory with q's rows
+ * is refused).  2^-64 <= scale <= 2^64, window >= 0, Hq a multiple of Hkv, Hq <= 1024, Hq / Hkv <= 256, T <= 2^22; pointers
  * need their element's alignment only.  The order of the sums depends on the
  * lengths of all sequences, T and the shapes: calls of one batch give
  * identical bits, a sequence in another batch may differ in its last ones.

@@ -929,6 +929,11 @@ moe_status moe_rope_append(const moe_kv_cache* cache, const moe_kv_batch* batch,
     return MOE_ERR_INVALID;
   if (q == qkv && (qkv_fmt != MOE_W_BF16 || q_stride != stride)) return MOE_ERR_INVALID;
   if (!(eps >= 0.0f) || !isfinite(rot_scale)) return MOE_ERR_INVALID;
+  // (in place, a thread writes the columns that it has read; elsewhere other
+  // threads still read what lies there)
+  const int64_t elem = qkv_fmt == MOE_W_F32 ? 4 : 2;
+  if (q != qkv && rows_meet(q, q_stride * 2, int64_t(Hq) * D * 2, qkv, stride * elem, width * elem, T))
+    return MOE_ERR_INVALID;
   a.qkv = qkv;
   a.fmt = qkv_fmt;
   a.stride = stride;

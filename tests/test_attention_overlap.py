@@ -5,8 +5,9 @@ import pytest
 import torch
 
 import routed_expert_ffn_gemv_amd as moe
+from oracle import attention as ref
 from paged import Setup
-from test_attention import FAKE, INVALID, _attend
+from test_attention import FAKE, INVALID, _append, _attend
 
 W = 4 * 128 * 2     # bytes of a row of queries
 
@@ -58,3 +59,36 @@ def test_outputs_beside_the_queries(q_at, q_stride, at, stride, x8):
     assert torch.equal(q, want)
     with pytest.raises(moe.MoEError):
         moe.moe_paged_attention(cache, batch, q, T, Hq, 0.1, ws, out=q)
+
+
+ROW = 8 * 128           # elements of a row of queries, keys and values
+
+
+@pytest.mark.parametrize("kw", [
+    dict(q=FAKE + 2, qs=ROW), dict(q=FAKE + W, qs=ROW), dict(q=FAKE + 2 * ROW - 2, qs=ROW + 8), dict(q=FAKE + 2),
+    dict(q=FAKE - 2, qs=ROW), dict(q=FAKE + 4 * 2 * ROW, qs=ROW), dict(q=FAKE + 5 * 2 * ROW - 2), dict(q=FAKE - 4 * 2 * ROW, qs=ROW),
+    dict(fmt=moe.MOE_W_F32, q=FAKE + 4, qs=2 * ROW), dict(fmt=moe.MOE_W_F32, q=FAKE + 5 * 4 * ROW - 2), dict(T=1, q=FAKE + 2 * ROW - 2),
+])
+def test_queries_within_other_parts_of_the_rows(kw):
+    assert _append(**kw) == INVALID
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("x_dtype", [torch.bfloat16, torch.float32])
+def test_queries_beside_the_rows(x_dtype):
+    """Queries in the gap behind each row of one allocation, as elsewhere."""
+    T, Hq, Hkv, D, R = 7, 3, 2, 64, 32
+    s = Setup([(T, 20)], Hkv, D)
+    wide = (2 if x_dtype == torch.float32 else 1) * (Hq + 2 * Hkv) * D      # in bf16 columns
+    buf = torch.zeros((T, wide + Hq * D), dtype=torch.bfloat16, device="cuda")
+    x = buf.view(x_dtype)[:, :(Hq + 2 * Hkv) * D]
+    x.copy_(torch.randn(x.shape, generator=torch.Generator().manual_seed(1)))
+    freq = torch.as_tensor(ref.frequencies(R, 1e4)[0], device="cuda")
+    got = []
+    for q in (torch.zeros((T, Hq * D), dtype=torch.bfloat16, device="cuda"), buf[:, wide:]):
+        cache, batch, d = s.device()
+        moe.moe_rope_append(cache, batch, x, T, Hq, q, freq=freq)
+        torch.cuda.synchronize()
+        got.append((q.clone(), d["k"], d["v"]))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
