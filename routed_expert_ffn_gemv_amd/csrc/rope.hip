@@ -235,7 +235,21 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(const RopeArgs a) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) ss = fmaf(v[j], v[j], ss);
             ss = group_sum<LPR>(ss);
-            const float inv = rsqrtf(ss * (1.0f / D) + a.eps);
+            float mean = ss * (1.0f / D) + a.eps;
+            // A row whose squares leave fp32's range is multiplied by a power of two
+            // first: sums of them then end within 2^120, and begin at 2^-106.
+            const bool out = !(mean >= 0x1p-80f && mean <= 0x1.fffffep127f);
+            if (__builtin_expect(__ballot(out) != 0, 0)) {
+              const float k = !out ? 1.0f : ss > 1.0f ? 0x1p-72f : 0x1p96f;
+              ss = 0.0f;
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                v[j] *= k;
+                ss = fmaf(v[j], v[j], ss);
+              }
+              mean = group_sum<LPR>(ss) * (1.0f / D) + a.eps * k * k;
+            }
+            const float inv = rsqrtf(mean);
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] = v[j] * inv * (key ? weights[1][j] : weights[0][j]);
           }
