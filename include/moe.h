@@ -504,7 +504,7 @@ moe_status moe_rope_frequencies(int32_t R, double theta, int32_t scaling, double
  *   a = a / sqrt(mean(a^2) + eps) * weight   (q_weight, k_weight [D]; NULL: a
  *       as it is)
  *   the first R columns rotated by angle_j = position * freq[j] (freq: device
- *       array of R / 2 doubles, angles in 64 bits): with c = rot_scale *
+ *       array of R / 2 doubles, all in 64 bits): with c = rot_scale *
  *       cos(angle_j), s = rot_scale * sin(angle_j) the pair (a1, a2) becomes
  *       (a1 c - a2 s, a2 c + a1 s).  Pair j is columns j and j + R / 2, or 2 j
  *       and 2 j + 1 (interleaved != 0).  R = 0: no rotation (freq not read).
