@@ -428,8 +428,8 @@ moe_status moe_scaled_linear(const uint8_t* x8, const float* x_scale, int32_t T,
 /* ---- The attention half of a decoder layer, between moe_add_rmsnorm's x and
  * the next moe_layer ([MD] "問題": 48 layers, of which the pages describe the
  * experts; "予測してから検証する": a verify pass of 1 + up to 3 drafts; "長い
- * プロンプトを読む": prompts read in chunks.  They name no attention: the
- * formulas below are the usual ones):
+ * プロンプトを読む": prompts read in chunks.  Of attention they say that
+ * some layers have it, and give no formula: those below are the usual ones):
  *   x8 -> moe_scaled_linear -> qkv -> moe_rope_append -> q and the cache
  *      -> moe_paged_attention -> x8 -> moe_scaled_linear -> y
  *
@@ -483,6 +483,8 @@ typedef struct {
  *      (2 pi n)) / (2 ln theta), lo = max(floor(d(fast)), 0), hi =
  *      min(ceil(d(slow)), R - 1) and w_j = clamp((j - lo) / max(hi - lo,
  *      0.001), 0, 1): freq_j = f_j (1 - w_j) + f_j / factor w_j
+ * (LINEAR was published as position interpolation, Chen et al. 2023, BASE as
+ * its NTK-aware form, BANDS as YaRN, Peng et al. 2023.)
  * *rot_scale, which multiplies cosines and sines: 1, for BANDS 0.1 ln(factor)
  * + 1.  R even, 2 <= R <= 256, theta > 1, factor >= 1 (not read by PLAIN);
  * context >= 1 and fast > slow > 0 are read by BANDS only. */
@@ -534,27 +536,35 @@ moe_status moe_rope_append(const moe_kv_cache* cache, const moe_kv_batch* batch,
  * A token that sees none gets zeros.  A query that is not finite makes NaN of
  * its own head's columns of its row (in x8 NaN codes, which its scale leaves
  * out) and of nothing else, and so do scores of +infinity, of NaN, or of
- * -infinity alone.  What lies in places of no position
- * seen (later slots of the last page, other pages) has no effect, NaN and
- * infinities included, except within a sequence's own kv_len positions, where
- * a NaN or infinity may reach every row of its step's tokens.  Scores,
- * maxima, sums and the weighted sums are fp32; the weights are rounded to
- * bf16 before they multiply the values.
+ * -infinity alone.  What lies in places of no position seen (later slots of the
+ * last page, other pages) has no effect, NaN and infinities included, except
+ * within a sequence's own kv_len positions, where a NaN or infinity may reach
+ * every row of its step's tokens.
+ *   Scores, maxima, sums and the weighted sums are fp32; weights (at most 1) are
+ * multiplied with the values as bf16 numbers: as the sum of three, which leaves
+ * 2^-24 of a weight at most, where the batch has up to 32 rows per sequence on
+ * average (new tokens times Hq / Hkv); beyond, as the sum of two (2^-16) where
+ * x8 is asked for, and as one (2^-8) for out alone.  Asking for x8 as well may
+ * therefore change out in its last bits.
  *   out: bf16, T rows of Hq * D (may be NULL)
  *   x8, x8_scale: the unrounded out in 8 bits for moe_scaled_linear, as
  *     moe_add_rmsnorm writes x8: [T][Hq * D] and [T][Hq * D / 128], contiguous
  *     (may be NULL, both or neither; D 128 or 256, else MOE_ERR_UNSUPPORTED)
  * At least one of out and x8 is not NULL; rows of no sequence are left as
  * they were.  No output overlaps an input (one that shares memory with q's rows
- * is refused).  2^-64 <= scale <= 2^64, window >= 0, Hq a multiple of Hkv, Hq <= 1024, Hq / Hkv <= 256, T <= 2^22; pointers
- * need their element's alignment only.  The order of the sums depends on the
- * lengths of all sequences, T and the shapes: calls of one batch give
- * identical bits, a sequence in another batch may differ in its last ones.
- * The host chooses the kernel from T, B, the heads, the window and the table's
- * width (it does not see the lengths): tables as wide as the texts are long
- * are best, and B without many sequences of no new tokens.  ws: moe_paged_attention_workspace_size bytes (no less for
- * a larger T; at present the same for every B), 256-byte aligned, in use by
- * one call at a time; what it holds before a call does not matter. */
+ * is refused).  2^-64 <= scale <= 2^64, window >= 0, Hq a multiple of Hkv, Hq <=
+ * 1024, Hq / Hkv <= 256, T <= 2^22, lengths up to 2^30; pointers need their
+ * element's alignment only.  The order of the sums depends on the lengths of all
+ * sequences, T, the shapes, the window, the table's width and on whether x8 is
+ * asked for: calls of one batch give identical bits, a sequence in another batch
+ * may differ in its last ones.  The host chooses the kernel from T, B, the
+ * heads, the window and the table's width (it does not see the lengths): tables
+ * as wide as the texts are long are best (a table 256 times as wide makes 512
+ * tokens from the start, 16 heads of 256, take 75 us in place of 35), and B
+ * without many sequences of no new tokens.  ws:
+ * moe_paged_attention_workspace_size bytes (no less for a larger T; at present
+ * the same for every B), 256-byte aligned, in use by one call at a time; what
+ * it holds before a call does not matter. */
 moe_status moe_paged_attention_workspace_size(int32_t T, int32_t B, int32_t Hq, int32_t Hkv,
                                               int32_t D, size_t* bytes);
 moe_status moe_paged_attention(const moe_kv_cache* cache, const moe_kv_batch* batch,

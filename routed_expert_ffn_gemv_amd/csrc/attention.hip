@@ -27,10 +27,11 @@
 // rounded ones: what is left is at most 2^-8 of the weighted mean of |v -
 // out|, and much less over many positions, whose roundings go either way.
 // For 8-bit outputs, whose scales are fp32, a weight is the sum of two bf16
-// numbers (half as much again to multiply), and for up to 32 rows, where HBM
-// is what counts, of three.  With an 8-bit cache codes become bf16
-// (exact), a position's key scale multiplies its scores and its value scale
-// its weights before their rounding; the sum is then that of the unrounded.
+// numbers (half as much again to multiply: a prompt of 16,384 tokens, 32 / 4 heads
+// of 128, takes 2890 us in place of 2140), and for up to 32 rows, where HBM is what
+// counts, of three.  With an 8-bit cache codes become bf16 (exact), a position's
+// key scale multiplies its scores and its value scale its weights before their
+// rounding.  In both cases the sum is that of the unrounded weights.
 //
 // The running maximum is raised to 2^8 above a row's largest when that passes
 // it: most steps leave the output's registers alone, and weights are at most 1,
@@ -48,10 +49,12 @@
 // workspace and join_kernel adds them up in order.
 //
 // What bounds it (16 query and 2 key heads of 256): decode HBM (64 x 8192
-// positions: 200 us, 5.4 TB/s; 5.18 is a copy's rate), a prompt the products and
-// exponentials (16,384 tokens: 2110-2240 us, 1,000-1,040 TFLOP/s; an 8192^3
+// positions: 197 us, 5.4 TB/s; 5.18 is a copy's rate), a prompt the products and
+// exponentials (16,384 tokens: 2050-2230 us, 990-1,070 TFLOP/s; an 8192^3
 // library product 1,176), one token at 4097 a chain of loads and two launches
-// (15.0 us).
+// (15.0 us).  Heads of 64 have as many exponentials, masks and roundings per
+// score for a quarter of the products: vector instructions are issued in 54 % of
+// a prompt's cycles, matrix instructions busy in 30 % (256: 43 and 48).
 
 #include <hip/hip_runtime.h>
 
@@ -1132,10 +1135,12 @@ hipError_t launch(const AttnArgs& a, hipStream_t st) {
   // Tall tiles multiply at twice the rate of those of 64 rows, but cutting them
   // moves rows * D * 4 bytes per workgroup out and in again: only for steps of
   // many products (as far as the host can tell: the tables may be wider than
-  // the texts are long).  512 tokens from the start, 16 heads of 256: 35 us with
-  // 64 rows, 75 with 256; 64 tokens at 8000: 47, 66; 525 tokens at 7001, 15 heads
-  // of 64: 61, 128 rows 53, 256 60; 2428 tokens, windows of 1024, 20 heads of 128:
-  // 78, 59, 57.
+  // the texts are long).  In us with 64, 128 and 256 rows at the products in
+  // brackets: 16 / 2 heads of 256, 512 tokens at 512 (1.1e9) 35, 61, 75, at 1024
+  // (2.1e9) 43, 55, 59, at 2048 (4.3e9) 60, 65, 65, at 4096 (8.6e9) 92, 80, 81, 64 at
+  // 32,000 (8.4e9) 100, 88, 82; 32 / 4 of 128, 512 at 1024 (2.1e9) 34, 34, 43, at 2048
+  // (4.3e9) 43, 42, 42, 64 at 32,000 (8.4e9) 88, 64, 61; 15 / 5 of 64, 512 at 4096 (2e9)
+  // 32, 32, 34.
   const int64_t cap = int64_t(a.kv.max_pages) << a.kv.page_shift;
   const int64_t seen = a.window && a.window < cap ? a.window : cap;
   const double work = double(a.T) * a.Hq * double(seen) * D;

@@ -10,7 +10,7 @@
 // Angles: position * freq in 64 bits, less its whole turns, so that a far
 // position loses nothing; cosine, sine and their product with rot_scale in 64
 // bits too, rounded once (with fp32 sines of the rest of a turn, off by up to 2^-23
-// radians, the same times: 148 us for the prompt below, 4.2 for one token).
+// radians, the same times: 149 us for the prompt below, 4.2 for one token).
 //
 // A lane holds 8 columns, D / 8 lanes a row, 256 threads 8 to 32 rows at a
 // time, and a thread has its next three rows under way.  For many tokens a
@@ -320,9 +320,10 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(const RopeArgs a) {
 template <int D, int FMT>
 hipError_t launch(const RopeArgs& a, hipStream_t st) {
   constexpr int ROWS = kThreads / (D / 8), TOKENS = kThreads / kWave;
-  // Four tokens per workgroup from 8 workgroups per CU on: 32,768 tokens of 20
-  // heads of 256 take 149 us (one each: 188), but 2196 of 15 heads of 64 take 9.0
-  // (7.9), as half of the CUs get two.
+  // Four tokens per workgroup from 8 workgroups per CU on: of 20 heads of 256,
+  // 32,768 tokens take 149 us (one each: 188), 16,384 79 (89), 8192 36 (36), 4096 20
+  // (21), 2048 16 (13), as half of the CUs get two; of 15 heads of 64 in fp32, 32,768
+  // 68 (65), 8192 21 (20), 2196 8.9 (8.0).
   if (a.T >= 8192) {
     rope_kernel<D, TOKENS, FMT><<<(a.T + TOKENS - 1) / TOKENS, kThreads, 0, st>>>(a);
   } else {
