@@ -540,7 +540,8 @@ moe_status moe_rope_append(const moe_kv_cache* cache, const moe_kv_batch* batch,
  * last page, other pages) has no effect, NaN and infinities included, except
  * within a sequence's own kv_len positions, where a NaN or infinity may reach
  * every row of its step's tokens.
- *   Scores, maxima, sums and the weighted sums are fp32; weights (at most 1) are
+ *   Scores, maxima, sums and the weighted sums are fp32; weights are at most 1
+ * (8-bit cache: 2^8, which sums of values near 2^118 overflow with), and are
  * multiplied with the values as bf16 numbers: as the sum of three, which leaves
  * 2^-24 of a weight at most, where the batch has up to 32 rows per sequence on
  * average (new tokens times Hq / Hkv); beyond, as the sum of two (2^-16) where

@@ -33,9 +33,12 @@
 // key scale multiplies its scores and its value scale its weights before their
 // rounding.  In both cases the sum is that of the unrounded weights.
 //
-// The running maximum is raised to 2^8 above a row's largest when that passes
-// it: most steps leave the output's registers alone, and weights are at most 1,
-// so that a weighted sum stays finite as far as the values' own sum does.  It is
+// The running maximum is raised when a row's largest score passes it by 2^8 (bf16:
+// to 2^8 above that score, when it passes it at all): most steps leave the
+// output's registers alone.  With a bf16 cache no weight passes 1, so that a
+// weighted sum stays finite as far as the values' own sum does; with an 8-bit one
+// weights are up to 2^8, as their products with small value scales would
+// otherwise be subnormal bf16 numbers (scales of 2^-122: off by 11 %).  It is
 // -infinity as long as a row has seen no position (then the row is zeros), and
 // at least kLowest behind that: a row of NaN scores, or of -infinity alone, is
 // NaN as its formula's 0 / 0 is, in whole tiles and in cut ones.
@@ -85,7 +88,7 @@ constexpr int kMaxLds = 160 * 1024;
 constexpr int kIds = 1024;                          // page numbers a workgroup holds at a time
 constexpr float kE4m3Max = 448.0f;
 constexpr float kScaleFloor = 448.0f * 0x1p-126f;   // keeps every scale a normal number
-constexpr float kRaise = 8.0f;                      // log2 of the maximum's headroom
+constexpr float kRaise = 8.0f;                      // log2 of how far a row's maximum is let grow
 constexpr float kLowest = -3.402823466e38f;         // maximum of a row that has seen no finite score
 constexpr int kMaxGrid = 2 * kCus;
 
@@ -811,9 +814,10 @@ __global__ __launch_bounds__(S::kThreads, S::kPerCu * S::kThreads / 256) void at
 #pragma unroll
             for (int j = 0; j < EACH; ++j) top = fmaxf(top, sc[n][j]);
           top = fmaxf(P::row_max(top) * a.scale2, least);     // (NaN is no maximum)
-          if (__ballot(top > mref)) {
+          constexpr float ABOVE = F8 ? 0.0f : kRaise;
+          if (__ballot(top > mref + (kRaise - ABOVE))) {
             // (a row by its own scores alone, whatever the rows beside it do)
-            const float m = top > mref ? top + kRaise : mref;
+            const float m = top > mref + (kRaise - ABOVE) ? top + ABOVE : mref;
             const float f = m == -INFINITY ? 1.0f : exp2_fast(mref - m);
             sum *= f, lost *= f;
 #pragma unroll
